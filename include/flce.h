@@ -359,6 +359,84 @@ flce_status_t flce_policy_loss_grad(const float* logprob, const float* old_logpr
                                     double eps_high, double denominator, const double* reduced,
                                     float* grad_logprob, struct ihipStream_t* stream);
 
+/*
+ * Element types and microscaled formats of the calls below.  A microscaled matrix keeps
+ * blocks of 32 consecutive elements of a row with one power-of-two scale: the smallest 2^e
+ * (-127 <= e <= 127) at which no element of the block exceeds the element format's largest
+ * value (at e = 127 elements are clamped to it); elements are rounded to nearest, ties to
+ * even.  Element formats: MXFP4 e2m1 (largest 6; two codes a byte, the even element in the
+ * low half), MXFP8 e4m3 (largest 448), MXINT8 an integer in [-127, 127] over 64.  A block
+ * that holds an infinity or a NaN stands for NaNs throughout.  Layout, row-major: codes,
+ * each row padded with zeros to a whole block, and scale bytes (e + 127; 255 for NaN), each
+ * row padded with zeros to a multiple of 16 bytes; flce_mx_sizes gives the bytes of a row.
+ * The products below rely on the padding: a matrix quantised elsewhere must have it too.
+ */
+typedef enum { FLCE_BF16 = 0, FLCE_FP32 = 1 } flce_dtype_t;
+typedef enum {
+  FLCE_MX_NONE = -1,
+  FLCE_MXFP4 = 0,
+  FLCE_MXFP8 = 1,
+  FLCE_MXINT8 = 2
+} flce_mx_format_t;
+
+/* Bytes of a row of codes and of a row of scales for `cols` elements (either output may be
+ * NULL).  1 <= cols <= 2^20. */
+flce_status_t flce_mx_sizes(int64_t cols, int format, int64_t* code_bytes, int64_t* scale_bytes);
+
+/*
+ * Quantise x [rows, cols] (bf16 or fp32, ldx elements between rows) to codes and scales, or
+ * write the values they stand for to out (rounded to nearest; every value of the three
+ * formats is exact in bf16 and fp32 unless its scale is near the end of the type's range).
+ * 0 <= rows <= 2^30; codes and scales 16-byte aligned; x and out naturally aligned, with
+ * any row stride >= cols.
+ */
+flce_status_t flce_mx_quantize(const void* x, int x_dtype, int64_t ldx, int64_t rows, int64_t cols,
+                               int format, void* codes, void* scales,
+                               struct ihipStream_t* stream);
+flce_status_t flce_mx_dequantize(const void* codes, const void* scales, int format, int64_t rows,
+                                 int64_t cols, void* out, int out_dtype, int64_t ldo,
+                                 struct ihipStream_t* stream);
+
+/*
+ * Layer norm over the rows of x [M, H], in 32 bits:
+ *   mean = sum x / H,  rstd = 1 / sqrt(sum (x - mean)^2 / H + eps)
+ *   y = weight (x - mean) rstd + bias          (NULL weight: 1, NULL bias: 0)
+ * x and y are (bf16, bf16), (fp32, bf16) or (fp32, fp32); weight and bias bf16 or fp32;
+ * mean and rstd fp32 [M].  With a checkpoint format (FLCE_MXFP8 or FLCE_MXINT8; otherwise
+ * FLCE_MX_NONE) the call also writes x in that format to codes and scales, for a backward
+ * that keeps a quarter to a half of x's bytes; y, mean and rstd are those of x itself.
+ * 0 <= M <= 2^30 (0: nothing is touched), 1 <= H <= 2^20; any row strides >= H (rows of
+ * multiples of 8 elements at 16-byte aligned addresses move fastest).  y may be x where
+ * their types and strides agree.
+ */
+flce_status_t flce_layer_norm_forward(const void* x, int x_dtype, int64_t ldx, const void* weight,
+                                      const void* bias, int param_dtype, int64_t M, int64_t H,
+                                      float eps, void* y, int y_dtype, int64_t ldy, float* mean,
+                                      float* rstd, int format, void* codes, void* scales,
+                                      struct ihipStream_t* stream);
+
+/* Workspace bytes of flce_layer_norm_backward (the partial sums of dweight and dbias). */
+flce_status_t flce_layer_norm_backward_workspace(int64_t M, int64_t H, size_t* bytes);
+
+/*
+ * Backward of the layer norm, with xh = (x - mean) rstd from the forward's mean and rstd:
+ *   g = weight dy,  dx = rstd (g - mean_j g - xh mean_j(g xh))
+ *   dweight = sum_m dy xh,  dbias = sum_m dy       (param_dtype; either may be NULL)
+ * x is given either itself (format FLCE_MX_NONE; dx has its type) or, with x NULL, as the
+ * forward's checkpoint (format, codes, scales; dx bf16 or fp32).  dy is bf16 or fp32 (fp32
+ * only with fp32 dx).  M = 0 writes zeros to dweight and dbias.  The sums over rows are
+ * formed in a fixed order without atomics: results are bitwise repeatable.  workspace:
+ * 256-byte aligned, at least flce_layer_norm_backward_workspace bytes.  dx may be dy or x
+ * where their types and strides agree.
+ */
+flce_status_t flce_layer_norm_backward(const void* dy, int dy_dtype, int64_t lddy, const void* x,
+                                       int x_dtype, int64_t ldx, int format, const void* codes,
+                                       const void* scales, const void* weight, int param_dtype,
+                                       const float* mean, const float* rstd, int64_t M, int64_t H,
+                                       void* dx, int dx_dtype, int64_t lddx, void* dweight,
+                                       void* dbias, void* workspace, size_t workspace_bytes,
+                                       struct ihipStream_t* stream);
+
 /* Static description of a status code. */
 const char* flce_status_string(flce_status_t status);
 

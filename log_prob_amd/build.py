@@ -9,11 +9,13 @@ import shutil
 import subprocess
 import sys
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = ["flce_kernels.hip", "flce_api.cpp"]
+SOURCES = ["flce_kernels.hip", "norm_kernels.hip", "mx_quant_kernels.hip", "flce_api.cpp",
+           "ops_api.cpp"]
 LIB = os.path.join(HERE, "libflce.so")
 ARCH = "gfx950"
 
@@ -39,15 +41,18 @@ def hipcc() -> str:
 def build(verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
     cc = hipcc()
     with tempfile.TemporaryDirectory() as tmp:
-        objs = []
-        for src in SOURCES:
+        def compile_one(src):
             obj = os.path.join(tmp, src + ".o")
             cmd = [cc, *HIPCC_FLAGS, *extra_flags, "-I", os.path.join(ROOT, "include"),
                    "-c", os.path.join(CSRC, src), "-o", obj]
             if verbose:
                 print(" ".join(cmd), flush=True)
             subprocess.run(cmd, check=True)
-            objs.append(obj)
+            return obj
+
+        # one compiler process a source, side by side
+        with ThreadPoolExecutor(max_workers=min(len(SOURCES), 4)) as pool:
+            objs = list(pool.map(compile_one, SOURCES))
         out_tmp = out + ".tmp"
         cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", out_tmp]
         if verbose:

@@ -11,11 +11,14 @@
 #include <cstring>
 
 #include "flce.h"
+#include "api_util.h"
 #include "flce_internal.h"
 
 namespace {
-
 thread_local char g_last_error[512] = "";
+}
+
+namespace flce {
 
 flce_status_t fail(flce_status_t st, const char* fmt, ...) {
   va_list ap;
@@ -29,6 +32,13 @@ flce_status_t ok() {
   g_last_error[0] = '\0';
   return FLCE_OK;
 }
+
+}  // namespace flce
+
+namespace {
+
+using flce::fail;
+using flce::ok;
 
 constexpr int64_t kTile = flce::kTile;
 constexpr int64_t kMaxM = int64_t(1) << 30;

@@ -1,0 +1,129 @@
+// Quantisation to microscaled formats and back (gfx950): one pass, bound by memory.
+//
+//   quantise    codes = round(x / 2^e) with 2^e the block's scale; scale byte e + 127
+//   dequantise  x = code 2^e
+//
+// A thread takes 8 consecutive elements at a time (a 16-byte load of bf16), so the block's
+// scale is found by the four lanes of a quad and nothing goes through LDS.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx_device.h"
+#include "ops_internal.h"
+
+namespace flce {
+
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int BATCH = 4;  // chunks a thread has in flight
+
+// Rows of TPR threads, THREADS / TPR rows a workgroup; thread t of a row takes chunks t,
+// t + TPR, ... of it.  A row's codes end with a whole block, so quads stay whole.
+template <class T, int FMT, bool VEC>
+__global__ __launch_bounds__(THREADS) void mx_quantize_kernel(MxQuantArgs p, int tpr) {
+  const int t = threadIdx.x & (tpr - 1), rows = THREADS / tpr;
+  const long blocks = mx_blocks(p.cols), chunks = 4 * blocks;
+  const long code_ld = mx_code_bytes(p.cols, FMT), scale_ld = mx_scale_bytes(p.cols);
+  for (long row = (long)blockIdx.x * rows + threadIdx.x / tpr; row < p.rows; row += (long)gridDim.x * rows) {
+    const typename T::mem* x = static_cast<const typename T::mem*>(p.x) + row * p.ldx;
+    uint8_t* codes = p.codes + row * code_ld;
+    uint8_t* scales = p.scales + row * scale_ld;
+    for (long c0 = t; c0 < chunks; c0 += (long)BATCH * tpr) {
+      float v[BATCH][8];
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) load8<T, VEC>(x, 8 * (c0 + (long)b * tpr), p.cols, v[b]);
+#pragma unroll
+      for (int b = 0; b < BATCH; ++b) {
+        const long c = c0 + (long)b * tpr;
+        const uint32_t byte = mx_scale_byte<FMT>(v[b]);
+        const u32x2_t q = mx_encode<FMT>(v[b], byte);
+        if (c < chunks) {
+          if constexpr (FMT == kMxFp4)
+            *reinterpret_cast<uint32_t*>(codes + 4 * c) = q.x;
+          else
+            *reinterpret_cast<u32x2_t*>(codes + 8 * c) = q;
+          if ((c & 3) == 0) scales[c >> 2] = (uint8_t)byte;
+        }
+      }
+    }
+    for (long i = blocks + t; i < scale_ld; i += tpr) scales[i] = 0;
+  }
+}
+
+template <class T, int FMT, bool VEC>
+__global__ __launch_bounds__(THREADS) void mx_dequantize_kernel(MxQuantArgs p, int tpr) {
+  const int t = threadIdx.x & (tpr - 1), rows = THREADS / tpr;
+  const long chunks = 4 * mx_blocks(p.cols);
+  const long code_ld = mx_code_bytes(p.cols, FMT), scale_ld = mx_scale_bytes(p.cols);
+  for (long row = (long)blockIdx.x * rows + threadIdx.x / tpr; row < p.rows; row += (long)gridDim.x * rows) {
+    typename T::mem* out = static_cast<typename T::mem*>(p.out) + row * p.ldo;
+    const uint8_t* codes = p.codes + row * code_ld;
+    const uint8_t* scales = p.scales + row * scale_ld;
+#pragma unroll 4
+    for (long c = t; c < chunks; c += tpr) {
+      u32x2_t q = {0u, 0u};
+      if constexpr (FMT == kMxFp4)
+        q.x = *reinterpret_cast<const uint32_t*>(codes + 4 * c);
+      else
+        q = *reinterpret_cast<const u32x2_t*>(codes + 8 * c);
+      float v[8];
+      mx_decode<FMT>(q, scales[c >> 2], v);
+      store8<T, VEC>(out, 8 * c, p.cols, v);
+    }
+  }
+}
+
+// Threads a row: the smallest power of two (at least a quad) that covers the row's chunks.
+int threads_per_row(long cols) {
+  const long chunks = 4 * mx_blocks(cols);
+  int t = 4;
+  while (t < THREADS && t < chunks) t *= 2;
+  return t;
+}
+
+constexpr long kMostGroups = 1l << 20;
+unsigned grid_of(const MxQuantArgs& a, int tpr) {
+  const long rows = THREADS / tpr, need = (a.rows + rows - 1) / rows;
+  return (unsigned)(need < kMostGroups ? need : kMostGroups);
+}
+
+template <class T, int FMT, bool VEC>
+void quantize(const MxQuantArgs& a, hipStream_t s) {
+  const int tpr = threads_per_row(a.cols);
+  mx_quantize_kernel<T, FMT, VEC><<<grid_of(a, tpr), THREADS, 0, s>>>(a, tpr);
+}
+template <class T, int FMT, bool VEC>
+void dequantize(const MxQuantArgs& a, hipStream_t s) {
+  const int tpr = threads_per_row(a.cols);
+  mx_dequantize_kernel<T, FMT, VEC><<<grid_of(a, tpr), THREADS, 0, s>>>(a, tpr);
+}
+
+template <int FMT>
+void quantize_any(const MxQuantArgs& a, int dtype, bool vec, hipStream_t s) {
+  if (dtype == kBf16) vec ? quantize<Bf16, FMT, true>(a, s) : quantize<Bf16, FMT, false>(a, s);
+  else vec ? quantize<F32, FMT, true>(a, s) : quantize<F32, FMT, false>(a, s);
+}
+template <int FMT>
+void dequantize_any(const MxQuantArgs& a, int dtype, bool vec, hipStream_t s) {
+  if (dtype == kBf16) vec ? dequantize<Bf16, FMT, true>(a, s) : dequantize<Bf16, FMT, false>(a, s);
+  else vec ? dequantize<F32, FMT, true>(a, s) : dequantize<F32, FMT, false>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s) {
+  if (fmt == kMxFp4) quantize_any<kMxFp4>(a, dtype, vec, s);
+  else if (fmt == kMxFp8) quantize_any<kMxFp8>(a, dtype, vec, s);
+  else quantize_any<kMxInt8>(a, dtype, vec, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s) {
+  if (fmt == kMxFp4) dequantize_any<kMxFp4>(a, dtype, vec, s);
+  else if (fmt == kMxFp8) dequantize_any<kMxFp8>(a, dtype, vec, s);
+  else dequantize_any<kMxInt8>(a, dtype, vec, s);
+  return hipGetLastError();
+}
+
+}  // namespace flce

@@ -1,0 +1,517 @@
+// Layer norm for gfx950, forward and backward.
+//
+//   mean = sum_j x_j / H,  rstd = (sum_j (x_j - mean)^2 / H + eps)^-1/2,
+//   xh = (x - mean) rstd,  y = weight xh + bias
+//   g = weight dy,  dx = rstd (g - mean_j g - xh mean_j(g xh)),
+//   dweight = sum_m dy xh,  dbias = sum_m dy
+//
+// All sums are in 32 bits.  The variance is that of the centred values, a second pass over
+// registers that also sums the centred values themselves: their mean is what the first pass
+// got wrong, and correcting both statistics by it makes an offset much larger than the
+// spread cost no digits (a constant row is centred to exact zeros).  Both directions are
+// bound by memory: every element is read once and written once.  A row lives in the
+// registers of one wave (H <= 2048) or one workgroup, 8 consecutive elements a chunk.
+// The forward can write a microscaled 8-bit copy of x on the way (the quad of lanes that
+// holds a block of 32 finds its scale), and the backward can read that copy in place of x.
+//
+// The backward's workgroups each walk many rows and keep the column sums of dweight and
+// dbias in registers; each leaves one row of partial sums, and a second kernel adds those in
+// a fixed order: no atomics, so results are bitwise repeatable.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx_device.h"
+#include "ops_internal.h"
+
+namespace flce {
+
+namespace {
+
+// The sum over the 64 lanes of a wave, in every lane.
+template <int CTRL>
+__device__ __forceinline__ float dpp_sum(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v = dpp_sum<0xB1>(v);   // lane ^ 1
+  v = dpp_sum<0x4E>(v);   // lane ^ 2
+  v = dpp_sum<0x141>(v);  // the other quad of 8 lanes (half-row mirror)
+  v = dpp_sum<0x140>(v);  // the other 8 lanes of 16 (row mirror)
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  return v;
+}
+
+// Sums of N <= 2 values over the NT threads that share a row (in every thread).  More than
+// one wave meet in LDS; `buf` (2 x NT / 64 x 2 floats) alternates halves, so that one barrier
+// a call is enough: a wave can only write a half again after the barrier of the call between,
+// which every wave reaches after it has read that half.
+template <int NT>
+struct RowSum {
+  float* buf;
+  int turn = 0;
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+    if constexpr (NT > 64) {
+      constexpr int W = NT / 64;
+      float* b = buf + turn * (2 * W);
+      turn ^= 1;
+      const int wave = threadIdx.x >> 6;
+      if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) b[wave * N + i] = v[i];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float s = b[i];
+#pragma unroll
+        for (int w = 1; w < W; ++w) s += b[w * N + i];
+        v[i] = s;
+      }
+    }
+  }
+};
+
+// 1 / sqrt(variance + eps) from the mean square about a value `off` away from the mean.
+__device__ __forceinline__ float row_rstd(float square, float off, float eps) {
+  const float var = fmaf(-off, off, square);
+  return 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);  // NaN stays NaN
+}
+
+// Elements [col, col + 8) of a parameter vector (or `other` everywhere without one), 0 past
+// the end.
+template <bool VEC>
+__device__ __forceinline__ void load_param(const void* p, int dtype, int col, int H, float other,
+                                           float (&v)[8]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = col + i < H ? other : 0.f;
+  } else if (dtype == kF32) {
+    load8<F32, VEC>(static_cast<const float*>(p), col, H, v);
+  } else {
+    load8<Bf16, VEC>(static_cast<const uint16_t*>(p), col, H, v);
+  }
+}
+
+// One block's share of a checkpoint row: 8 codes, and the scale byte from the quad's first
+// lane.
+template <int FMT>
+__device__ __forceinline__ void save8(const float (&v)[8], int col, uint8_t* codes, uint8_t* scales) {
+  const uint32_t byte = mx_scale_byte<FMT>(v);
+  *reinterpret_cast<u32x2_t*>(codes + col) = mx_encode<FMT>(v, byte);
+  if ((col & 31) == 0) scales[col >> 5] = (uint8_t)byte;
+}
+
+// Rows of H <= 8 NT CH elements, NT threads a row.
+template <class TX, class TY, int NT, int CH, bool VEC>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_fwd_kernel(NormFwdArgs p) {
+  constexpr int THREADS = NT < 256 ? 256 : NT, ROWS = THREADS / NT;
+  __shared__ float red[4 * (NT / 64)];
+  const int t = threadIdx.x % NT, H = p.H;
+  RowSum<NT> sum{red};
+  float w[CH][8], b[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    load_param<VEC>(p.weight, p.param_dtype, 8 * (t + NT * c), H, 1.f, w[c]);
+    load_param<VEC>(p.bias, p.param_dtype, 8 * (t + NT * c), H, 0.f, b[c]);
+  }
+  const float rh = 1.f / (float)H;
+  const long code_ld = mx_code_bytes(H, kMxFp8), scale_ld = mx_scale_bytes(H);
+  // rows are uniform over the threads that meet at a barrier
+  for (long row = (long)blockIdx.x * ROWS + threadIdx.x / NT; row < p.M; row += (long)gridDim.x * ROWS) {
+    const typename TX::mem* x = static_cast<const typename TX::mem*>(p.x) + row * p.ldx;
+    float v[CH][8];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c) load8<TX, VEC>(x, 8 * (t + NT * c), H, v[c]);
+    if (p.fmt != kMxNone) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = 8 * (t + NT * c);
+        // whole quads: the codes' rows end with a whole block
+        if (col < code_ld) {
+          if (p.fmt == kMxFp8)
+            save8<kMxFp8>(v[c], col, p.codes + row * code_ld, p.scales + row * scale_ld);
+          else
+            save8<kMxInt8>(v[c], col, p.codes + row * code_ld, p.scales + row * scale_ld);
+        }
+      }
+      for (long i = mx_blocks(H) + t; i < scale_ld; i += NT) p.scales[row * scale_ld + i] = 0;
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] += v[c][i];
+    sum(s);
+    const float first = s[0] / (float)H;
+    float q[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = 8 * (t + NT * c) + (VEC ? 0 : i) < H ? v[c][i] - first : 0.f;
+        v[c][i] = d;
+        q[0] += d;
+        q[1] = fmaf(d, d, q[1]);
+      }
+    sum(q);
+    const float off = q[0] * rh, mean = first + off;
+    const float rstd = row_rstd(q[1] * rh, off, p.eps);
+    typename TY::mem* y = static_cast<typename TY::mem*>(p.y) + row * p.ldy;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = fmaf((v[c][i] - off) * rstd, w[c][i], b[c][i]);
+      store8<TY, VEC>(y, 8 * (t + NT * c), H, o);
+    }
+    if (t == 0) {
+      p.mean[row] = mean;
+      p.rstd[row] = rstd;
+    }
+  }
+}
+
+// The backward's view of the input: a matrix of T, or its 8-bit checkpoint.
+struct Saved {};
+template <class TX, bool VEC>
+__device__ __forceinline__ void load_x(const NormBwdArgs& p, long row, int col, float (&v)[8]) {
+  if constexpr (__is_same(TX, Saved)) {
+    const long code_ld = mx_code_bytes(p.H, kMxFp8), scale_ld = mx_scale_bytes(p.H);
+    if (col < code_ld) {
+      const u32x2_t r = *reinterpret_cast<const u32x2_t*>(p.codes + row * code_ld + col);
+      const uint32_t byte = p.scales[row * scale_ld + (col >> 5)];
+      if (p.fmt == kMxFp8)
+        mx_decode<kMxFp8>(r, byte, v);
+      else
+        mx_decode<kMxInt8>(r, byte, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
+  } else {
+    load8<TX, VEC>(static_cast<const typename TX::mem*>(p.x) + row * p.ldx, col, p.H, v);
+  }
+}
+
+// Rows of H <= 8 NT CH elements; group g of the launch takes rows g, g + groups, ... and
+// leaves the column sums of its rows.  Rows that share a workgroup (NT = 64) join their sums
+// in LDS first, in order.
+template <class TX, class TY, class TD, int NT, int CH, bool VEC>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_bwd_kernel(NormBwdArgs p) {
+  constexpr int THREADS = NT < 256 ? 256 : NT, ROWS = THREADS / NT;
+  __shared__ float red[4 * (NT / 64)];
+  __shared__ float join[ROWS > 1 ? 16 * NT * CH : 1];
+  const int t = threadIdx.x % NT, slot = threadIdx.x / NT, H = p.H;
+  RowSum<NT> sum{red};
+  float w[CH][8], dw[CH][8], db[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    load_param<VEC>(p.weight, p.param_dtype, 8 * (t + NT * c), H, 1.f, w[c]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[c][i] = db[c][i] = 0.f;
+  }
+  const float rh = 1.f / (float)H;
+  for (long row = (long)blockIdx.x * ROWS + slot; row < p.M; row += (long)gridDim.x * ROWS) {
+    const typename TY::mem* dy = static_cast<const typename TY::mem*>(p.dy) + row * p.lddy;
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    float x[CH][8], g[CH][8];
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      load_x<TX, VEC>(p, row, 8 * (t + NT * c), x[c]);
+      load8<TY, VEC>(dy, 8 * (t + NT * c), H, g[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // past the row g is 0, and so is its share of every sum
+        const float xh = (x[c][i] - mean) * rstd;
+        dw[c][i] = fmaf(g[c][i], xh, dw[c][i]);
+        db[c][i] += g[c][i];
+        g[c][i] *= w[c][i];
+        x[c][i] = xh;
+        s[0] += g[c][i];
+        s[1] = fmaf(g[c][i], xh, s[1]);
+      }
+    sum(s);
+    const float m0 = s[0] * rh, m1 = s[1] * rh;
+    typename TD::mem* dx = static_cast<typename TD::mem*>(p.dx) + row * p.lddx;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = rstd * (g[c][i] - m0 - x[c][i] * m1);
+      store8<TD, VEC>(dx, 8 * (t + NT * c), H, o);
+    }
+  }
+  if constexpr (ROWS > 1) {
+    // slot 0 adds the other slots' sums to its own, one slot after another
+    float* jw = join + 16 * CH * t;
+    for (int k = 1; k < ROWS; ++k) {
+      if (slot == k) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            jw[16 * c + i] = dw[c][i];
+            jw[16 * c + 8 + i] = db[c][i];
+          }
+      }
+      __syncthreads();
+      if (slot == 0) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            dw[c][i] += jw[16 * c + i];
+            db[c][i] += jw[16 * c + 8 + i];
+          }
+      }
+      __syncthreads();
+    }
+    if (slot != 0) return;
+  }
+  float* pw = p.part + (long)blockIdx.x * H;
+  float* pb = pw + (long)p.groups * H;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    store8<F32, VEC>(pw, 8 * (t + NT * c), H, dw[c]);
+    store8<F32, VEC>(pb, 8 * (t + NT * c), H, db[c]);
+  }
+}
+
+// Rows too long for a workgroup's registers: passes over memory (the row is in L2 after the
+// first).  Thread t takes chunks t, t + 1024, ...
+constexpr int WIDE = 1024;
+template <class TX, class TY, bool VEC>
+__global__ __launch_bounds__(WIDE) void norm_fwd_wide_kernel(NormFwdArgs p) {
+  __shared__ float red[4 * (WIDE / 64)];
+  RowSum<WIDE> sum{red};
+  const int t = threadIdx.x, H = p.H;
+  const float rh = 1.f / (float)H;
+  const long code_ld = mx_code_bytes(H, kMxFp8), scale_ld = mx_scale_bytes(H);
+  for (long row = blockIdx.x; row < p.M; row += gridDim.x) {
+    const typename TX::mem* x = static_cast<const typename TX::mem*>(p.x) + row * p.ldx;
+    float s[1] = {0.f};
+    float v[8], w[8], b[8];
+    for (int col = 8 * t; col < code_ld; col += 8 * WIDE) {
+      load8<TX, VEC>(x, col, H, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] += v[i];
+      if (p.fmt == kMxFp8)
+        save8<kMxFp8>(v, col, p.codes + row * code_ld, p.scales + row * scale_ld);
+      else if (p.fmt == kMxInt8)
+        save8<kMxInt8>(v, col, p.codes + row * code_ld, p.scales + row * scale_ld);
+    }
+    if (p.fmt != kMxNone)
+      for (long i = mx_blocks(H) + t; i < scale_ld; i += WIDE) p.scales[row * scale_ld + i] = 0;
+    sum(s);
+    const float first = s[0] / (float)H;
+    float q[2] = {0.f, 0.f};
+    for (int col = 8 * t; col < H; col += 8 * WIDE) {
+      load8<TX, VEC>(x, col, H, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = col + i < H ? v[i] - first : 0.f;
+        q[0] += d;
+        q[1] = fmaf(d, d, q[1]);
+      }
+    }
+    sum(q);
+    const float off = q[0] * rh, mean = first + off;
+    const float rstd = row_rstd(q[1] * rh, off, p.eps);
+    typename TY::mem* y = static_cast<typename TY::mem*>(p.y) + row * p.ldy;
+    for (int col = 8 * t; col < H; col += 8 * WIDE) {
+      load8<TX, VEC>(x, col, H, v);
+      load_param<VEC>(p.weight, p.param_dtype, col, H, 1.f, w);
+      load_param<VEC>(p.bias, p.param_dtype, col, H, 0.f, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = fmaf((v[i] - first - off) * rstd, w[i], b[i]);
+      store8<TY, VEC>(y, col, H, v);
+    }
+    if (t == 0) {
+      p.mean[row] = mean;
+      p.rstd[row] = rstd;
+    }
+  }
+}
+
+// Column sums travel through the workgroup's own row of partial sums: cleared by its first
+// row, added to by the others (each element always by the same thread).
+template <class TX, class TY, class TD, bool VEC>
+__global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormBwdArgs p) {
+  __shared__ float red[4 * (WIDE / 64)];
+  RowSum<WIDE> sum{red};
+  const int t = threadIdx.x, H = p.H;
+  const float rh = 1.f / (float)H;
+  float* pw = p.part + (long)blockIdx.x * H;
+  float* pb = pw + (long)p.groups * H;
+  bool first = true;
+  for (long row = blockIdx.x; row < p.M; row += gridDim.x) {
+    const typename TY::mem* dy = static_cast<const typename TY::mem*>(p.dy) + row * p.lddy;
+    typename TD::mem* dx = static_cast<typename TD::mem*>(p.dx) + row * p.lddx;
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    float s[2] = {0.f, 0.f};
+    float x[8], g[8], w[8], a[8], b[8];
+    for (int col = 8 * t; col < H; col += 8 * WIDE) {
+      load_x<TX, VEC>(p, row, col, x);
+      load8<TY, VEC>(dy, col, H, g);
+      load_param<VEC>(p.weight, p.param_dtype, col, H, 1.f, w);
+      if (first) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.f;
+      } else {
+        load8<F32, VEC>(pw, col, H, a);
+        load8<F32, VEC>(pb, col, H, b);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float xh = (x[i] - mean) * rstd;
+        a[i] = fmaf(g[i], xh, a[i]);
+        b[i] += g[i];
+        g[i] *= w[i];
+        s[0] += g[i];
+        s[1] = fmaf(g[i], xh, s[1]);
+      }
+      store8<F32, VEC>(pw, col, H, a);
+      store8<F32, VEC>(pb, col, H, b);
+    }
+    first = false;
+    sum(s);
+    const float m0 = s[0] * rh, m1 = s[1] * rh;
+    for (int col = 8 * t; col < H; col += 8 * WIDE) {
+      load_x<TX, VEC>(p, row, col, x);
+      load8<TY, VEC>(dy, col, H, g);
+      load_param<VEC>(p.weight, p.param_dtype, col, H, 1.f, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = rstd * (g[i] * w[i] - m0 - (x[i] - mean) * rstd * m1);
+      store8<TD, VEC>(dx, col, H, x);
+    }
+  }
+}
+
+// dweight and dbias: the sum of the groups' partial rows, in a fixed order.  A workgroup
+// takes 64 columns; its 16 waves share the groups and meet in LDS.
+constexpr int REDUCE_COLS = 64, REDUCE_SLICES = 16;
+__global__ __launch_bounds__(REDUCE_COLS * REDUCE_SLICES) void norm_reduce_kernel(NormReduceArgs p) {
+  __shared__ float part[REDUCE_SLICES][REDUCE_COLS];
+  const int lane = threadIdx.x % REDUCE_COLS, slice = threadIdx.x / REDUCE_COLS;
+  const int per = (p.H + REDUCE_COLS - 1) / REDUCE_COLS;
+  const bool bias = (int)blockIdx.x >= per;
+  void* out = bias ? p.dbias : p.dweight;
+  const long col = (long)((int)blockIdx.x - (bias ? per : 0)) * REDUCE_COLS + lane;
+  if (!out) return;  // uniform over the workgroup
+  const float* src = p.part + (bias ? (long)p.groups * p.H : 0) + col;
+  float s = 0.f;
+  if (col < p.H) {
+#pragma unroll 4
+    for (int g = slice; g < p.groups; g += REDUCE_SLICES) s += src[(long)g * p.H];
+  }
+  part[slice][lane] = s;
+  __syncthreads();
+  if (slice != 0 || col >= p.H) return;
+#pragma unroll
+  for (int k = 1; k < REDUCE_SLICES; ++k) s += part[k][lane];
+  if (p.param_dtype == kF32)
+    static_cast<float*>(out)[col] = s;
+  else
+    static_cast<uint16_t*>(out)[col] = Bf16::from_f32(s);
+}
+
+constexpr int kComputeUnits = 256;
+
+template <class TX, class TY, bool VEC>
+void fwd_rows(const NormFwdArgs& a, hipStream_t s) {
+  auto grid = [&](int rows_per_group, int groups_per_unit) {
+    const long need = (a.M + rows_per_group - 1) / rows_per_group;
+    const long most = (long)kComputeUnits * groups_per_unit;
+    return (unsigned)(need < most ? need : most);
+  };
+  if (a.H <= 512)
+    norm_fwd_kernel<TX, TY, 64, 1, VEC><<<grid(4, 8), 256, 0, s>>>(a);
+  else if (a.H <= 1024)
+    norm_fwd_kernel<TX, TY, 64, 2, VEC><<<grid(4, 8), 256, 0, s>>>(a);
+  else if (a.H <= 2048)
+    norm_fwd_kernel<TX, TY, 64, 4, VEC><<<grid(4, 4), 256, 0, s>>>(a);
+  else if (a.H <= 4096)
+    norm_fwd_kernel<TX, TY, 256, 2, VEC><<<grid(1, 8), 256, 0, s>>>(a);
+  else if (a.H <= 8192)
+    norm_fwd_kernel<TX, TY, 512, 2, VEC><<<grid(1, 4), 512, 0, s>>>(a);
+  else if (a.H <= 16384)
+    norm_fwd_kernel<TX, TY, 1024, 2, VEC><<<grid(1, 2), 1024, 0, s>>>(a);
+  else
+    norm_fwd_wide_kernel<TX, TY, VEC><<<grid(1, 2), WIDE, 0, s>>>(a);
+}
+
+template <class TX, class TY, class TD, bool VEC>
+void bwd_rows(const NormBwdArgs& a, hipStream_t s) {
+  const unsigned g = (unsigned)a.groups;
+  if (a.H <= 512)
+    norm_bwd_kernel<TX, TY, TD, 64, 1, VEC><<<g, 256, 0, s>>>(a);
+  else if (a.H <= 1024)
+    norm_bwd_kernel<TX, TY, TD, 64, 2, VEC><<<g, 256, 0, s>>>(a);
+  else if (a.H <= 2048)
+    norm_bwd_kernel<TX, TY, TD, 256, 1, VEC><<<g, 256, 0, s>>>(a);
+  else if (a.H <= 4096)
+    norm_bwd_kernel<TX, TY, TD, 256, 2, VEC><<<g, 256, 0, s>>>(a);
+  else if (a.H <= 8192)
+    norm_bwd_kernel<TX, TY, TD, 512, 2, VEC><<<g, 512, 0, s>>>(a);
+  else
+    norm_bwd_wide_kernel<TX, TY, TD, VEC><<<g, WIDE, 0, s>>>(a);
+}
+
+template <class TX, class TY, class TD>
+void bwd_vec(const NormBwdArgs& a, bool vec, hipStream_t s) {
+  if (vec) bwd_rows<TX, TY, TD, true>(a, s);
+  else bwd_rows<TX, TY, TD, false>(a, s);
+}
+template <class TX, class TY>
+void fwd_vec(const NormFwdArgs& a, bool vec, hipStream_t s) {
+  if (vec) fwd_rows<TX, TY, true>(a, s);
+  else fwd_rows<TX, TY, false>(a, s);
+}
+
+}  // namespace
+
+int norm_bwd_groups(long M, int H) {
+  const int rows = H <= 1024 ? 4 : 1;
+  const int per_unit = H <= 1024 ? 4 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1;
+  const long need = (M + rows - 1) / rows, most = (long)kComputeUnits * per_unit;
+  return (int)(need < most ? need : most);
+}
+
+hipError_t launch_norm_fwd(const NormFwdArgs& a, int x_dtype, int y_dtype, bool vec, hipStream_t s) {
+  if (x_dtype == kBf16) fwd_vec<Bf16, Bf16>(a, vec, s);
+  else if (y_dtype == kBf16) fwd_vec<F32, Bf16>(a, vec, s);
+  else fwd_vec<F32, F32>(a, vec, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_bwd(const NormBwdArgs& a, int x_dtype, int dy_dtype, int dx_dtype, bool vec,
+                           hipStream_t s) {
+  if (!a.x) {
+    if (dx_dtype == kBf16) bwd_vec<Saved, Bf16, Bf16>(a, vec, s);
+    else if (dy_dtype == kBf16) bwd_vec<Saved, Bf16, F32>(a, vec, s);
+    else bwd_vec<Saved, F32, F32>(a, vec, s);
+  } else if (x_dtype == kBf16) {
+    bwd_vec<Bf16, Bf16, Bf16>(a, vec, s);
+  } else if (dy_dtype == kBf16) {
+    bwd_vec<F32, Bf16, F32>(a, vec, s);
+  } else {
+    bwd_vec<F32, F32, F32>(a, vec, s);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_reduce(const NormReduceArgs& a, hipStream_t s) {
+  const unsigned per = (unsigned)((a.H + REDUCE_COLS - 1) / REDUCE_COLS);
+  norm_reduce_kernel<<<2 * per, REDUCE_COLS * REDUCE_SLICES, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace flce

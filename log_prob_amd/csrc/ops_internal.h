@@ -1,0 +1,116 @@
+// Internal interface between the libflce host code and the kernels of the operators
+// around the head: layer norm, microscaled formats, the head with 4-bit weights.
+// Not installed; not part of the C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "flce_internal.h"
+
+namespace flce {
+
+// Element types and microscaled formats: the values of the C ABI's enumerations.
+constexpr int kBf16 = 0, kF32 = 1;
+constexpr int kMxNone = -1, kMxFp4 = 0, kMxFp8 = 1, kMxInt8 = 2;
+
+// Microscaled layout: row bytes of codes (whole blocks of 32) and of scales (a multiple of
+// 16, so that a row's scales can be read 16 bytes at a time).
+constexpr int64_t mx_blocks(int64_t cols) { return (cols + 31) / 32; }
+constexpr int64_t mx_code_bytes(int64_t cols, int fmt) {
+  return mx_blocks(cols) * (fmt == kMxFp4 ? 16 : 32);
+}
+constexpr int64_t mx_scale_bytes(int64_t cols) { return (mx_blocks(cols) + 15) / 16 * 16; }
+
+struct NormFwdArgs {
+  const void* x;
+  long ldx;                // elements between rows
+  const void* weight;      // [H] or nullptr (1)
+  const void* bias;        // [H] or nullptr (0)
+  int param_dtype;
+  long M;
+  int H;
+  float eps;
+  void* y;
+  long ldy;
+  float* mean;
+  float* rstd;
+  int fmt;                 // checkpoint format, kMxNone for none
+  uint8_t* codes;
+  uint8_t* scales;
+};
+
+struct NormBwdArgs {
+  const void* dy;
+  long lddy;
+  const void* x;           // the input, or nullptr: codes and scales of it
+  long ldx;
+  int fmt;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const void* weight;      // [H] or nullptr (1)
+  int param_dtype;
+  const float* mean;
+  const float* rstd;
+  long M;
+  int H;
+  void* dx;
+  long lddx;
+  float* part;             // [2][groups][H] partial sums of dweight and dbias
+  int groups;              // workgroups of the row kernel = rows of each partial array
+};
+
+struct NormReduceArgs {
+  const float* part;
+  int groups;
+  int H;
+  void* dweight;           // [H] or nullptr
+  void* dbias;
+  int param_dtype;
+};
+
+// Workgroups of the backward's row kernel for a shape (they share the rows between them and
+// leave one partial sum each).
+int norm_bwd_groups(long M, int H);
+hipError_t launch_norm_fwd(const NormFwdArgs& a, int x_dtype, int y_dtype, bool vec, hipStream_t s);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, int x_dtype, int dy_dtype, int dx_dtype, bool vec,
+                           hipStream_t s);
+hipError_t launch_norm_reduce(const NormReduceArgs& a, hipStream_t s);
+
+struct MxQuantArgs {
+  const void* x;           // quantise: the matrix; dequantise: unused
+  long ldx;
+  void* out;               // dequantise: the values
+  long ldo;
+  uint8_t* codes;
+  uint8_t* scales;
+  long rows;
+  long cols;
+};
+hipError_t launch_mx_quantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s);
+hipError_t launch_mx_dequantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s);
+
+// The head with 4-bit weights: X and W as MXFP4 codes and scales.
+struct MxOperand {
+  const uint8_t* codes;
+  const uint8_t* scales;
+};
+struct MxLogitsArgs {
+  MxOperand x, w;
+  int M, H, V;
+  float scale;
+  void* out;               // [M, V] logits
+  long ldo;
+  int out_dtype;
+  int n_mt, n_vt;
+};
+hipError_t launch_mx_logits(const MxLogitsArgs& a, bool vec, hipStream_t s);
+// Log-prob partials: f holds the outputs and sizes (f.X and f.W unused).
+struct MxFwdArgs {
+  MxOperand x, w;
+  FwdTileArgs f;
+};
+hipError_t launch_mx_fwd_tile(const MxFwdArgs& a, bool entropy, hipStream_t s);
+hipError_t launch_mx_target_logit(const MxFwdArgs& a, hipStream_t s);
+
+}  // namespace flce

@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import Any, NamedTuple, Optional, Tuple
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libflce.so")
@@ -27,6 +27,8 @@ EXPORTS = ("flce_workspace_query", "flce_forward_workspace_min", "flce_forward_w
            "flce_forward_partials_shard", "flce_forward_merge_shards",
            "flce_backward_shard_workspace_query", "flce_backward_shard", "flce_nll_reduce",
            "flce_nll_mean_grad", "flce_policy_loss_reduce", "flce_policy_loss_grad",
+           "flce_mx_sizes", "flce_mx_quantize", "flce_mx_dequantize", "flce_layer_norm_forward",
+           "flce_layer_norm_backward_workspace", "flce_layer_norm_backward",
            "flce_status_string",
            "flce_last_error_message", "flce_version")
 
@@ -78,7 +80,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     D = c.c_double
     lib.flce_policy_loss_reduce.argtypes = [P, P, P, P, I64, I64, I64, D, D, D, P, P, P, P]
     lib.flce_policy_loss_grad.argtypes = [P, P, P, P, I64, I64, I64, D, D, D, P, P, P]
-    for name in ("flce_nll_reduce", "flce_nll_mean_grad", "flce_policy_loss_reduce",
+    I = c.c_int
+    lib.flce_mx_sizes.argtypes = [I64, I, c.POINTER(I64), c.POINTER(I64)]
+    lib.flce_mx_quantize.argtypes = [P, I, I64, I64, I64, I, P, P, P]
+    lib.flce_mx_dequantize.argtypes = [P, P, I, I64, I64, P, I, I64, P]
+    lib.flce_layer_norm_forward.argtypes = [P, I, I64, P, P, I, I64, I64, c.c_float, P, I, I64, P,
+                                            P, I, P, P, P]
+    lib.flce_layer_norm_backward_workspace.argtypes = [I64, I64, c.POINTER(SZ)]
+    lib.flce_layer_norm_backward.argtypes = [P, I, I64, P, I, I64, I, P, P, P, I, P, P, I64, I64,
+                                             P, I, I64, P, P, P, SZ, P]
+    for name in ("flce_mx_sizes", "flce_mx_quantize", "flce_mx_dequantize",
+                 "flce_layer_norm_forward", "flce_layer_norm_backward_workspace",
+                 "flce_layer_norm_backward", "flce_nll_reduce", "flce_nll_mean_grad", "flce_policy_loss_reduce",
                  "flce_policy_loss_grad", "flce_workspace_query",
                  "flce_forward_workspace_min", "flce_forward_wave_rows",
                  "flce_backward_workspace_min", "flce_backward_chunk_cols",
@@ -460,3 +473,263 @@ def policy_loss_grad(logprob, old_logprob, advantages, targets, V: int, reduced=
         int(ignore_index), float(eps_low), float(eps_high), float(denominator), _ptr(reduced),
         _ptr(out), _stream(logprob.device)))
     return out
+
+
+# ----------------------------------------------------------------------------
+# operators around the head: microscaled formats and the layer norm in front of it
+MX_FORMATS = {"mxfp4": 0, "mxfp8": 1, "mxint8": 2}
+_MX_NONE = -1
+
+
+class MXTensor(NamedTuple):
+    """A matrix [rows, cols] in a microscaled format: uint8 codes and scale bytes, laid out
+    as include/flce.h states (mx_quantize makes them)."""
+    codes: Any
+    scales: Any
+    fmt: str
+    cols: int
+
+
+def _dtype_id(t, name) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype == torch.float32:
+        return 1
+    raise TypeError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+
+
+def _rows(t, name, dev, shape=None):
+    """Check a matrix whose rows are contiguous; returns its row stride."""
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    m, h = t.shape
+    if h > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if m <= 1:
+        return h
+    if t.stride(0) < h:
+        raise ValueError(f"{name}: rows overlap")
+    return t.stride(0)
+
+
+def _on_gpu(t, name):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: expected a GPU tensor")
+    return t.device
+
+
+def _vector(t, name, dev, dtype, n):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
+    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous elements, got shape {tuple(t.shape)}")
+
+
+def _launch(dev, fn, *args):
+    """Call fn(*args, stream) with dev's current stream, on dev."""
+    import torch
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        _check(fn(*args, stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream))
+
+
+def _mx_format(fmt, allowed=tuple(MX_FORMATS)) -> int:
+    if fmt not in allowed:
+        raise ValueError(f"microscaled format: expected one of {allowed}, got {fmt!r}")
+    return MX_FORMATS[fmt]
+
+
+def mx_sizes(cols: int, fmt: str) -> Tuple[int, int]:
+    """Bytes of a row of codes and of a row of scales for `cols` elements."""
+    a, b = ctypes.c_int64(), ctypes.c_int64()
+    _check(load().flce_mx_sizes(int(cols), _mx_format(fmt), ctypes.byref(a), ctypes.byref(b)))
+    return a.value, b.value
+
+
+def _mx_row_bytes(cols, f):
+    blocks = -(-cols // 32)
+    return blocks * (16 if f == 0 else 32), -(-blocks // 16) * 16
+
+
+def _mx_empty(rows, cols, fmt, f, dev):
+    import torch
+    cb, sb = _mx_row_bytes(cols, f)
+    return MXTensor(torch.empty((rows, cb), dtype=torch.uint8, device=dev),
+                    torch.empty((rows, sb), dtype=torch.uint8, device=dev), fmt, cols)
+
+
+def _mx_check(q, name, dev, f, rows, cols):
+    import torch
+    cb, sb = _mx_row_bytes(cols, f)
+    if q.cols != cols:
+        raise ValueError(f"{name}: expected {cols} columns, got {q.cols}")
+    for part, t, n in (("codes", q.codes, cb), ("scales", q.scales, sb)):
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{name}.{part}: expected uint8, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name}.{part}: expected a tensor on {dev}, got {t.device}")
+        if tuple(t.shape) != (rows, n) or not t.is_contiguous():
+            raise ValueError(f"{name}.{part}: expected contiguous shape {(rows, n)}, got "
+                             f"{tuple(t.shape)}")
+
+
+def mx_quantize(x, fmt: str, out: Optional[MXTensor] = None) -> MXTensor:
+    """x [rows, cols] (bf16 or fp32) in a microscaled format: "mxfp4", "mxfp8" or "mxint8"."""
+    f = _mx_format(fmt)
+    dev = _on_gpu(x, "x")
+    xd, ldx = _dtype_id(x, "x"), _rows(x, "x", dev)
+    m, h = x.shape
+    if out is None:
+        out = _mx_empty(m, h, fmt, f, dev)
+    else:
+        if out.fmt != fmt:
+            raise ValueError(f"out: expected format {fmt}, got {out.fmt}")
+        _mx_check(out, "out", dev, f, m, h)
+    _launch(dev, load().flce_mx_quantize, x.data_ptr(), xd, ldx, m, h, f, out.codes.data_ptr(),
+            out.scales.data_ptr())
+    return out
+
+
+def mx_dequantize(q: MXTensor, dtype=None, out=None):
+    """The values of a microscaled matrix, as bf16 (the default) or fp32."""
+    import torch
+    f = _mx_format(q.fmt)
+    dev = _on_gpu(q.codes, "codes")
+    m = q.codes.shape[0]
+    _mx_check(q, "q", dev, f, m, q.cols)
+    if out is None:
+        out = torch.empty((m, q.cols), dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out: expected {dtype}, got {out.dtype}")
+    od, ldo = _dtype_id(out, "out"), _rows(out, "out", dev, (m, q.cols))
+    _launch(dev, load().flce_mx_dequantize, q.codes.data_ptr(), q.scales.data_ptr(), f, m, q.cols,
+            out.data_ptr(), od, ldo)
+    return out
+
+
+def _params(weight, bias, dev, h):
+    """The parameters' common element type (bf16 without any)."""
+    pd = None
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is None:
+            continue
+        d = _dtype_id(t, name)
+        if pd is not None and d != pd:
+            raise TypeError("weight and bias must have the same dtype")
+        pd = d
+        _vector(t, name, dev, t.dtype, h)
+    return 0 if pd is None else pd
+
+
+def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out_dtype=None,
+                       checkpoint: Optional[str] = None, out=None):
+    """(y, mean, rstd) of the layer norm over the rows of x [M, H], and with `checkpoint`
+    ("mxfp8" or "mxint8") a fourth result: x in that format, for layer_norm_backward.
+
+    x is bf16 or fp32, y has out_dtype (x's by default; bf16 from fp32 is the usual step from
+    an fp32 residual stream into the bf16 head), mean and rstd are fp32 [M].  `out` may supply
+    the results' buffers."""
+    import torch
+    dev = _on_gpu(x, "x")
+    xd, ldx = _dtype_id(x, "x"), _rows(x, "x", dev)
+    m, h = x.shape
+    pd = _params(weight, bias, dev, h)
+    f = _MX_NONE if checkpoint is None else _mx_format(checkpoint, ("mxfp8", "mxint8"))
+    kept = None
+    if out is None:
+        y = torch.empty((m, h), dtype=x.dtype if out_dtype is None else out_dtype, device=dev)
+        mean = torch.empty(m, dtype=torch.float32, device=dev)
+        rstd = torch.empty(m, dtype=torch.float32, device=dev)
+        if checkpoint is not None:
+            kept = _mx_empty(m, h, checkpoint, f, dev)
+    else:
+        y, mean, rstd = out[:3]
+        if out_dtype is not None and y.dtype != out_dtype:
+            raise TypeError(f"y: expected {out_dtype}, got {y.dtype}")
+        _vector(mean, "mean", dev, torch.float32, m)
+        _vector(rstd, "rstd", dev, torch.float32, m)
+        if checkpoint is not None:
+            kept = out[3]
+            if kept.fmt != checkpoint:
+                raise ValueError(f"checkpoint: expected format {checkpoint}, got {kept.fmt}")
+            _mx_check(kept, "checkpoint", dev, f, m, h)
+    yd, ldy = _dtype_id(y, "y"), _rows(y, "y", dev, (m, h))
+    codes, scales = (None, None) if kept is None else (kept.codes.data_ptr(), kept.scales.data_ptr())
+    _launch(dev, load().flce_layer_norm_forward, x.data_ptr(), xd, ldx, _ptr(weight), _ptr(bias),
+            pd, m, h, eps, y.data_ptr(), yd, ldy, mean.data_ptr(), rstd.data_ptr(), f, codes, scales)
+    return (y, mean, rstd) if kept is None else (y, mean, rstd, kept)
+
+
+def layer_norm_backward_workspace(M: int, H: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load().flce_layer_norm_backward_workspace(int(M), int(H), ctypes.byref(b)))
+    return b.value
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, dx_dtype=None, need_params: bool = True,
+                        param_dtype=None, workspace=None, out=None):
+    """(dx, dweight, dbias) of layer_norm_forward; x is its input or its checkpoint.
+
+    dx has x's dtype (from a checkpoint: dx_dtype, dy's by default), dweight and dbias have
+    weight's (without one: param_dtype, fp32 by default), or are None without need_params.
+    `out` may supply the three buffers."""
+    import torch
+    dev = _on_gpu(dy, "dy")
+    dyd, lddy = _dtype_id(dy, "dy"), _rows(dy, "dy", dev)
+    m, h = dy.shape
+    if isinstance(x, MXTensor):
+        f = _mx_format(x.fmt, ("mxfp8", "mxint8"))
+        _mx_check(x, "x", dev, f, m, h)
+        xp, xd, ldx, codes, scales = None, 0, h, x.codes.data_ptr(), x.scales.data_ptr()
+        dx_dtype = dy.dtype if dx_dtype is None else dx_dtype
+    else:
+        f = _MX_NONE
+        xd, ldx = _dtype_id(x, "x"), _rows(x, "x", dev, (m, h))
+        xp, codes, scales = x.data_ptr(), None, None
+        if dx_dtype is not None and dx_dtype != x.dtype:
+            raise TypeError(f"dx_dtype: expected x's {x.dtype}, got {dx_dtype}")
+        dx_dtype = x.dtype
+    _vector(mean, "mean", dev, torch.float32, m)
+    _vector(rstd, "rstd", dev, torch.float32, m)
+    if weight is not None:
+        _params(weight, None, dev, h)
+        if param_dtype is not None and param_dtype != weight.dtype:
+            raise TypeError(f"param_dtype: expected weight's {weight.dtype}, got {param_dtype}")
+        param_dtype = weight.dtype
+    elif param_dtype is None:
+        param_dtype = torch.float32
+    dw = db = None
+    if out is None:
+        dx = torch.empty((m, h), dtype=dx_dtype, device=dev)
+        if need_params:
+            dw = torch.empty(h, dtype=param_dtype, device=dev)
+            db = torch.empty(h, dtype=param_dtype, device=dev)
+    else:
+        dx, dw, db = out
+        if dx.dtype != dx_dtype:
+            raise TypeError(f"dx: expected {dx_dtype}, got {dx.dtype}")
+        for name, t in (("dweight", dw), ("dbias", db)):
+            if t is not None:
+                _vector(t, name, dev, param_dtype, h)
+    dxd, lddx = _dtype_id(dx, "dx"), _rows(dx, "dx", dev, (m, h))
+    pd = {torch.bfloat16: 0, torch.float32: 1}.get(param_dtype)
+    if pd is None:
+        raise TypeError(f"param_dtype: expected bfloat16 or float32, got {param_dtype}")
+    if workspace is None:
+        workspace = alloc_workspace(layer_norm_backward_workspace(m, h), dev)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace: expected a tensor on {dev}, got {workspace.device}")
+    _launch(dev, load().flce_layer_norm_backward, dy.data_ptr(), dyd, lddy, xp, xd, ldx, f, codes,
+            scales, _ptr(weight), pd, mean.data_ptr(), rstd.data_ptr(), m, h, dx.data_ptr(), dxd,
+            lddx, _ptr(dw), _ptr(db), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return dx, dw, db

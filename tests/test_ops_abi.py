@@ -1,0 +1,122 @@
+"""Refusals of the layer norm and microscaled calls: all of them on the host, before any HIP
+call, so no device is needed (pointers are never followed)."""
+import pytest
+
+from log_prob_amd import flce
+
+INVALID, UNSUPPORTED, TOO_SMALL = 1, 2, 3
+P = 1 << 20   # an address that is only looked at
+
+
+def status(name, *args):
+    return getattr(flce.load(), name)(*args)
+
+
+def norm_forward(**kw):
+    a = dict(x=P, xd=0, ldx=64, w=P, b=P, pd=0, M=4, H=64, eps=1e-5, y=P, yd=0, ldy=64, mean=P,
+             rstd=P, fmt=-1, codes=None, scales=None)
+    a.update(kw)
+    return status("flce_layer_norm_forward", *a.values(), None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(M=-1)), (INVALID, dict(H=0)), (UNSUPPORTED, dict(M=(1 << 30) + 1)),
+    (UNSUPPORTED, dict(H=(1 << 20) + 1, ldx=1 << 21, ldy=1 << 21)),
+    (INVALID, dict(xd=2)), (INVALID, dict(yd=-1)), (INVALID, dict(pd=7)),
+    (UNSUPPORTED, dict(xd=0, yd=1)), (INVALID, dict(eps=-1e-5)), (INVALID, dict(eps=float("nan"))),
+    (INVALID, dict(eps=float("inf"))), (INVALID, dict(fmt=0, codes=P, scales=P)),
+    (INVALID, dict(fmt=5, codes=P, scales=P)), (INVALID, dict(fmt=1)),
+    (INVALID, dict(fmt=2, codes=P)), (UNSUPPORTED, dict(fmt=2, codes=P + 8, scales=P)),
+    (INVALID, dict(x=None)), (INVALID, dict(y=None)), (INVALID, dict(mean=None)),
+    (INVALID, dict(rstd=None)), (INVALID, dict(ldx=63)), (INVALID, dict(ldy=0)),
+    (UNSUPPORTED, dict(ldx=(1 << 40) + 1)), (UNSUPPORTED, dict(x=P + 1)),
+    (UNSUPPORTED, dict(xd=1, x=P + 2)), (UNSUPPORTED, dict(w=P + 1)),
+    (UNSUPPORTED, dict(pd=1, b=P + 2)), (UNSUPPORTED, dict(mean=P + 2)),
+])
+def test_layer_norm_forward(want, kw):
+    assert norm_forward(**kw) == want
+    assert flce.load().flce_last_error_message()
+
+
+def norm_backward(**kw):
+    a = dict(dy=P, dyd=0, lddy=64, x=P, xd=0, ldx=64, fmt=-1, codes=None, scales=None, w=P, pd=0,
+             mean=P, rstd=P, M=4, H=64, dx=P, dxd=0, lddx=64, dw=P, db=P, ws=P, wsb=1 << 20)
+    a.update(kw)
+    return status("flce_layer_norm_backward", *a.values(), None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(M=-1)), (INVALID, dict(H=-8)), (INVALID, dict(dyd=3)), (INVALID, dict(xd=3)),
+    (INVALID, dict(dxd=3)), (INVALID, dict(pd=3)),
+    (INVALID, dict(fmt=1, codes=P, scales=P)),              # x and a checkpoint
+    (INVALID, dict(x=None)),                                # neither
+    (INVALID, dict(x=None, fmt=0, codes=P, scales=P)),      # no 4-bit checkpoints
+    (INVALID, dict(x=None, fmt=1)), (UNSUPPORTED, dict(x=None, fmt=1, codes=P, scales=P + 4)),
+    (UNSUPPORTED, dict(xd=1)), (UNSUPPORTED, dict(dyd=1)), (INVALID, dict(dy=None)),
+    (INVALID, dict(mean=None)), (INVALID, dict(dx=None)), (INVALID, dict(ws=None)),
+    (INVALID, dict(lddy=8)), (INVALID, dict(lddx=8)), (INVALID, dict(ldx=8)),
+    (UNSUPPORTED, dict(ws=P + 64)), (TOO_SMALL, dict(wsb=2 * 4 * 64 - 1)),
+    (UNSUPPORTED, dict(dw=P + 1)), (UNSUPPORTED, dict(rstd=P + 1)),
+])
+def test_layer_norm_backward(want, kw):
+    assert norm_backward(**kw) == want
+
+
+def test_layer_norm_workspace():
+    assert flce.layer_norm_backward_workspace(0, 64) == 0
+    assert flce.layer_norm_backward_workspace(1, 64) == 2 * 4 * 64
+    # bounded, whatever the number of rows
+    assert (flce.layer_norm_backward_workspace(1 << 30, 4096)
+            == flce.layer_norm_backward_workspace(1 << 20, 4096) <= 1024 * 2 * 4 * 4096)
+    with pytest.raises(flce.FlceError):
+        flce.layer_norm_backward_workspace(1, 0)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(rows=-1)), (INVALID, dict(cols=0)), (UNSUPPORTED, dict(cols=(1 << 20) + 1)),
+    (INVALID, dict(xd=2)), (INVALID, dict(fmt=-1)), (INVALID, dict(fmt=3)), (INVALID, dict(x=None)),
+    (INVALID, dict(ldx=31)), (UNSUPPORTED, dict(x=P + 1)), (INVALID, dict(codes=None)),
+    (INVALID, dict(scales=None)), (UNSUPPORTED, dict(codes=P + 8)), (UNSUPPORTED, dict(scales=P + 1)),
+])
+def test_quantize(want, kw):
+    a = dict(x=P, xd=0, ldx=32, rows=2, cols=32, fmt=0, codes=P, scales=P)
+    a.update(kw)
+    assert status("flce_mx_quantize", *a.values(), None) == want
+    d = dict(codes=a["codes"], scales=a["scales"], fmt=a["fmt"], rows=a["rows"], cols=a["cols"],
+             out=a["x"], od=a["xd"], ldo=a["ldx"])
+    assert status("flce_mx_dequantize", *d.values(), None) == want
+
+
+def test_sizes():
+    assert flce.mx_sizes(1, "mxfp4") == (16, 16)
+    assert flce.mx_sizes(32, "mxfp8") == (32, 16)
+    assert flce.mx_sizes(513, "mxint8") == (544, 32)
+    assert flce.mx_sizes(512, "mxfp4") == (256, 16)
+    with pytest.raises(ValueError):
+        flce.mx_sizes(32, "fp4")
+    for cols, fmt in ((0, "mxfp8"), ((1 << 20) + 1, "mxfp4")):
+        with pytest.raises(flce.FlceError):
+            flce.mx_sizes(cols, fmt)
+    # the binding's own arithmetic is the library's
+    for cols in (1, 31, 32, 33, 511, 512, 513, 4096, 10007):
+        for fmt, f in flce.MX_FORMATS.items():
+            assert flce._mx_row_bytes(cols, f) == flce.mx_sizes(cols, fmt)
+
+
+def test_empty_calls_touch_nothing():
+    assert norm_forward(M=0, x=None, y=None, mean=None, rstd=None) == 0
+    assert norm_backward(M=0, dy=None, x=None, dx=None, mean=None, rstd=None, ws=None, wsb=0, dw=None,
+                         db=None) == 0
+    assert status("flce_mx_quantize", None, 0, 32, 0, 32, 0, None, None, None) == 0
+    assert status("flce_mx_dequantize", None, None, 0, 0, 32, None, 0, 32, None) == 0
+
+
+def test_binding_refuses_host_tensors_and_wrong_types():
+    import torch
+    x = torch.zeros(2, 32)
+    with pytest.raises(ValueError):
+        flce.layer_norm_forward(x)
+    with pytest.raises(ValueError):
+        flce.mx_quantize(x, "mxfp4")
+    with pytest.raises(ValueError):
+        flce.mx_quantize(x, "int4")
