@@ -14,8 +14,8 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = ["flce_kernels.hip", "norm_kernels.hip", "mx_quant_kernels.hip", "flce_api.cpp",
-           "ops_api.cpp"]
+SOURCES = ["flce_kernels.hip", "norm_kernels.hip", "mx_quant_kernels.hip",
+           "mx_head_kernels.hip", "flce_api.cpp", "ops_api.cpp"]
 LIB = os.path.join(HERE, "libflce.so")
 ARCH = "gfx950"
 

@@ -13,6 +13,7 @@
 #include "flce.h"
 #include "api_util.h"
 #include "flce_internal.h"
+#include "ops_internal.h"
 
 namespace {
 thread_local char g_last_error[512] = "";
@@ -733,6 +734,172 @@ flce_status_t flce_forward_noalloc(const void* X, const void* W, const int64_t* 
   if (e != hipSuccess) return hip_fail(e, "device scratch address");
   return forward_waves(X, W, targets, M, H, V, ignore_index, scale, ent, logprob, lse, entropy,
                        static_cast<char*>(scratch), rows, stream);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The head with 4-bit weights.
+namespace {
+
+// Workspace of X's own MXFP4 copy: codes, then scales.
+size_t mx_x_codes_bytes(int64_t rows, int64_t H) {
+  return align_up(size_t(rows) * size_t(flce::mx_code_bytes(H, flce::kMxFp4)));
+}
+size_t mx_x_bytes(int64_t rows, int64_t H) {
+  return mx_x_codes_bytes(rows, H) + align_up(size_t(rows) * size_t(flce::mx_scale_bytes(H)));
+}
+
+// Bytes of a forward wave of `rows` rows: X's copy, then the partials.
+size_t mx_wave_bytes(int64_t rows, int64_t H, int64_t V, bool ent) {
+  return mx_x_bytes(rows, H) + fwd_layout(rows, V, ent).total;
+}
+
+// Tallest wave that fits in `bytes` (all M rows, or a multiple of 256); 0 if none does.
+int64_t mx_wave_rows(int64_t M, int64_t H, int64_t V, bool ent, size_t bytes) {
+  const int64_t cap = max_wave_rows(V);
+  if (M <= cap && mx_wave_bytes(M, H, V, ent) <= bytes) return M;
+  int64_t lo = 0, hi = (M < cap ? cdiv(M, kTile) : cap / kTile) + 1;  // lo fits (or 0), hi does not
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    if (mx_wave_bytes(mid * kTile, H, V, ent) <= bytes) lo = mid; else hi = mid;
+  }
+  return lo * kTile;
+}
+
+flce_status_t check_mx_call(const void* X, const void* W_codes, const void* W_scales, int64_t M,
+                            int64_t H, int64_t V, float scale) {
+  flce_status_t st = check_shape(M, H, V);
+  if (st != FLCE_OK) return st;
+  if (!std::isfinite(scale)) return fail(FLCE_ERR_INVALID_VALUE, "scale is not finite");
+  if (M == 0) return FLCE_OK;
+  if (!X || !W_codes || !W_scales)
+    return fail(FLCE_ERR_INVALID_VALUE, "NULL pointer among X, W_codes, W_scales");
+  if (!aligned(X, 16) || !aligned(W_codes, 16) || !aligned(W_scales, 16))
+    return fail(FLCE_ERR_UNSUPPORTED, "X, W_codes and W_scales must be 16-byte aligned");
+  return FLCE_OK;
+}
+
+// Quantise rows [r0, r0 + rows) of X to the workspace.
+hipError_t mx_quantize_x(const void* X, int64_t r0, int64_t rows, int64_t H, char* ws,
+                         flce::MxOperand* x, hipStream_t stream) {
+  uint8_t* codes = reinterpret_cast<uint8_t*>(ws);
+  uint8_t* scales = codes + mx_x_codes_bytes(rows, H);
+  *x = flce::MxOperand{codes, scales};
+  const flce::MxQuantArgs q{static_cast<const uint16_t*>(X) + r0 * H, long(H), nullptr, 0, codes,
+                            scales, long(rows), long(H)};
+  return flce::launch_mx_quantize(q, flce::kBf16, flce::kMxFp4, true, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+flce_status_t flce_mx_workspace_query(int64_t M, int64_t H, int64_t V, int compute_entropy,
+                                      size_t* logits_bytes, size_t* fwd_bytes) {
+  if (compute_entropy != 0 && compute_entropy != 1)
+    return fail(FLCE_ERR_INVALID_VALUE, "compute_entropy must be 0 or 1");
+  flce_status_t st = check_shape(M, H, V);
+  if (st != FLCE_OK) return st;
+  if (logits_bytes) *logits_bytes = mx_x_bytes(M, H);
+  if (fwd_bytes) {
+    const int64_t cap = max_wave_rows(V);
+    *fwd_bytes = mx_wave_bytes(M < cap ? M : cap, H, V, compute_entropy == 1);
+  }
+  return ok();
+}
+
+flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_scales, int64_t M,
+                             int64_t H, int64_t V, float scale, void* out, int out_dtype,
+                             int64_t ldo, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+  flce_status_t st = check_mx_call(X, W_codes, W_scales, M, H, V, scale);
+  if (st != FLCE_OK) return st;
+  if (out_dtype != FLCE_BF16 && out_dtype != FLCE_FP32)
+    return fail(FLCE_ERR_INVALID_VALUE, "unknown element type");
+  if (M == 0) return ok();
+  if (!out || !workspace) return fail(FLCE_ERR_INVALID_VALUE, "NULL pointer among out, workspace");
+  if (ldo < V)
+    return fail(FLCE_ERR_INVALID_VALUE, "out: row stride %lld is below its %lld columns",
+                (long long)ldo, (long long)V);
+  if (ldo > (int64_t(1) << 40))
+    return fail(FLCE_ERR_UNSUPPORTED, "out: row stride too large (limit 2^40)");
+  if (!aligned(out, out_dtype == FLCE_BF16 ? 2 : 4))
+    return fail(FLCE_ERR_UNSUPPORTED, "out must be naturally aligned");
+  if (!aligned(workspace, kAlign))
+    return fail(FLCE_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
+  if (workspace_bytes < mx_x_bytes(M, H))
+    return fail(FLCE_ERR_WORKSPACE_TOO_SMALL, "logits need %zu workspace bytes, got %zu",
+                mx_x_bytes(M, H), workspace_bytes);
+  flce::MxOperand x;
+  hipError_t e = mx_quantize_x(X, 0, M, H, static_cast<char*>(workspace), &x, stream);
+  if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
+  // one launch covers up to max_wave_rows(V) rows (the dispatch limit)
+  const int64_t rows = max_wave_rows(V);
+  for (int64_t r0 = 0; r0 < M; r0 += rows) {
+    flce::MxLogitsArgs a{};
+    a.x.codes = x.codes + r0 * flce::mx_code_bytes(H, flce::kMxFp4);
+    a.x.scales = x.scales + r0 * flce::mx_scale_bytes(H);
+    a.w = flce::MxOperand{static_cast<const uint8_t*>(W_codes), static_cast<const uint8_t*>(W_scales)};
+    a.M = int(M - r0 < rows ? M - r0 : rows);
+    a.H = int(H);
+    a.V = int(V);
+    a.scale = scale;
+    a.out = static_cast<char*>(out) + r0 * ldo * (out_dtype == FLCE_BF16 ? 2 : 4);
+    a.ldo = long(ldo);
+    a.out_dtype = out_dtype;
+    a.n_mt = int(cdiv(a.M, flce::kFwdTileM));
+    a.n_vt = int(cdiv(V, flce::kFwdTileN));
+    e = flce::launch_mx_logits(a, stream);
+    if (e != hipSuccess) return hip_fail(e, "4-bit logits kernel launch");
+  }
+  return ok();
+}
+
+flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_scales,
+                              const int64_t* targets, int64_t M, int64_t H, int64_t V,
+                              int64_t ignore_index, float scale, int compute_entropy,
+                              float* logprob, float* lse, float* entropy, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+  if (compute_entropy != 0 && compute_entropy != 1)
+    return fail(FLCE_ERR_INVALID_VALUE, "compute_entropy must be 0 or 1");
+  flce_status_t st = check_mx_call(X, W_codes, W_scales, M, H, V, scale);
+  if (st != FLCE_OK) return st;
+  if (M == 0) return ok();
+  if (!targets || !logprob || !lse || !workspace)
+    return fail(FLCE_ERR_INVALID_VALUE, "NULL pointer among targets, logprob, lse, workspace");
+  if (!aligned(targets, 8)) return fail(FLCE_ERR_UNSUPPORTED, "targets must be 8-byte aligned");
+  st = check_forward_outputs(compute_entropy, logprob, lse, entropy);
+  if (st != FLCE_OK) return st;
+  if (!aligned(workspace, kAlign))
+    return fail(FLCE_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
+  const bool ent = compute_entropy == 1;
+  const int64_t rows = mx_wave_rows(M, H, V, ent, workspace_bytes);
+  if (rows == 0)
+    return fail(FLCE_ERR_WORKSPACE_TOO_SMALL,
+                "4-bit forward needs at least %zu workspace bytes, got %zu",
+                mx_wave_bytes(M < kTile ? M : kTile, H, V, ent), workspace_bytes);
+  char* ws = static_cast<char*>(workspace);
+  for (int64_t r0 = 0; r0 < M; r0 += rows) {
+    const int64_t mw = M - r0 < rows ? M - r0 : rows;
+    const FwdLayout L = fwd_layout(mw, V, ent);
+    char* part = ws + mx_x_bytes(mw, H);
+    flce::MxFwdArgs a{};
+    a.w = flce::MxOperand{static_cast<const uint8_t*>(W_codes), static_cast<const uint8_t*>(W_scales)};
+    a.f = tile_args(nullptr, nullptr, targets + r0, mw, H, V, 0, ignore_index, scale, ent, L, part);
+    hipError_t e = mx_quantize_x(X, r0, mw, H, ws, &a.x, stream);
+    if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
+    e = flce::launch_mx_target_logit(a, stream);  // zeroes the queue counters
+    if (e != hipSuccess) return hip_fail(e, "4-bit target logit kernel launch");
+    e = flce::launch_mx_fwd_tile(a, ent, stream);
+    if (e != hipSuccess) return hip_fail(e, "4-bit forward kernel launch");
+    const flce::FwdMergeArgs b =
+        merge_args_single(targets + r0, mw, V, ignore_index, ent, logprob + r0, lse + r0,
+                          ent ? entropy + r0 : nullptr, L, part);
+    e = flce::launch_fwd_merge(b, ent, stream);
+    if (e != hipSuccess) return hip_fail(e, "forward merge kernel launch");
+  }
+  return ok();
 }
 
 }  // extern "C"

@@ -104,7 +104,7 @@ struct MxLogitsArgs {
   int out_dtype;
   int n_mt, n_vt;
 };
-hipError_t launch_mx_logits(const MxLogitsArgs& a, bool vec, hipStream_t s);
+hipError_t launch_mx_logits(const MxLogitsArgs& a, hipStream_t s);
 // Log-prob partials: f holds the outputs and sizes (f.X and f.W unused).
 struct MxFwdArgs {
   MxOperand x, w;

@@ -29,6 +29,7 @@ EXPORTS = ("flce_workspace_query", "flce_forward_workspace_min", "flce_forward_w
            "flce_nll_mean_grad", "flce_policy_loss_reduce", "flce_policy_loss_grad",
            "flce_mx_sizes", "flce_mx_quantize", "flce_mx_dequantize", "flce_layer_norm_forward",
            "flce_layer_norm_backward_workspace", "flce_layer_norm_backward",
+           "flce_mx_workspace_query", "flce_mx_logits", "flce_mx_forward",
            "flce_status_string",
            "flce_last_error_message", "flce_version")
 
@@ -89,7 +90,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.flce_layer_norm_backward_workspace.argtypes = [I64, I64, c.POINTER(SZ)]
     lib.flce_layer_norm_backward.argtypes = [P, I, I64, P, I, I64, I, P, P, P, I, P, P, I64, I64,
                                              P, I, I64, P, P, P, SZ, P]
-    for name in ("flce_mx_sizes", "flce_mx_quantize", "flce_mx_dequantize",
+    lib.flce_mx_workspace_query.argtypes = [I64, I64, I64, I, c.POINTER(SZ), c.POINTER(SZ)]
+    lib.flce_mx_logits.argtypes = [P, P, P, I64, I64, I64, c.c_float, P, I, I64, P, SZ, P]
+    lib.flce_mx_forward.argtypes = [P, P, P, P, I64, I64, I64, I64, c.c_float, I, P, P, P, P, SZ, P]
+    for name in ("flce_mx_workspace_query", "flce_mx_logits", "flce_mx_forward", "flce_mx_sizes", "flce_mx_quantize", "flce_mx_dequantize",
                  "flce_layer_norm_forward", "flce_layer_norm_backward_workspace",
                  "flce_layer_norm_backward", "flce_nll_reduce", "flce_nll_mean_grad", "flce_policy_loss_reduce",
                  "flce_policy_loss_grad", "flce_workspace_query",
@@ -733,3 +737,79 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx_dtype=None, need_para
             scales, _ptr(weight), pd, mean.data_ptr(), rstd.data_ptr(), m, h, dx.data_ptr(), dxd,
             lddx, _ptr(dw), _ptr(db), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dx, dw, db
+
+
+def mxfp4_workspace_query(M: int, H: int, V: int, compute_entropy: bool = True) -> Tuple[int, int]:
+    """Workspace bytes of (mxfp4_logits, mxfp4_forward with every row at once)."""
+    lo, fw = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().flce_mx_workspace_query(int(M), int(H), int(V), int(bool(compute_entropy)),
+                                          ctypes.byref(lo), ctypes.byref(fw)))
+    return lo.value, fw.value
+
+
+def _mx_head(X, W):
+    """Checks shared by the calls of the 4-bit head; returns (device, M, H, V)."""
+    import torch
+    dev = _on_gpu(X, "X")
+    if X.dtype != torch.bfloat16:
+        raise TypeError(f"X: expected torch.bfloat16, got {X.dtype}")
+    if X.dim() != 2 or not X.is_contiguous():
+        raise ValueError("X: expected a contiguous matrix")
+    if not isinstance(W, MXTensor) or W.fmt != "mxfp4":
+        raise ValueError('W: expected an MXTensor in format "mxfp4" (see mx_quantize)')
+    m, h = X.shape
+    v = W.codes.shape[0]
+    _mx_check(W, "W", dev, 0, v, h)
+    return dev, m, h, v
+
+
+def _workspace(workspace, nbytes, dev):
+    if workspace is None:
+        return alloc_workspace(nbytes, dev)
+    if workspace.device != dev:
+        raise ValueError(f"workspace: expected a tensor on {dev}, got {workspace.device}")
+    return workspace
+
+
+def mxfp4_logits(X, W: MXTensor, scale: float = 1.0, out_dtype=None, workspace=None, out=None):
+    """scale * Q(X) W^T [M, V] for a head W in MXFP4, as bf16 (the default) or fp32.
+
+    X [M, H] bf16 is rounded to MXFP4 on the way; sums are in fp32."""
+    import torch
+    dev, m, h, v = _mx_head(X, W)
+    if out is None:
+        out = torch.empty((m, v), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
+    od, ldo = _dtype_id(out, "out"), _rows(out, "out", dev, (m, v))
+    workspace = _workspace(workspace, mxfp4_workspace_query(m, h, v)[0] if workspace is None else 0, dev)
+    _launch(dev, load().flce_mx_logits, X.data_ptr(), W.codes.data_ptr(), W.scales.data_ptr(), m, h,
+            v, scale, out.data_ptr(), od, ldo, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return out
+
+
+def mxfp4_forward(X, W: MXTensor, targets, ignore_index: int = -100, scale: float = 1.0,
+                  compute_entropy: bool = True, workspace=None, out=None):
+    """forward() with a head in MXFP4: (logprob, lse, entropy-or-None) as fp32 [M] tensors.
+
+    X [M, H] bf16 is rounded to MXFP4 on the way.  Not differentiable."""
+    import torch
+    dev, m, h, v = _mx_head(X, W)
+    _vector(targets, "targets", dev, torch.int64, m)
+    if out is None:
+        logprob = torch.empty(m, dtype=torch.float32, device=dev)
+        lse = torch.empty(m, dtype=torch.float32, device=dev)
+        entropy = torch.empty(m, dtype=torch.float32, device=dev) if compute_entropy else None
+    else:
+        logprob, lse, entropy = out
+        for name, t in (("logprob", logprob), ("lse", lse), ("entropy", entropy)):
+            if t is not None:
+                _vector(t, name, dev, torch.float32, m)
+    ent = int(bool(compute_entropy))
+    workspace = _workspace(
+        workspace, mxfp4_workspace_query(m, h, v, ent)[1] if workspace is None else 0, dev)
+    _launch(dev, load().flce_mx_forward, X.data_ptr(), W.codes.data_ptr(), W.scales.data_ptr(),
+            targets.data_ptr(), m, h, v, ignore_index, scale, ent, logprob.data_ptr(), lse.data_ptr(),
+            _ptr(entropy), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return logprob, lse, entropy

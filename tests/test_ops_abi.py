@@ -120,3 +120,49 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         flce.mx_quantize(x, "mxfp4")
     with pytest.raises(ValueError):
         flce.mx_quantize(x, "int4")
+
+
+def logits(**kw):
+    a = dict(X=P, wc=P, ws=P, M=4, H=64, V=100, scale=1.0, out=P, od=0, ldo=100, work=P, wb=1 << 20)
+    a.update(kw)
+    return status("flce_mx_logits", *a.values(), None)
+
+
+def mx_forward(**kw):
+    a = dict(X=P, wc=P, ws=P, t=P, M=4, H=64, V=100, ignore=-100, scale=1.0, ent=1, lp=P, lse=P, en=P,
+             work=P, wb=1 << 24)
+    a.update(kw)
+    return status("flce_mx_forward", *a.values(), None)
+
+
+HEAD = [(INVALID, dict(M=-1)), (INVALID, dict(H=0)), (INVALID, dict(V=0)), (UNSUPPORTED, dict(H=60)),
+        (UNSUPPORTED, dict(M=(1 << 30) + 1)), (INVALID, dict(scale=float("inf"))),
+        (INVALID, dict(X=None)), (INVALID, dict(wc=None)), (INVALID, dict(ws=None)),
+        (UNSUPPORTED, dict(X=P + 8)), (UNSUPPORTED, dict(wc=P + 8)), (UNSUPPORTED, dict(ws=P + 4)),
+        (INVALID, dict(work=None)), (UNSUPPORTED, dict(work=P + 16)), (TOO_SMALL, dict(wb=100))]
+
+
+@pytest.mark.parametrize("want,kw", HEAD + [
+    (INVALID, dict(od=2)), (INVALID, dict(out=None)), (INVALID, dict(ldo=99)),
+    (UNSUPPORTED, dict(ldo=(1 << 40) + 1)), (UNSUPPORTED, dict(out=P + 1)),
+    (UNSUPPORTED, dict(od=1, out=P + 2))])
+def test_mx_logits(want, kw):
+    assert logits(**kw) == want
+
+
+@pytest.mark.parametrize("want,kw", HEAD + [
+    (INVALID, dict(ent=2)), (INVALID, dict(t=None)), (INVALID, dict(lp=None)), (INVALID, dict(lse=None)),
+    (INVALID, dict(en=None)), (UNSUPPORTED, dict(t=P + 4)), (UNSUPPORTED, dict(lse=P + 2))])
+def test_mx_forward(want, kw):
+    assert mx_forward(**kw) == want
+
+
+def test_mx_workspace():
+    # X's copy: 32 bytes of codes and 16 of scales a row, each part rounded up to 256
+    lo, fw = flce.mxfp4_workspace_query(4, 64, 100)
+    assert lo == 512
+    assert fw == 512 + flce.workspace_query(4, 64, 100, True)[0]
+    assert flce.mxfp4_workspace_query(0, 64, 100) == (0, 0)
+    assert mx_forward(wb=fw - 1) == TOO_SMALL and logits(wb=lo - 1) == TOO_SMALL
+    assert mx_forward(M=0, X=None, t=None, lp=None, lse=None, en=None, work=None, wb=0) == 0
+    assert logits(M=0, X=None, out=None, work=None, wb=0) == 0
