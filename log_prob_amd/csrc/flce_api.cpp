@@ -848,6 +848,7 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
     a.out = static_cast<char*>(out) + r0 * ldo * (out_dtype == FLCE_BF16 ? 2 : 4);
     a.ldo = long(ldo);
     a.out_dtype = out_dtype;
+    a.stream = M <= flce::kMxStreamTokens;
     a.n_mt = int(cdiv(a.M, flce::kFwdTileM));
     a.n_vt = int(cdiv(V, flce::kFwdTileN));
     e = flce::launch_mx_logits(a, stream);
@@ -887,6 +888,7 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
     flce::MxFwdArgs a{};
     a.w = flce::MxOperand{static_cast<const uint8_t*>(W_codes), static_cast<const uint8_t*>(W_scales)};
     a.f = tile_args(nullptr, nullptr, targets + r0, mw, H, V, 0, ignore_index, scale, ent, L, part);
+    a.stream = M <= flce::kMxStreamTokens;
     hipError_t e = mx_quantize_x(X, r0, mw, H, ws, &a.x, stream);
     if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
     e = flce::launch_mx_target_logit(a, stream);  // zeroes the queue counters

@@ -259,6 +259,297 @@ __global__ __launch_bounds__(64 * TL_ROWS) void mx_target_logit_kernel(MxFwdArgs
   if (lane == 0) p.zt[row] = s * p.scale;
 }
 
+// ---------------------------------------------------------------------------
+// Many tokens: 256 x 256 tiles, 4 waves of 128 x 128.
+//
+// The pipeline of the bf16 kernels, on code tiles: a step is 256 K, 128 bytes of codes a row
+// (the bytes of 64 bf16), two stages of 64 KiB in LDS filled by direct-to-LDS loads, half of
+// a step's loads issued right after the barrier that frees its stage and half under the next
+// sub-step, and each sub-step's fragments read while the one before it computes.  Scales come
+// 16 bytes of a row (two steps) at a time into two 8 KiB buffers of their own, and each lane
+// reads a dword of them (its four blocks of a step) per 32-row fragment.
+using MxShape = Shape<256, 256, 64, 2, 1>;   // BK in units of 2 bytes of codes
+constexpr int MX_SCALE_BYTES = 16 * 256;     // one operand's scales of two steps
+constexpr int MX_LDS = MxShape::PIPE_BYTES + 4 * MX_SCALE_BYTES;
+static_assert(MX_LDS <= 160 * 1024, "LDS");
+
+// One operand tile: codes and scales of its first row, rows that exist, bytes of a row.
+struct MxTile {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int valid;
+  int H;
+};
+
+// LDS byte offsets of a lane's fragments.  Row r = idx0 + 32 blk + l % 32 holds chunk c at
+// position c ^ kc_swz(r), and kc_swz changes by 4 from one 32-row block to the next, so a
+// block's parity and kk select one of 8 offsets and the rest is an immediate.
+struct MxFrag {
+  uint32_t code[2][4];
+  uint32_t scale;
+  __device__ __forceinline__ void init(int idx0, int lane, uint32_t region, uint32_t scale_region) {
+    const int r = idx0 + (lane & 31), half = lane >> 5;
+#pragma unroll
+    for (int par = 0; par < 2; ++par)
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        code[par][kk] = region + (uint32_t)(r * 128 + (((4 * half + kk) ^ kc_swz<8>(r) ^ (4 * par)) << 4));
+    scale = scale_region + (uint32_t)(16 * r + 4 * half);
+  }
+  __device__ __forceinline__ u32x4 read(const char* stage, int blk, int kk) const {
+    return *reinterpret_cast<const u32x4*>(stage + code[blk & 1][kk] + 4096 * blk);
+  }
+  // parity: which of the pair's two steps
+  __device__ __forceinline__ int read_scale(const char* pair, int blk, int parity) const {
+    return *reinterpret_cast<const int*>(pair + scale + 512 * blk + 8 * parity);
+  }
+};
+
+// Loads of an operand's scales: wave w brings rows 64 w .. + 63, a lane one row's 16 bytes.
+struct MxScaleDma {
+  i32x4 rsrc;
+  uint32_t voff, lds;
+  int pairs;
+  __device__ __forceinline__ void init(const MxTile& t, int wave, const char* lds0) {
+    const int row = 64 * wave + (int)(threadIdx.x & 63);
+    const uint32_t ld = (uint32_t)mx_scale_bytes(t.H);
+    rsrc = make_rsrc_fixed(t.scales);
+    voff = row < t.valid ? (uint32_t)row * ld : OOB_OFFSET;
+    lds = lds_addr_of(lds0) + (uint32_t)(1024 * wave);
+    pairs = (int)(ld / 16);
+  }
+  // steps 2 pair and 2 pair + 1 into buffer `pair % 2`; a pair past the end is all zeros
+  __device__ __forceinline__ void issue(int pair) const {
+    const bool live = pair < pairs;
+    dma16<0>(rsrc, live ? voff : OOB_OFFSET, live ? 16u * (uint32_t)pair : 0u,
+             lds + (uint32_t)((pair & 1) * 2 * MX_SCALE_BYTES));
+  }
+};
+
+struct MxRegs {
+  u32x4 a[2][4], b[2][4];  // fragments of sub-steps of either parity
+  int sa[2][4], sb[2][4];  // scales of steps of either parity
+};
+
+// Group g of 16 of sub-step kk: one MFMA, every other group a fragment read of the next
+// sub-step (RKK, of the stage at ra / rb), and a share of the loads [JB, JE).
+template <int kk, int RKK, int STG, int g, int JB, int JE, class Ops>
+__device__ __forceinline__ void mx_group(f32x16 (&acc)[4][4], MxRegs& r, const char* ra,
+                                         const char* rb, const MxFrag& fa, const MxFrag& fb, Ops& dma) {
+  constexpr int cur = kk & 1, nxt = cur ^ 1, mb = g / 4, nb = g % 4, D = JE - JB;
+  if constexpr (g % 2 == 0) {
+    constexpr int i = g / 2;
+    if constexpr (i < 4) r.a[nxt][i] = fa.read(ra, i, RKK);
+    else r.b[nxt][i - 4] = fb.read(rb, i - 4, RKK);
+  }
+  acc[mb][nb] = mx_mfma<kk>(r.a[cur][mb], r.b[cur][nb], acc[mb][nb], r.sa[STG][mb], r.sb[STG][nb]);
+  if constexpr (g % 2 == 0) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+  if constexpr (D > 0) {
+    __builtin_amdgcn_sched_barrier(0);
+    dma.issue(JB + g * D / 16, JB + (g + 1) * D / 16);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+template <int kk, int RKK, int STG, int JB, int JE, class Ops, int... G>
+__device__ __forceinline__ void mx_substep(f32x16 (&acc)[4][4], MxRegs& r, const char* ra,
+                                           const char* rb, const MxFrag& fa, const MxFrag& fb,
+                                           Ops& dma, std::integer_sequence<int, G...>) {
+  (mx_group<kk, RKK, STG, G, JB, JE>(acc, r, ra, rb, fa, fb, dma), ...);
+}
+
+// acc[mb][nb] = the 32 x 32 block (32 mb, 32 nb) of the wave's 128 x 128 of A B^T.
+__device__ __forceinline__ void mx_mainloop(f32x16 (&acc)[4][4], char* smem, const MxTile& A,
+                                            const MxTile& B) {
+  using S = MxShape;
+  constexpr int D = S::DMA_STAGE, EARLY = D / 2;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[mb][nb][e] = 0.f;
+  const int K = (int)(mx_code_bytes(A.H, kMxFp4) / 2);  // in 2-byte units
+  const int nk = (K + S::BK - 1) / S::BK, nfull = K / S::BK;
+  const TileSrc sa{reinterpret_cast<const uint16_t*>(A.codes), K, A.valid, K, 0};
+  const TileSrc sb{reinterpret_cast<const uint16_t*>(B.codes), K, B.valid, K, 0};
+  typename StageDma<S, true, true>::PA plan_a;
+  typename StageDma<S, true, true>::PB plan_b;
+  plan_a.init(sa, wave);
+  plan_b.init(sb, wave);
+  char* scale_lds = smem + S::PIPE_BYTES;  // buffers of a pair: A's rows, then B's
+  MxScaleDma da, db;
+  da.init(A, wave, scale_lds);
+  db.init(B, wave, scale_lds + MX_SCALE_BYTES);
+  MxFrag fa, fb;
+  fa.init((wave / 2) * 128, lane, 0u, 0u);
+  fb.init((wave % 2) * 128, lane, 2u * S::A_BYTES, (uint32_t)MX_SCALE_BYTES);
+  auto stage_dma = [&](auto fast, int st, int s) {
+    constexpr bool FAST = decltype(fast)::value;
+    StageDma<S, true, true, FAST, true> d;
+    d.pa = &plan_a;
+    d.pb = &plan_b;
+    const bool active = st < nk;
+    const int k0 = (active ? st : 0) * S::BK;
+    d.a = tile_dma<FAST>(sa, plan_a, k0, active, smem + s * S::A_BYTES);
+    d.b = tile_dma<FAST>(sb, plan_b, k0, active, smem + 2 * S::A_BYTES + s * S::B_BYTES);
+    return d;
+  };
+  using Slow = std::integral_constant<bool, false>;
+  using Fast = std::integral_constant<bool, true>;
+  using Stage0 = std::integral_constant<int, 0>;
+  using Stage1 = std::integral_constant<int, 1>;
+  MxRegs r;
+  auto read_scales = [&](int st, int set) {
+    const char* pair = scale_lds + ((st >> 1) & 1) * 2 * MX_SCALE_BYTES;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.sa[set][i] = fa.read_scale(pair, i, set);
+      r.sb[set][i] = fb.read_scale(pair, i, set);
+    }
+  };
+  // prologue: the first pair's scales, step 0, and the early loads of step 1
+  da.issue(0);
+  db.issue(0);
+  stage_dma(Slow(), 0, 0).issue(0, D);
+  stage_dma(Slow(), 1, 1).issue(0, EARLY);
+  wait_vmcnt<EARLY>();
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.a[0][i] = fa.read(smem, i, 0);
+    r.b[0][i] = fb.read(smem, i, 0);
+  }
+  read_scales(0, 0);
+  constexpr auto groups = std::make_integer_sequence<int, 16>();
+  auto step = [&](auto stg, auto fast, int kt) {
+    constexpr int STG = decltype(stg)::value;
+    const char* ca = smem + STG * S::A_BYTES;
+    const char* cb = smem + STG * S::B_BYTES;
+    const char* na = smem + (1 - STG) * S::A_BYTES;
+    const char* nb = smem + (1 - STG) * S::B_BYTES;
+    {
+      auto dma = stage_dma(fast, kt + 1, 1 - STG);
+      mx_substep<0, 1, STG, EARLY, D>(acc, r, ca, cb, fa, fb, dma, groups);
+      mx_substep<1, 2, STG, 0, 0>(acc, r, ca, cb, fa, fb, dma, groups);
+      mx_substep<2, 3, STG, 0, 0>(acc, r, ca, cb, fa, fb, dma, groups);
+    }
+    // keep the barrier after every MFMA issued so far (the compiler would hoist it)
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<0>();
+    __syncthreads();
+    // the stage of step kt is free: it receives step kt + 2, and after an even step the pair
+    // buffer that held steps kt - 2 and kt - 1 receives the scales of kt + 2 and kt + 3
+    {
+      if constexpr (STG == 0) {
+        da.issue((kt >> 1) + 1);
+        db.issue((kt >> 1) + 1);
+      }
+      read_scales(kt + 1, 1 - STG);
+      __builtin_amdgcn_sched_barrier(0);
+      auto dma = stage_dma(fast, kt + 2, STG);
+      mx_substep<3, 0, STG, 0, EARLY>(acc, r, na, nb, fa, fb, dma, groups);
+    }
+  };
+  int kt = 0;
+  for (; kt + 3 < nfull; kt += 2) {
+    step(Stage0(), Fast(), kt);
+    step(Stage1(), Fast(), kt + 1);
+  }
+  for (; kt < nk; kt += 2) {
+    step(Stage0(), Slow(), kt);
+    step(Stage1(), Slow(), kt + 1);
+  }
+  // the zero fills issued under the last steps must land before the caller reuses LDS
+  wait_vmcnt<0>();
+  __syncthreads();
+}
+
+// The tile of vocabulary rows (A) and tokens (B) of a workgroup.
+__device__ __forceinline__ void mx_tile_product(f32x16 (&acc)[4][4], char* smem, const MxOperand& x,
+                                                const MxOperand& w, int M, int H, int V, int mt, int vt) {
+  const long code_ld = mx_code_bytes(H, kMxFp4), scale_ld = mx_scale_bytes(H);
+  const int row0 = mt * 256, col0 = vt * 256;
+  const MxTile A{w.codes + col0 * code_ld, w.scales + col0 * scale_ld, V - col0, H};
+  const MxTile B{x.codes + row0 * code_ld, x.scales + row0 * scale_ld, M - row0, H};
+  mx_mainloop(acc, smem, A, B);
+}
+
+template <bool ENT>
+__global__ __launch_bounds__(256, 1) void mx_tile_fwd_kernel(MxFwdArgs a) {
+  __shared__ __attribute__((aligned(1024))) char smem[MX_LDS];
+  const int L = tile_claim(a.f.n_mt * a.f.n_vt, a.f.tq);
+  if (L < 0) return;
+  int mt, vt;
+  group_coords(L, a.f.n_mt, a.f.n_vt, FWD_GROUP_M, mt, vt);
+  f32x16 acc[4][4];
+  mx_tile_product(acc, smem, a.x, a.w, a.f.M, a.f.H, a.f.V, mt, vt);
+  fwd_epilogue<MxShape, ENT>(acc, smem, a.f, mt, vt);
+}
+
+// Logits of a tile: a lane holds 4 consecutive vocabulary entries of a token at a time.  Each
+// wave turns its 128 x 128 block around in a 16 KiB slice of its own, 32 tokens at a time (no
+// workgroup barrier): rows of 128 entries, 16-byte chunks swizzled by token, then whole rows
+// to memory, 16 bytes a lane where the output allows it and element by element otherwise.
+template <class T, bool VEC>
+__global__ __launch_bounds__(256, 1) void mx_tile_logits_kernel(MxLogitsArgs p) {
+  __shared__ __attribute__((aligned(1024))) char smem[MX_LDS];
+  int mt, vt;
+  tile_coords((int)blockIdx.x, p.n_mt * p.n_vt, p.n_mt, p.n_vt, FWD_GROUP_M, mt, vt);
+  f32x16 acc[4][4];
+  mx_tile_product(acc, smem, p.x, p.w, p.M, p.H, p.V, mt, vt);
+  constexpr int ES = (int)sizeof(typename T::mem), RB = 128 * ES, CH = RB / 16;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lc = lane & 31, half = lane >> 5;
+  const int v0 = vt * 256 + (wave / 2) * 128, t0 = mt * 256 + (wave % 2) * 128;
+  char* slice = smem + wave * 16384;
+  typename T::mem* out = static_cast<typename T::mem*>(p.out);
+#pragma unroll
+  for (int nb = 0; nb < 4; ++nb) {
+#pragma unroll
+    for (int mb = 0; mb < 4; ++mb)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // entries 32 mb + 8 q + 4 half .. + 3 of token lc
+        float d[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = p.scale * acc[mb][nb][4 * q + i];
+        if constexpr (ES == 4) {
+          const int c = 8 * mb + 2 * q + half;
+          *reinterpret_cast<f32x4_t*>(slice + lc * RB + ((c ^ lc) << 4)) = f32x4_t{d[0], d[1], d[2], d[3]};
+        } else {
+          const int c = 4 * mb + q;
+          *reinterpret_cast<u32x2*>(slice + lc * RB + ((c ^ (lc & 15)) << 4) + 8 * half) =
+              u32x2{pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3])};
+        }
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if constexpr (VEC) {
+      constexpr int RPI = 64 / CH;  // rows an instruction
+#pragma unroll
+      for (int it = 0; it < 32 / RPI; ++it) {
+        const int r = it * RPI + lane / CH, c = lane % CH;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(slice + r * RB + ((c ^ (r & (CH - 1))) << 4));
+        const int t = t0 + 32 * nb + r, col = v0 + c * (16 / ES);
+        if (t < p.M && col < p.V) *reinterpret_cast<u32x4*>(out + (long)t * p.ldo + col) = v;
+      }
+    } else {
+      for (int it = 0; it < 64; ++it) {
+        const int r = it / 2, i = 64 * (it & 1) + lane;
+        const typename T::mem v = *reinterpret_cast<const typename T::mem*>(
+            slice + r * RB + (((i * ES / 16) ^ (r & (CH - 1))) << 4) + i * ES % 16);
+        const int t = t0 + 32 * nb + r, col = v0 + i;
+        if (t < p.M && col < p.V) out[(long)t * p.ldo + col] = v;
+      }
+    }
+    // the slice's reads have returned before the next 32 tokens overwrite it
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+}
+
 template <class T>
 void stream_logits(const MxLogitsArgs& a, hipStream_t s) {
   const int tb = a.M <= 32 ? 1 : a.M <= 64 ? 2 : 4;
@@ -279,17 +570,49 @@ void stream_fwd(const MxFwdArgs& a, hipStream_t s) {
   else mx_stream_fwd_kernel<4, ENT><<<g, n, 0, s>>>(a);
 }
 
+// Whole 16-byte stores: rows and columns in multiples of them.
+template <class T>
+void tile_logits(const MxLogitsArgs& a, hipStream_t s) {
+  constexpr int E = 16 / (int)sizeof(typename T::mem);
+  const bool vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.ldo % E == 0 && a.V % E == 0;
+  const unsigned g = (unsigned)((int64_t)a.n_mt * a.n_vt);
+  if (vec) mx_tile_logits_kernel<T, true><<<g, 256, 0, s>>>(a);
+  else mx_tile_logits_kernel<T, false><<<g, 256, 0, s>>>(a);
+}
+
+template <bool ENT>
+void tile_fwd(const MxFwdArgs& a, hipStream_t s) {
+  MxFwdArgs b = a;
+  const int64_t n = (int64_t)a.f.n_mt * a.f.n_vt;
+  const QueueShape qs = queue_shape(n);
+  b.f.tq.clear = nullptr;
+  b.f.tq.queue = qs.queue;
+  mx_tile_fwd_kernel<ENT><<<(unsigned)(n + qs.spare), 256, 0, s>>>(b);
+}
+
 }  // namespace
 
 hipError_t launch_mx_logits(const MxLogitsArgs& a, hipStream_t s) {
-  if (a.out_dtype == kBf16) stream_logits<Bf16>(a, s);
-  else stream_logits<F32>(a, s);
+  if (a.stream) {
+    if (a.out_dtype == kBf16) stream_logits<Bf16>(a, s);
+    else stream_logits<F32>(a, s);
+  } else if (a.out_dtype == kBf16) {
+    tile_logits<Bf16>(a, s);
+  } else {
+    tile_logits<F32>(a, s);
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_mx_fwd_tile(const MxFwdArgs& a, bool entropy, hipStream_t s) {
-  if (entropy) stream_fwd<true>(a, s);
-  else stream_fwd<false>(a, s);
+  if (a.stream) {
+    if (entropy) stream_fwd<true>(a, s);
+    else stream_fwd<false>(a, s);
+  } else if (entropy) {
+    tile_fwd<true>(a, s);
+  } else {
+    tile_fwd<false>(a, s);
+  }
   return hipGetLastError();
 }
 

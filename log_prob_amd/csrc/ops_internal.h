@@ -90,7 +90,9 @@ struct MxQuantArgs {
 hipError_t launch_mx_quantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s);
 
-// The head with 4-bit weights: X and W as MXFP4 codes and scales.
+// The head with 4-bit weights: X and W as MXFP4 codes and scales.  Calls of at most
+// kMxStreamTokens tokens run the kernels that stream W through registers.
+constexpr int64_t kMxStreamTokens = 128;
 struct MxOperand {
   const uint8_t* codes;
   const uint8_t* scales;
@@ -103,12 +105,15 @@ struct MxLogitsArgs {
   long ldo;
   int out_dtype;
   int n_mt, n_vt;
+  bool stream;
 };
 hipError_t launch_mx_logits(const MxLogitsArgs& a, hipStream_t s);
 // Log-prob partials: f holds the outputs and sizes (f.X and f.W unused).
 struct MxFwdArgs {
   MxOperand x, w;
   FwdTileArgs f;
+  bool stream;             // the kernel for few tokens: chosen for the whole call, so that a
+                           // token wave does not change its rows' bits
 };
 hipError_t launch_mx_fwd_tile(const MxFwdArgs& a, bool entropy, hipStream_t s);
 hipError_t launch_mx_target_logit(const MxFwdArgs& a, hipStream_t s);
