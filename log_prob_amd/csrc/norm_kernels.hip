@@ -107,8 +107,8 @@ __device__ __forceinline__ void save8(const float (&v)[8], int col, uint8_t* cod
 
 // Rows of H <= 8 NT CH elements, NT threads a row.
 template <class TX, class TY, int NT, int CH, bool VEC>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_fwd_kernel(NormFwdArgs p) {
-  constexpr int THREADS = NT < 256 ? 256 : NT, ROWS = THREADS / NT;
+__global__ __launch_bounds__(NT == 64 ? 256 : NT) void norm_fwd_kernel(NormFwdArgs p) {
+  constexpr int ROWS = NT == 64 ? 4 : 1;  // a row of its own for a wave; no barrier then
   __shared__ float red[4 * (NT / 64)];
   const int t = threadIdx.x % NT, H = p.H;
   RowSum<NT> sum{red};
@@ -175,34 +175,72 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_fwd_kernel(NormFwdAr
   }
 }
 
+// Eight elements of a row as they come from memory, so that a row can be fetched while the
+// one before it is worked on at few registers' cost; value() makes floats of them.
+template <class T, bool VEC>
+struct Chunk {
+  float v[8];
+  __device__ __forceinline__ void load(const typename T::mem* row, int col, int H) {
+    load8<T, VEC>(row, col, H, v);
+  }
+  __device__ __forceinline__ void value(float (&o)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = v[i];
+  }
+};
+template <>
+struct Chunk<Bf16, true> {
+  u32x4_t u;
+  __device__ __forceinline__ void load(const uint16_t* row, int col, int H) {
+    u = u32x4_t{0u, 0u, 0u, 0u};
+    if (col < H) u = *reinterpret_cast<const u32x4_t*>(row + col);
+  }
+  __device__ __forceinline__ void value(float (&o)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = bf16_lo(u[i]);
+      o[2 * i + 1] = bf16_hi(u[i]);
+    }
+  }
+};
+
 // The backward's view of the input: a matrix of T, or its 8-bit checkpoint.
 struct Saved {};
 template <class TX, bool VEC>
-__device__ __forceinline__ void load_x(const NormBwdArgs& p, long row, int col, float (&v)[8]) {
-  if constexpr (__is_same(TX, Saved)) {
-    const long code_ld = mx_code_bytes(p.H, kMxFp8), scale_ld = mx_scale_bytes(p.H);
-    if (col < code_ld) {
-      const u32x2_t r = *reinterpret_cast<const u32x2_t*>(p.codes + row * code_ld + col);
-      const uint32_t byte = p.scales[row * scale_ld + (col >> 5)];
-      if (p.fmt == kMxFp8)
-        mx_decode<kMxFp8>(r, byte, v);
-      else
-        mx_decode<kMxInt8>(r, byte, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
-  } else {
-    load8<TX, VEC>(static_cast<const typename TX::mem*>(p.x) + row * p.ldx, col, p.H, v);
+struct Input {
+  Chunk<TX, VEC> c;
+  __device__ __forceinline__ void load(const NormBwdArgs& p, long row, int col) {
+    c.load(static_cast<const typename TX::mem*>(p.x) + row * p.ldx, col, p.H);
   }
-}
+  __device__ __forceinline__ void value(const NormBwdArgs&, float (&o)[8]) const { c.value(o); }
+};
+template <bool VEC>
+struct Input<Saved, VEC> {
+  u32x2_t r;
+  uint32_t byte;
+  __device__ __forceinline__ void load(const NormBwdArgs& p, long row, int col) {
+    const long code_ld = mx_code_bytes(p.H, kMxFp8), scale_ld = mx_scale_bytes(p.H);
+    r = u32x2_t{0u, 0u};
+    byte = 0u;
+    if (col < code_ld) {
+      r = *reinterpret_cast<const u32x2_t*>(p.codes + row * code_ld + col);
+      byte = p.scales[row * scale_ld + (col >> 5)];
+    }
+  }
+  __device__ __forceinline__ void value(const NormBwdArgs& p, float (&o)[8]) const {
+    if (p.fmt == kMxFp8)
+      mx_decode<kMxFp8>(r, byte, o);
+    else
+      mx_decode<kMxInt8>(r, byte, o);
+  }
+};
 
-// Rows of H <= 8 NT CH elements; group g of the launch takes rows g, g + groups, ... and
-// leaves the column sums of its rows.  Rows that share a workgroup (NT = 64) join their sums
-// in LDS first, in order.
+// Rows of H <= 8 NT CH elements; group g of the launch takes rows g, g + groups, ..., with
+// the next row's loads in flight under the work on this one, and leaves the column sums of
+// its rows.  Rows that share a workgroup (NT = 64) join their sums in LDS first, in order.
 template <class TX, class TY, class TD, int NT, int CH, bool VEC>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_bwd_kernel(NormBwdArgs p) {
-  constexpr int THREADS = NT < 256 ? 256 : NT, ROWS = THREADS / NT;
+__global__ __launch_bounds__(NT == 64 ? 256 : NT) void norm_bwd_kernel(NormBwdArgs p) {
+  constexpr int ROWS = NT == 64 ? 4 : 1;  // a row of its own for a wave; no barrier then
   __shared__ float red[4 * (NT / 64)];
   __shared__ float join[ROWS > 1 ? 16 * NT * CH : 1];
   const int t = threadIdx.x % NT, slot = threadIdx.x / NT, H = p.H;
@@ -215,15 +253,34 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_bwd_kernel(NormBwdAr
     for (int i = 0; i < 8; ++i) dw[c][i] = db[c][i] = 0.f;
   }
   const float rh = 1.f / (float)H;
-  for (long row = (long)blockIdx.x * ROWS + slot; row < p.M; row += (long)gridDim.x * ROWS) {
-    const typename TY::mem* dy = static_cast<const typename TY::mem*>(p.dy) + row * p.lddy;
-    const float mean = p.mean[row], rstd = p.rstd[row];
+  struct Row {
+    Input<TX, VEC> x[CH];
+    Chunk<TY, VEC> dy[CH];
+    float mean, rstd;
+    __device__ __forceinline__ void load(const NormBwdArgs& p, long row, int t) {
+      const typename TY::mem* dyr = static_cast<const typename TY::mem*>(p.dy) + row * p.lddy;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        x[c].load(p, row, 8 * (t + NT * c));
+        dy[c].load(dyr, 8 * (t + NT * c), p.H);
+      }
+      mean = p.mean[row];
+      rstd = p.rstd[row];
+    }
+  } next;
+  const long step = (long)gridDim.x * ROWS;
+  long row = (long)blockIdx.x * ROWS + slot;
+  if (row < p.M) next.load(p, row, t);
+  for (; row < p.M; row += step) {
+    const Row cur = next;
+    if (row + step < p.M) next.load(p, row + step, t);
+    const float mean = cur.mean, rstd = cur.rstd;
     float x[CH][8], g[CH][8];
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      load_x<TX, VEC>(p, row, 8 * (t + NT * c), x[c]);
-      load8<TY, VEC>(dy, 8 * (t + NT * c), H, g[c]);
+      cur.x[c].value(p, x[c]);
+      cur.dy[c].value(g[c]);
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -359,7 +416,9 @@ __global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormBwdArgs p) {
     float s[2] = {0.f, 0.f};
     float x[8], g[8], w[8], a[8], b[8];
     for (int col = 8 * t; col < H; col += 8 * WIDE) {
-      load_x<TX, VEC>(p, row, col, x);
+      Input<TX, VEC> in;
+      in.load(p, row, col);
+      in.value(p, x);
       load8<TY, VEC>(dy, col, H, g);
       load_param<VEC>(p.weight, p.param_dtype, col, H, 1.f, w);
       if (first) {
@@ -385,7 +444,9 @@ __global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormBwdArgs p) {
     sum(s);
     const float m0 = s[0] * rh, m1 = s[1] * rh;
     for (int col = 8 * t; col < H; col += 8 * WIDE) {
-      load_x<TX, VEC>(p, row, col, x);
+      Input<TX, VEC> in;
+      in.load(p, row, col);
+      in.value(p, x);
       load8<TY, VEC>(dy, col, H, g);
       load_param<VEC>(p.weight, p.param_dtype, col, H, 1.f, w);
 #pragma unroll
@@ -396,8 +457,9 @@ __global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormBwdArgs p) {
 }
 
 // dweight and dbias: the sum of the groups' partial rows, in a fixed order.  A workgroup
-// takes 64 columns; its 16 waves share the groups and meet in LDS.
-constexpr int REDUCE_COLS = 64, REDUCE_SLICES = 16;
+// takes 16 columns (64-byte pieces of the partial rows, so that a few thousand columns fill
+// the chip); 64 slices of threads share the groups and meet in LDS.
+constexpr int REDUCE_COLS = 16, REDUCE_SLICES = 64;
 __global__ __launch_bounds__(REDUCE_COLS * REDUCE_SLICES) void norm_reduce_kernel(NormReduceArgs p) {
   __shared__ float part[REDUCE_SLICES][REDUCE_COLS];
   const int lane = threadIdx.x % REDUCE_COLS, slice = threadIdx.x / REDUCE_COLS;
@@ -409,14 +471,19 @@ __global__ __launch_bounds__(REDUCE_COLS * REDUCE_SLICES) void norm_reduce_kerne
   const float* src = p.part + (bias ? (long)p.groups * p.H : 0) + col;
   float s = 0.f;
   if (col < p.H) {
-#pragma unroll 4
+#pragma unroll 8
     for (int g = slice; g < p.groups; g += REDUCE_SLICES) s += src[(long)g * p.H];
   }
   part[slice][lane] = s;
   __syncthreads();
-  if (slice != 0 || col >= p.H) return;
+  // halves of the slices onto one another, in a fixed order
 #pragma unroll
-  for (int k = 1; k < REDUCE_SLICES; ++k) s += part[k][lane];
+  for (int n = REDUCE_SLICES / 2; n > 0; n /= 2) {
+    if (slice < n) part[slice][lane] += part[slice + n][lane];
+    __syncthreads();
+  }
+  if (slice != 0 || col >= p.H) return;
+  s = part[0][lane];
   if (p.param_dtype == kF32)
     static_cast<float*>(out)[col] = s;
   else
@@ -425,6 +492,13 @@ __global__ __launch_bounds__(REDUCE_COLS * REDUCE_SLICES) void norm_reduce_kerne
 
 constexpr int kComputeUnits = 256;
 
+// A row takes as many threads as it has chunks where that is at most 1024: one chunk a
+// thread keeps the registers few and the waves in flight many (32767 x 2048 bf16 forward:
+// 49 us with 256 threads of one chunk a row, 78 us with a wave of four).  Past 4096 elements
+// the forward gives a thread two (8192 x 8192: 59 us against 75 us with 1024 threads, whose
+// barriers span 16 waves); the backward, with its column sums in registers, does not (88 us
+// against 119 us before its loads ran ahead), but keeps rows of up to 1024 in a wave, without
+// a barrier (65535 x 1024: 79 us against 85 us).  Workgroups stay and walk the rows, so the parameters are read once each.
 template <class TX, class TY, bool VEC>
 void fwd_rows(const NormFwdArgs& a, hipStream_t s) {
   auto grid = [&](int rows_per_group, int groups_per_unit) {
@@ -433,13 +507,13 @@ void fwd_rows(const NormFwdArgs& a, hipStream_t s) {
     return (unsigned)(need < most ? need : most);
   };
   if (a.H <= 512)
-    norm_fwd_kernel<TX, TY, 64, 1, VEC><<<grid(4, 8), 256, 0, s>>>(a);
+    norm_fwd_kernel<TX, TY, 64, 1, VEC><<<grid(4, 16), 256, 0, s>>>(a);
   else if (a.H <= 1024)
-    norm_fwd_kernel<TX, TY, 64, 2, VEC><<<grid(4, 8), 256, 0, s>>>(a);
+    norm_fwd_kernel<TX, TY, 128, 1, VEC><<<grid(1, 32), 128, 0, s>>>(a);
   else if (a.H <= 2048)
-    norm_fwd_kernel<TX, TY, 64, 4, VEC><<<grid(4, 4), 256, 0, s>>>(a);
+    norm_fwd_kernel<TX, TY, 256, 1, VEC><<<grid(1, 16), 256, 0, s>>>(a);
   else if (a.H <= 4096)
-    norm_fwd_kernel<TX, TY, 256, 2, VEC><<<grid(1, 8), 256, 0, s>>>(a);
+    norm_fwd_kernel<TX, TY, 512, 1, VEC><<<grid(1, 8), 512, 0, s>>>(a);
   else if (a.H <= 8192)
     norm_fwd_kernel<TX, TY, 512, 2, VEC><<<grid(1, 4), 512, 0, s>>>(a);
   else if (a.H <= 16384)
@@ -458,9 +532,9 @@ void bwd_rows(const NormBwdArgs& a, hipStream_t s) {
   else if (a.H <= 2048)
     norm_bwd_kernel<TX, TY, TD, 256, 1, VEC><<<g, 256, 0, s>>>(a);
   else if (a.H <= 4096)
-    norm_bwd_kernel<TX, TY, TD, 256, 2, VEC><<<g, 256, 0, s>>>(a);
+    norm_bwd_kernel<TX, TY, TD, 512, 1, VEC><<<g, 512, 0, s>>>(a);
   else if (a.H <= 8192)
-    norm_bwd_kernel<TX, TY, TD, 512, 2, VEC><<<g, 512, 0, s>>>(a);
+    norm_bwd_kernel<TX, TY, TD, 1024, 1, VEC><<<g, 1024, 0, s>>>(a);
   else
     norm_bwd_wide_kernel<TX, TY, TD, VEC><<<g, WIDE, 0, s>>>(a);
 }
@@ -478,11 +552,17 @@ void fwd_vec(const NormFwdArgs& a, bool vec, hipStream_t s) {
 
 }  // namespace
 
+// Workgroups of the backward's row kernel.  Each leaves two rows of partial sums, and the next
+// row's loads in flight keep memory busy with few of them (us with 1, 2, 3, 4 a compute unit:
+// 65535 x 1024 77, 78, -, 88; 32767 x 2048 110, 77, 79, 84, and from the checkpoint 111, 74,
+// 67, 70; 16384 x 4096 77, 82, 91; 8192 x 8192 84, 91).  Past one a unit each has 16 turns.
 int norm_bwd_groups(long M, int H) {
-  const int rows = H <= 1024 ? 4 : 1;
-  const int per_unit = H <= 1024 ? 4 : H <= 2048 ? 4 : H <= 4096 ? 2 : 1;
-  const long need = (M + rows - 1) / rows, most = (long)kComputeUnits * per_unit;
-  return (int)(need < most ? need : most);
+  const long rows = H <= 1024 ? 4 : 1;
+  const long most = kComputeUnits * (H <= 512 ? 2 : H <= 1024 ? 1 : H <= 2048 ? 3 : 1);
+  const long need = (M + rows - 1) / rows;
+  const long shared = need / 16 > kComputeUnits ? need / 16 : kComputeUnits;
+  const long g = need < shared ? need : shared;
+  return (int)(g < most ? g : most);
 }
 
 hipError_t launch_norm_fwd(const NormFwdArgs& a, int x_dtype, int y_dtype, bool vec, hipStream_t s) {

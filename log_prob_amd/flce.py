@@ -7,6 +7,7 @@ If the library is missing, loading fails loudly; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Any, NamedTuple, Optional, Tuple
 
@@ -522,7 +523,7 @@ def _rows(t, name, dev, shape=None):
 
 
 def _on_gpu(t, name):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: expected a GPU tensor")
     return t.device
 
@@ -539,12 +540,15 @@ def _vector(t, name, dev, dtype, n):
 def _launch(dev, fn, *args):
     """Call fn(*args, stream) with dev's current stream, on dev."""
     import torch
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        _check(fn(*args, stream))
+    # the handle of torch.cuda.current_stream(dev), without making a Stream object: 1.8 us
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if torch._C._cuda_getDevice() == dev.index:
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, stream))
+            status = fn(*args, stream)
+    if status != FLCE_OK:
+        _check(status)
 
 
 def _mx_format(fmt, allowed=tuple(MX_FORMATS)) -> int:
@@ -674,7 +678,9 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out_dtype=N
     return (y, mean, rstd) if kept is None else (y, mean, rstd, kept)
 
 
+@functools.lru_cache(maxsize=256)
 def layer_norm_backward_workspace(M: int, H: int) -> int:
+    """Workspace bytes of layer_norm_backward."""
     b = ctypes.c_size_t()
     _check(load().flce_layer_norm_backward_workspace(int(M), int(H), ctypes.byref(b)))
     return b.value
@@ -739,6 +745,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx_dtype=None, need_para
     return dx, dw, db
 
 
+@functools.lru_cache(maxsize=256)
 def mxfp4_workspace_query(M: int, H: int, V: int, compute_entropy: bool = True) -> Tuple[int, int]:
     """Workspace bytes of (mxfp4_logits, mxfp4_forward with every row at once)."""
     lo, fw = ctypes.c_size_t(), ctypes.c_size_t()
