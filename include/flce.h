@@ -451,8 +451,9 @@ flce_status_t flce_layer_norm_backward(const void* dy, int dy_dtype, int64_t ldd
  * aligned).  flce_mx_forward writes logprob, lse and entropy of targets, which never leave
  * the chip as logits: validity, ignored rows, outputs and token waves as in flce_forward,
  * with z from the 4-bit operands.  Workspaces: 256-byte aligned; flce_mx_workspace_query
- * gives what flce_mx_logits needs and what flce_mx_forward takes all rows at once with
- * (a smaller one, down to that of min(M, 256) rows, runs in waves).  M = 0 is accepted and
+ * gives what flce_mx_logits needs and what flce_mx_forward takes all rows at once with (a
+ * smaller one, down to one wave of 256 rows, runs in waves; past 128 tokens both hold a copy
+ * of W's scale bytes in another order).  M = 0 is accepted and
  * touches nothing.  Not differentiable: the weights are frozen.
  */
 flce_status_t flce_mx_workspace_query(int64_t M, int64_t H, int64_t V, int compute_entropy,

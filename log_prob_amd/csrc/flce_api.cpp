@@ -746,23 +746,35 @@ namespace {
 size_t mx_x_codes_bytes(int64_t rows, int64_t H) {
   return align_up(size_t(rows) * size_t(flce::mx_code_bytes(H, flce::kMxFp4)));
 }
-size_t mx_x_bytes(int64_t rows, int64_t H) {
-  return mx_x_codes_bytes(rows, H) + align_up(size_t(rows) * size_t(flce::mx_scale_bytes(H)));
+// Scales of whole 256-row tiles (the tile kernels' form), or of just the rows there are.
+size_t mx_scales_bytes(int64_t rows, int64_t H, bool tiled) {
+  return align_up(size_t(tiled ? cdiv(rows, kTile) * kTile : rows) * size_t(flce::mx_scale_bytes(H)));
 }
 
-// Bytes of a forward wave of `rows` rows: X's copy, then the partials.
-size_t mx_wave_bytes(int64_t rows, int64_t H, int64_t V, bool ent) {
-  return mx_x_bytes(rows, H) + fwd_layout(rows, V, ent).total;
+// Calls past kMxStreamTokens tokens run the tile kernels, which read the scales of W from a
+// copy in their own form.
+bool mx_streams(int64_t M) { return M <= flce::kMxStreamTokens; }
+size_t mx_w_bytes(int64_t M, int64_t H, int64_t V) {
+  return mx_streams(M) ? 0 : mx_scales_bytes(V, H, true);
+}
+// X's copy of `rows` of the call's M rows.
+size_t mx_x_bytes(int64_t M, int64_t rows, int64_t H) {
+  return mx_x_codes_bytes(rows, H) + mx_scales_bytes(rows, H, !mx_streams(M));
+}
+
+// Bytes of a forward wave of `rows` of the call's M rows: W's scales, X's copy, the partials.
+size_t mx_wave_bytes(int64_t M, int64_t rows, int64_t H, int64_t V, bool ent) {
+  return mx_w_bytes(M, H, V) + mx_x_bytes(M, rows, H) + fwd_layout(rows, V, ent).total;
 }
 
 // Tallest wave that fits in `bytes` (all M rows, or a multiple of 256); 0 if none does.
 int64_t mx_wave_rows(int64_t M, int64_t H, int64_t V, bool ent, size_t bytes) {
   const int64_t cap = max_wave_rows(V);
-  if (M <= cap && mx_wave_bytes(M, H, V, ent) <= bytes) return M;
+  if (M <= cap && mx_wave_bytes(M, M, H, V, ent) <= bytes) return M;
   int64_t lo = 0, hi = (M < cap ? cdiv(M, kTile) : cap / kTile) + 1;  // lo fits (or 0), hi does not
   while (hi - lo > 1) {
     const int64_t mid = (lo + hi) / 2;
-    if (mx_wave_bytes(mid * kTile, H, V, ent) <= bytes) lo = mid; else hi = mid;
+    if (mx_wave_bytes(M, mid * kTile, H, V, ent) <= bytes) lo = mid; else hi = mid;
   }
   return lo * kTile;
 }
@@ -780,15 +792,26 @@ flce_status_t check_mx_call(const void* X, const void* W_codes, const void* W_sc
   return FLCE_OK;
 }
 
-// Quantise rows [r0, r0 + rows) of X to the workspace.
-hipError_t mx_quantize_x(const void* X, int64_t r0, int64_t rows, int64_t H, char* ws,
+// Quantise rows [r0, r0 + rows) of X to ws, its scales laid out for the call's kernels.
+hipError_t mx_quantize_x(const void* X, int64_t r0, int64_t rows, int64_t H, bool stream_form, char* ws,
                          flce::MxOperand* x, hipStream_t stream) {
   uint8_t* codes = reinterpret_cast<uint8_t*>(ws);
   uint8_t* scales = codes + mx_x_codes_bytes(rows, H);
-  *x = flce::MxOperand{codes, scales};
+  *x = flce::MxOperand{codes, scales, stream_form ? flce::mx_row_major(H) : flce::mx_tiled(H)};
   const flce::MxQuantArgs q{static_cast<const uint16_t*>(X) + r0 * H, long(H), nullptr, 0, codes,
-                            scales, long(rows), long(H)};
+                            scales, long(rows), long(H), x->layout};
   return flce::launch_mx_quantize(q, flce::kBf16, flce::kMxFp4, true, stream);
+}
+
+// W as the call's kernels read it: as given, or with its scales turned into ws.
+hipError_t mx_weights(const void* W_codes, const void* W_scales, int64_t M, int64_t H, int64_t V,
+                      char* ws, flce::MxOperand* w, hipStream_t stream) {
+  const uint8_t* scales = static_cast<const uint8_t*>(W_scales);
+  *w = flce::MxOperand{static_cast<const uint8_t*>(W_codes), scales, flce::mx_row_major(H)};
+  if (mx_streams(M)) return hipSuccess;
+  w->scales = reinterpret_cast<uint8_t*>(ws);
+  w->layout = flce::mx_tiled(H);
+  return flce::launch_mx_turn_scales(scales, reinterpret_cast<uint8_t*>(ws), long(V), long(H), stream);
 }
 
 }  // namespace
@@ -801,10 +824,10 @@ flce_status_t flce_mx_workspace_query(int64_t M, int64_t H, int64_t V, int compu
     return fail(FLCE_ERR_INVALID_VALUE, "compute_entropy must be 0 or 1");
   flce_status_t st = check_shape(M, H, V);
   if (st != FLCE_OK) return st;
-  if (logits_bytes) *logits_bytes = mx_x_bytes(M, H);
+  if (logits_bytes) *logits_bytes = mx_w_bytes(M, H, V) + mx_x_bytes(M, M, H);
   if (fwd_bytes) {
     const int64_t cap = max_wave_rows(V);
-    *fwd_bytes = mx_wave_bytes(M < cap ? M : cap, H, V, compute_entropy == 1);
+    *fwd_bytes = mx_wave_bytes(M, M < cap ? M : cap, H, V, compute_entropy == 1);
   }
   return ok();
 }
@@ -828,19 +851,23 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
     return fail(FLCE_ERR_UNSUPPORTED, "out must be naturally aligned");
   if (!aligned(workspace, kAlign))
     return fail(FLCE_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
-  if (workspace_bytes < mx_x_bytes(M, H))
-    return fail(FLCE_ERR_WORKSPACE_TOO_SMALL, "logits need %zu workspace bytes, got %zu",
-                mx_x_bytes(M, H), workspace_bytes);
-  flce::MxOperand x;
-  hipError_t e = mx_quantize_x(X, 0, M, H, static_cast<char*>(workspace), &x, stream);
+  const size_t need = mx_w_bytes(M, H, V) + mx_x_bytes(M, M, H);
+  if (workspace_bytes < need)
+    return fail(FLCE_ERR_WORKSPACE_TOO_SMALL, "logits need %zu workspace bytes, got %zu", need,
+                workspace_bytes);
+  char* ws = static_cast<char*>(workspace);
+  flce::MxOperand x, w;
+  hipError_t e = mx_weights(W_codes, W_scales, M, H, V, ws, &w, stream);
+  if (e != hipSuccess) return hip_fail(e, "scale layout kernel launch");
+  e = mx_quantize_x(X, 0, M, H, mx_streams(M), ws + mx_w_bytes(M, H, V), &x, stream);
   if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
   // one launch covers up to max_wave_rows(V) rows (the dispatch limit)
   const int64_t rows = max_wave_rows(V);
   for (int64_t r0 = 0; r0 < M; r0 += rows) {
     flce::MxLogitsArgs a{};
-    a.x.codes = x.codes + r0 * flce::mx_code_bytes(H, flce::kMxFp4);
-    a.x.scales = x.scales + r0 * flce::mx_scale_bytes(H);
-    a.w = flce::MxOperand{static_cast<const uint8_t*>(W_codes), static_cast<const uint8_t*>(W_scales)};
+    a.x = flce::MxOperand{x.codes + r0 * flce::mx_code_bytes(H, flce::kMxFp4),
+                          x.scales + r0 / 256 * x.layout.tile_stride, x.layout};
+    a.w = w;
     a.M = int(M - r0 < rows ? M - r0 : rows);
     a.H = int(H);
     a.V = int(V);
@@ -848,7 +875,7 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
     a.out = static_cast<char*>(out) + r0 * ldo * (out_dtype == FLCE_BF16 ? 2 : 4);
     a.ldo = long(ldo);
     a.out_dtype = out_dtype;
-    a.stream = M <= flce::kMxStreamTokens;
+    a.stream = mx_streams(M);
     a.n_mt = int(cdiv(a.M, flce::kFwdTileM));
     a.n_vt = int(cdiv(V, flce::kFwdTileN));
     e = flce::launch_mx_logits(a, stream);
@@ -879,17 +906,21 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
   if (rows == 0)
     return fail(FLCE_ERR_WORKSPACE_TOO_SMALL,
                 "4-bit forward needs at least %zu workspace bytes, got %zu",
-                mx_wave_bytes(M < kTile ? M : kTile, H, V, ent), workspace_bytes);
+                mx_wave_bytes(M, M < kTile ? M : kTile, H, V, ent), workspace_bytes);
   char* ws = static_cast<char*>(workspace);
+  flce::MxOperand w;
+  hipError_t e = mx_weights(W_codes, W_scales, M, H, V, ws, &w, stream);
+  if (e != hipSuccess) return hip_fail(e, "scale layout kernel launch");
+  ws += mx_w_bytes(M, H, V);
   for (int64_t r0 = 0; r0 < M; r0 += rows) {
     const int64_t mw = M - r0 < rows ? M - r0 : rows;
     const FwdLayout L = fwd_layout(mw, V, ent);
-    char* part = ws + mx_x_bytes(mw, H);
+    char* part = ws + mx_x_bytes(M, mw, H);
     flce::MxFwdArgs a{};
-    a.w = flce::MxOperand{static_cast<const uint8_t*>(W_codes), static_cast<const uint8_t*>(W_scales)};
+    a.w = w;
     a.f = tile_args(nullptr, nullptr, targets + r0, mw, H, V, 0, ignore_index, scale, ent, L, part);
-    a.stream = M <= flce::kMxStreamTokens;
-    hipError_t e = mx_quantize_x(X, r0, mw, H, ws, &a.x, stream);
+    a.stream = mx_streams(M);
+    e = mx_quantize_x(X, r0, mw, H, a.stream, ws, &a.x, stream);
     if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
     e = flce::launch_mx_target_logit(a, stream);  // zeroes the queue counters
     if (e != hipSuccess) return hip_fail(e, "4-bit target logit kernel launch");

@@ -47,6 +47,11 @@ __device__ __forceinline__ f32x16 mx_mfma(u32x4 a, u32x4 b, f32x16 c, int sa, in
 constexpr int STREAM_WAVES = 8, STREAM_ROWS = 32 * STREAM_WAVES;  // vocabulary rows a workgroup
 static_assert(STREAM_ROWS == kFwdTileN, "partials of whole vocabulary tiles");
 
+// Offset of a row's scale bytes.
+__device__ __forceinline__ long mx_scale_row(const MxScaleLayout& l, long row) {
+  return (row >> 8) * l.tile_stride + (row & 255) * l.row_stride;
+}
+
 // One lane's share of a step: its four blocks of a row and their scale bytes.
 struct StreamFrag {
   u32x4 c[4];
@@ -57,10 +62,12 @@ struct StreamFrag {
 struct StreamRow {
   const uint8_t* codes;
   const uint8_t* scales;
+  long quad;   // bytes between the row's 16-byte pieces of scales
   int blocks;  // blocks of the row from this lane's first on (may be <= 0)
   __device__ __forceinline__ void init(const MxOperand& op, long row, int H, int half) {
     codes = op.codes + row * mx_code_bytes(H, kMxFp4) + 64 * half;
-    scales = op.scales + row * mx_scale_bytes(H) + 4 * half;
+    scales = op.scales + mx_scale_row(op.layout, row) + 4 * half;
+    quad = op.layout.quad_stride;
     blocks = (int)mx_blocks(H) - 4 * half;
   }
   // step st; TAIL: blocks past the row's end read as zero codes
@@ -73,7 +80,7 @@ struct StreamRow {
       else
         f.c[j] = u32x4{0u, 0u, 0u, 0u};
     }
-    f.s = *reinterpret_cast<const uint32_t*>(scales + 8l * st);
+    f.s = *reinterpret_cast<const uint32_t*>(scales + (st >> 1) * quad + 8 * (st & 1));
   }
 };
 
@@ -236,7 +243,10 @@ __global__ __launch_bounds__(64 * TL_ROWS) void mx_target_logit_kernel(MxFwdArgs
   if (row >= p.M) return;
   const int64_t t = p.targets[row];
   if (t == p.ignore_index || t < 0 || t >= p.V) return;
-  const long code_ld = mx_code_bytes(p.H, kMxFp4), scale_ld = mx_scale_bytes(p.H);
+  const long code_ld = mx_code_bytes(p.H, kMxFp4);
+  auto scale = [](const MxOperand& o, long r, int b) {
+    return mx_scale(o.scales[mx_scale_row(o.layout, r) + (b >> 4) * o.layout.quad_stride + (b & 15)]);
+  };
   float s = 0.f;
   for (int b = lane; b < (int)mx_blocks(p.H); b += 64) {
     const u32x4 xc = *reinterpret_cast<const u32x4*>(a.x.codes + row * code_ld + 16l * b);
@@ -250,9 +260,7 @@ __global__ __launch_bounds__(64 * TL_ROWS) void mx_target_logit_kernel(MxFwdArgs
 #pragma unroll
       for (int j = 0; j < 8; ++j) d = fmaf(xv[j], wv[j], d);
     }
-    const float sx = mx_scale(a.x.scales[row * scale_ld + b]);
-    const float sw = mx_scale(a.w.scales[t * scale_ld + b]);
-    s = fmaf(d * sx, sw, s);
+    s = fmaf(d * scale(a.x, row, b), scale(a.w, t, b), s);
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
@@ -273,7 +281,7 @@ constexpr int MX_SCALE_BYTES = 16 * 256;     // one operand's scales of two step
 constexpr int MX_LDS = MxShape::PIPE_BYTES + 4 * MX_SCALE_BYTES;
 static_assert(MX_LDS <= 160 * 1024, "LDS");
 
-// One operand tile: codes and scales of its first row, rows that exist, bytes of a row.
+// One operand tile: codes of its first row, its scales (tiled form), rows that exist, columns.
 struct MxTile {
   const uint8_t* codes;
   const uint8_t* scales;
@@ -305,23 +313,23 @@ struct MxFrag {
   }
 };
 
-// Loads of an operand's scales: wave w brings rows 64 w .. + 63, a lane one row's 16 bytes.
+// Loads of an operand's scales: wave w brings rows 64 w .. + 63, a lane one row's 16 bytes, a
+// kilobyte in all.
 struct MxScaleDma {
   i32x4 rsrc;
   uint32_t voff, lds;
   int pairs;
   __device__ __forceinline__ void init(const MxTile& t, int wave, const char* lds0) {
     const int row = 64 * wave + (int)(threadIdx.x & 63);
-    const uint32_t ld = (uint32_t)mx_scale_bytes(t.H);
     rsrc = make_rsrc_fixed(t.scales);
-    voff = row < t.valid ? (uint32_t)row * ld : OOB_OFFSET;
+    voff = row < t.valid ? 16u * (uint32_t)row : OOB_OFFSET;
     lds = lds_addr_of(lds0) + (uint32_t)(1024 * wave);
-    pairs = (int)(ld / 16);
+    pairs = (int)(mx_scale_bytes(t.H) / 16);
   }
   // steps 2 pair and 2 pair + 1 into buffer `pair % 2`; a pair past the end is all zeros
   __device__ __forceinline__ void issue(int pair) const {
     const bool live = pair < pairs;
-    dma16<0>(rsrc, live ? voff : OOB_OFFSET, live ? 16u * (uint32_t)pair : 0u,
+    dma16<0>(rsrc, live ? voff : OOB_OFFSET, live ? 4096u * (uint32_t)pair : 0u,
              lds + (uint32_t)((pair & 1) * 2 * MX_SCALE_BYTES));
   }
 };
@@ -470,10 +478,10 @@ __device__ __forceinline__ void mx_mainloop(f32x16 (&acc)[4][4], char* smem, con
 // The tile of vocabulary rows (A) and tokens (B) of a workgroup.
 __device__ __forceinline__ void mx_tile_product(f32x16 (&acc)[4][4], char* smem, const MxOperand& x,
                                                 const MxOperand& w, int M, int H, int V, int mt, int vt) {
-  const long code_ld = mx_code_bytes(H, kMxFp4), scale_ld = mx_scale_bytes(H);
+  const long code_ld = mx_code_bytes(H, kMxFp4);
   const int row0 = mt * 256, col0 = vt * 256;
-  const MxTile A{w.codes + col0 * code_ld, w.scales + col0 * scale_ld, V - col0, H};
-  const MxTile B{x.codes + row0 * code_ld, x.scales + row0 * scale_ld, M - row0, H};
+  const MxTile A{w.codes + col0 * code_ld, w.scales + vt * w.layout.tile_stride, V - col0, H};
+  const MxTile B{x.codes + row0 * code_ld, x.scales + mt * x.layout.tile_stride, M - row0, H};
   mx_mainloop(acc, smem, A, B);
 }
 

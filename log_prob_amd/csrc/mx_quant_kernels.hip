@@ -18,17 +18,25 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int BATCH = 4;  // chunks a thread has in flight
 
+// Offset of a row's scale bytes, and of block b's byte from there.
+__device__ __forceinline__ long row_at(const MxScaleLayout& l, long row) {
+  return (row >> 8) * l.tile_stride + (row & 255) * l.row_stride;
+}
+__device__ __forceinline__ long scale_at(const MxScaleLayout& l, long b) {
+  return (b >> 4) * l.quad_stride + (b & 15);
+}
+
 // Rows of TPR threads, THREADS / TPR rows a workgroup; thread t of a row takes chunks t,
 // t + TPR, ... of it.  A row's codes end with a whole block, so quads stay whole.
 template <class T, int FMT, bool VEC>
 __global__ __launch_bounds__(THREADS) void mx_quantize_kernel(MxQuantArgs p, int tpr) {
   const int t = threadIdx.x & (tpr - 1), rows = THREADS / tpr;
   const long blocks = mx_blocks(p.cols), chunks = 4 * blocks;
-  const long code_ld = mx_code_bytes(p.cols, FMT), scale_ld = mx_scale_bytes(p.cols);
+  const long code_ld = mx_code_bytes(p.cols, FMT), quads = mx_scale_bytes(p.cols) / 16;
   for (long row = (long)blockIdx.x * rows + threadIdx.x / tpr; row < p.rows; row += (long)gridDim.x * rows) {
     const typename T::mem* x = static_cast<const typename T::mem*>(p.x) + row * p.ldx;
     uint8_t* codes = p.codes + row * code_ld;
-    uint8_t* scales = p.scales + row * scale_ld;
+    uint8_t* scales = p.scales + row_at(p.layout, row);
     for (long c0 = t; c0 < chunks; c0 += (long)BATCH * tpr) {
       float v[BATCH][8];
 #pragma unroll
@@ -36,18 +44,18 @@ __global__ __launch_bounds__(THREADS) void mx_quantize_kernel(MxQuantArgs p, int
 #pragma unroll
       for (int b = 0; b < BATCH; ++b) {
         const long c = c0 + (long)b * tpr;
-        const uint32_t byte = mx_scale_byte<FMT>(v[b]);
-        const u32x2_t q = mx_encode<FMT>(v[b], byte);
-        if (c < chunks) {
+        if (c < chunks) {  // the same for a whole quad
+          const uint32_t byte = mx_scale_byte<FMT>(v[b]);
+          const u32x2_t q = mx_encode<FMT>(v[b], byte);
           if constexpr (FMT == kMxFp4)
             *reinterpret_cast<uint32_t*>(codes + 4 * c) = q.x;
           else
             *reinterpret_cast<u32x2_t*>(codes + 8 * c) = q;
-          if ((c & 3) == 0) scales[c >> 2] = (uint8_t)byte;
+          if ((c & 3) == 0) scales[scale_at(p.layout, c >> 2)] = (uint8_t)byte;
         }
       }
     }
-    for (long i = blocks + t; i < scale_ld; i += tpr) scales[i] = 0;
+    for (long i = blocks + t; i < 16 * quads; i += tpr) scales[scale_at(p.layout, i)] = 0;
   }
 }
 
@@ -55,11 +63,11 @@ template <class T, int FMT, bool VEC>
 __global__ __launch_bounds__(THREADS) void mx_dequantize_kernel(MxQuantArgs p, int tpr) {
   const int t = threadIdx.x & (tpr - 1), rows = THREADS / tpr;
   const long chunks = 4 * mx_blocks(p.cols);
-  const long code_ld = mx_code_bytes(p.cols, FMT), scale_ld = mx_scale_bytes(p.cols);
+  const long code_ld = mx_code_bytes(p.cols, FMT);
   for (long row = (long)blockIdx.x * rows + threadIdx.x / tpr; row < p.rows; row += (long)gridDim.x * rows) {
     typename T::mem* out = static_cast<typename T::mem*>(p.out) + row * p.ldo;
     const uint8_t* codes = p.codes + row * code_ld;
-    const uint8_t* scales = p.scales + row * scale_ld;
+    const uint8_t* scales = p.scales + row_at(p.layout, row);
 #pragma unroll 4
     for (long c = t; c < chunks; c += tpr) {
       u32x2_t q = {0u, 0u};
@@ -68,9 +76,24 @@ __global__ __launch_bounds__(THREADS) void mx_dequantize_kernel(MxQuantArgs p, i
       else
         q = *reinterpret_cast<const u32x2_t*>(codes + 8 * c);
       float v[8];
-      mx_decode<FMT>(q, scales[c >> 2], v);
+      mx_decode<FMT>(q, scales[scale_at(p.layout, c >> 2)], v);
       store8<T, VEC>(out, 8 * c, p.cols, v);
     }
+  }
+}
+
+// 16-byte pieces from [rows][quads] to [rows / 256][quads][256]: 8 lanes read 128 contiguous
+// bytes of a row and 8 write 128 of a quad.
+__global__ __launch_bounds__(THREADS) void mx_turn_scales_kernel(const u32x4_t* __restrict__ src,
+                                                                 u32x4_t* __restrict__ dst, long rows,
+                                                                 int quads, int qtiles) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const long n = (rows + 7) / 8 * qtiles;
+  for (long i = (long)blockIdx.x * (THREADS / 64) + wave; i < n; i += (long)gridDim.x * (THREADS / 64)) {
+    const long row = i / qtiles * 8 + lane / 8;
+    const int q = (int)(i % qtiles) * 8 + (lane & 7);
+    if (row < rows && q < quads)
+      dst[(row >> 8) * (256l * quads) + q * 256l + (row & 255)] = src[row * quads + q];
   }
 }
 
@@ -111,6 +134,14 @@ void dequantize_any(const MxQuantArgs& a, int dtype, bool vec, hipStream_t s) {
 }
 
 }  // namespace
+
+hipError_t launch_mx_turn_scales(const uint8_t* src, uint8_t* dst, long rows, long cols, hipStream_t s) {
+  const int quads = (int)(mx_scale_bytes(cols) / 16), qtiles = (quads + 7) / 8;
+  const long need = ((rows + 7) / 8 * qtiles + 3) / 4;
+  mx_turn_scales_kernel<<<(unsigned)(need < 4096 ? need : 4096), THREADS, 0, s>>>(
+      reinterpret_cast<const u32x4_t*>(src), reinterpret_cast<u32x4_t*>(dst), rows, quads, qtiles);
+  return hipGetLastError();
+}
 
 hipError_t launch_mx_quantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s) {
   if (fmt == kMxFp4) quantize_any<kMxFp4>(a, dtype, vec, s);

@@ -77,6 +77,18 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a, int x_dtype, int dy_dtype, int 
                            hipStream_t s);
 hipError_t launch_norm_reduce(const NormReduceArgs& a, hipStream_t s);
 
+// Where the scale bytes of a microscaled matrix lie: those of blocks 16 q .. 16 q + 15 of row
+// r are the 16 bytes at (r / 256) tile_stride + (r % 256) row_stride + q quad_stride.  The
+// public form is row-major; the tile kernels read a form in which the rows of a 256-row tile
+// are side by side and a tile's bytes contiguous.
+struct MxScaleLayout {
+  long row_stride, quad_stride, tile_stride;
+};
+inline MxScaleLayout mx_row_major(int64_t cols) {
+  return {long(mx_scale_bytes(cols)), 16, long(256 * mx_scale_bytes(cols))};
+}
+inline MxScaleLayout mx_tiled(int64_t cols) { return {16, 16 * 256, long(256 * mx_scale_bytes(cols))}; }
+
 struct MxQuantArgs {
   const void* x;           // quantise: the matrix; dequantise: unused
   long ldx;
@@ -86,6 +98,7 @@ struct MxQuantArgs {
   uint8_t* scales;
   long rows;
   long cols;
+  MxScaleLayout layout;
 };
 hipError_t launch_mx_quantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s);
@@ -96,7 +109,10 @@ constexpr int64_t kMxStreamTokens = 128;
 struct MxOperand {
   const uint8_t* codes;
   const uint8_t* scales;
+  MxScaleLayout layout;
 };
+// Scales of `rows` rows from row-major to the tile kernels' form (whole 256-row tiles).
+hipError_t launch_mx_turn_scales(const uint8_t* src, uint8_t* dst, long rows, long cols, hipStream_t s);
 struct MxLogitsArgs {
   MxOperand x, w;
   int M, H, V;
