@@ -452,7 +452,7 @@ flce_status_t flce_layer_norm_backward(const void* dy, int dy_dtype, int64_t ldd
  * the chip as logits: validity, ignored rows, outputs and token waves as in flce_forward,
  * with z from the 4-bit operands.  Workspaces: 256-byte aligned; flce_mx_workspace_query
  * gives what flce_mx_logits needs and what flce_mx_forward takes all rows at once with (a
- * smaller one, down to one wave of 256 rows, runs in waves; past 128 tokens both hold a copy
+ * smaller one, down to one wave of 256 rows, runs in waves; for large calls both hold a copy
  * of W's scale bytes in another order).  M = 0 is accepted and
  * touches nothing.  Not differentiable: the weights are frozen.
  */

@@ -751,11 +751,16 @@ size_t mx_scales_bytes(int64_t rows, int64_t H, bool tiled) {
   return align_up(size_t(tiled ? cdiv(rows, kTile) * kTile : rows) * size_t(flce::mx_scale_bytes(H)));
 }
 
-// Calls past kMxStreamTokens tokens run the tile kernels, which read the scales of W from a
-// copy in their own form.
+// Calls past kMxStreamTokens tokens run the tile kernels.  Those read scales fastest in their
+// own form, and X's are written so; turning W's costs a launch and a pass over them (3 to 8
+// us), which calls of this size win back (M=H=4096, V=128256: 1081 -> 1036 us; M=257, H=1600,
+// V=50257: 54 -> 58 us).
 bool mx_streams(int64_t M) { return M <= flce::kMxStreamTokens; }
+bool mx_turns(int64_t M, int64_t H, int64_t V) {
+  return M >= 2048 && double(M) * double(H) * double(V) >= 2.5e11;
+}
 size_t mx_w_bytes(int64_t M, int64_t H, int64_t V) {
-  return mx_streams(M) ? 0 : mx_scales_bytes(V, H, true);
+  return mx_turns(M, H, V) ? mx_scales_bytes(V, H, true) : 0;
 }
 // X's copy of `rows` of the call's M rows.
 size_t mx_x_bytes(int64_t M, int64_t rows, int64_t H) {
@@ -808,7 +813,7 @@ hipError_t mx_weights(const void* W_codes, const void* W_scales, int64_t M, int6
                       char* ws, flce::MxOperand* w, hipStream_t stream) {
   const uint8_t* scales = static_cast<const uint8_t*>(W_scales);
   *w = flce::MxOperand{static_cast<const uint8_t*>(W_codes), scales, flce::mx_row_major(H)};
-  if (mx_streams(M)) return hipSuccess;
+  if (!mx_turns(M, H, V)) return hipSuccess;
   w->scales = reinterpret_cast<uint8_t*>(ws);
   w->layout = flce::mx_tiled(H);
   return flce::launch_mx_turn_scales(scales, reinterpret_cast<uint8_t*>(ws), long(V), long(H), stream);

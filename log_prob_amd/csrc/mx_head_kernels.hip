@@ -276,36 +276,72 @@ __global__ __launch_bounds__(64 * TL_ROWS) void mx_target_logit_kernel(MxFwdArgs
 // sub-step, and each sub-step's fragments read while the one before it computes.  Scales come
 // 16 bytes of a row (two steps) at a time into two 8 KiB buffers of their own, and each lane
 // reads a dword of them (its four blocks of a step) per 32-row fragment.
-using MxShape = Shape<256, 256, 64, 2, 1>;   // BK in units of 2 bytes of codes
+using MxShape = BigShape;                    // of the products and the epilogue
+constexpr int MX_TILE_BYTES = 128 * 256;     // one operand's codes of a step
 constexpr int MX_SCALE_BYTES = 16 * 256;     // one operand's scales of two steps
-constexpr int MX_LDS = MxShape::PIPE_BYTES + 4 * MX_SCALE_BYTES;
+constexpr int MX_LDS = 4 * MX_TILE_BYTES + 4 * MX_SCALE_BYTES;
 static_assert(MX_LDS <= 160 * 1024, "LDS");
 
-// One operand tile: codes of its first row, its scales (tiled form), rows that exist, columns.
+// One operand tile: codes and scales of its first row, strides of the scales, rows that exist,
+// columns.
 struct MxTile {
   const uint8_t* codes;
   const uint8_t* scales;
+  uint32_t row_stride, quad_stride;
   int valid;
   int H;
 };
 
-// LDS byte offsets of a lane's fragments.  Row r = idx0 + 32 blk + l % 32 holds chunk c at
-// position c ^ kc_swz(r), and kc_swz changes by 4 from one 32-row block to the next, so a
-// block's parity and kk select one of 8 offsets and the rest is an immediate.
+// Chunk c (16 bytes) of row r of a code tile sits at position c ^ mx_swz(r) of the row's 128
+// bytes: the 16 rows that one cycle of a fragment read serves land on 16 distinct 16-byte bank
+// groups, and the swizzle is the same for rows 32 apart, so a fragment's 32-row block is an
+// immediate offset.
+__device__ __forceinline__ int mx_swz(int r) { return (r ^ ((r >> 3) & 3)) & 7; }
+
+// Direct-to-LDS loads of a step's operand tile: 8 a wave, load j bringing rows 64 wave + 8 j
+// .. + 7, lane i the 16 bytes of row i / 8 whose position is i % 8.  A lane's offset depends
+// on j only through the swizzle (j % 4); the rows and the step move with the scalar offset.
+// Both operands have the same rows of codes, so they share all of it.
+struct MxCodeDma {
+  uint32_t voff[4];
+  uint32_t ld, row0;  // bytes of a row of codes; offset of the wave's first row
+  int wave;
+  __device__ __forceinline__ void init(int H, int wave_id) {
+    wave = wave_id;
+    ld = (uint32_t)mx_code_bytes(H, kMxFp4);
+    row0 = 64u * (uint32_t)wave * ld;
+    const uint32_t lane = threadIdx.x & 63, r = lane >> 3;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) voff[j] = r * ld + (((lane & 7) ^ r ^ j) << 4);
+  }
+  // load j of step st (byte offset 128 st) from the tile at rsrc to the LDS tile at lds.  FAST:
+  // every row and chunk exists; otherwise rows past `valid` and chunks past `lim` are zeros.
+  template <bool FAST>
+  __device__ __forceinline__ void issue(const i32x4& rsrc, int valid, int lim, int st, int j,
+                                        uint32_t lds) const {
+    uint32_t v = voff[j & 3];
+    if constexpr (!FAST) {
+      const int lane = threadIdx.x & 63, r = lane >> 3;
+      v = r + 64 * wave + 8 * j < valid && ((lane & 7) ^ r ^ (j & 3)) < lim ? v : OOB_OFFSET;
+    }
+    dma16<0>(rsrc, v, 128u * (uint32_t)st + row0 + 8u * (uint32_t)j * ld,
+             lds + 8192u * (uint32_t)wave + 1024u * (uint32_t)j);
+  }
+};
+
+// LDS byte offsets of a lane's fragments and scales, block 0 of the wave's rows from idx0.
 struct MxFrag {
-  uint32_t code[2][4];
+  uint32_t code[4];
   uint32_t scale;
   __device__ __forceinline__ void init(int idx0, int lane, uint32_t region, uint32_t scale_region) {
     const int r = idx0 + (lane & 31), half = lane >> 5;
 #pragma unroll
-    for (int par = 0; par < 2; ++par)
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        code[par][kk] = region + (uint32_t)(r * 128 + (((4 * half + kk) ^ kc_swz<8>(r) ^ (4 * par)) << 4));
+    for (int kk = 0; kk < 4; ++kk)
+      code[kk] = region + (uint32_t)(r * 128 + (((4 * half + kk) ^ mx_swz(r)) << 4));
     scale = scale_region + (uint32_t)(16 * r + 4 * half);
   }
   __device__ __forceinline__ u32x4 read(const char* stage, int blk, int kk) const {
-    return *reinterpret_cast<const u32x4*>(stage + code[blk & 1][kk] + 4096 * blk);
+    return *reinterpret_cast<const u32x4*>(stage + code[kk] + 4096 * blk);
   }
   // parity: which of the pair's two steps
   __device__ __forceinline__ int read_scale(const char* pair, int blk, int parity) const {
@@ -313,23 +349,24 @@ struct MxFrag {
   }
 };
 
-// Loads of an operand's scales: wave w brings rows 64 w .. + 63, a lane one row's 16 bytes, a
-// kilobyte in all.
+// Loads of an operand's scales: wave w brings rows 64 w .. + 63, a lane one row's 16 bytes: a
+// contiguous kilobyte in the tiled form, a line each in the row-major one.
 struct MxScaleDma {
   i32x4 rsrc;
-  uint32_t voff, lds;
+  uint32_t voff, quad_stride, lds;
   int pairs;
   __device__ __forceinline__ void init(const MxTile& t, int wave, const char* lds0) {
     const int row = 64 * wave + (int)(threadIdx.x & 63);
     rsrc = make_rsrc_fixed(t.scales);
-    voff = row < t.valid ? 16u * (uint32_t)row : OOB_OFFSET;
+    voff = row < t.valid ? t.row_stride * (uint32_t)row : OOB_OFFSET;
+    quad_stride = t.quad_stride;
     lds = lds_addr_of(lds0) + (uint32_t)(1024 * wave);
     pairs = (int)(mx_scale_bytes(t.H) / 16);
   }
   // steps 2 pair and 2 pair + 1 into buffer `pair % 2`; a pair past the end is all zeros
   __device__ __forceinline__ void issue(int pair) const {
     const bool live = pair < pairs;
-    dma16<0>(rsrc, live ? voff : OOB_OFFSET, live ? 4096u * (uint32_t)pair : 0u,
+    dma16<0>(rsrc, live ? voff : OOB_OFFSET, live ? quad_stride * (uint32_t)pair : 0u,
              lds + (uint32_t)((pair & 1) * 2 * MX_SCALE_BYTES));
   }
 };
@@ -339,38 +376,53 @@ struct MxRegs {
   int sa[2][4], sb[2][4];  // scales of steps of either parity
 };
 
-// Group g of 16 of sub-step kk: one MFMA, every other group a fragment read of the next
-// sub-step (RKK, of the stage at ra / rb), and a share of the loads [JB, JE).
-template <int kk, int RKK, int STG, int g, int JB, int JE, class Ops>
-__device__ __forceinline__ void mx_group(f32x16 (&acc)[4][4], MxRegs& r, const char* ra,
-                                         const char* rb, const MxFrag& fa, const MxFrag& fb, Ops& dma) {
+// Group g of 16 of sub-step kk: one MFMA, every other group a fragment read
+// of the next sub-step (RKK, of `stage`), and a share of the loads [JB, JE).
+template <int kk, int RKK, int STG, int g, int JB, int JE, bool FAST, class Ops>
+__device__ __forceinline__ void mx_group(f32x16 (&acc)[4][4], MxRegs& r, const char* stage,
+                                         const MxFrag& fa, const MxFrag& fb, const Ops& dma) {
   constexpr int cur = kk & 1, nxt = cur ^ 1, mb = g / 4, nb = g % 4, D = JE - JB;
   if constexpr (g % 2 == 0) {
     constexpr int i = g / 2;
-    if constexpr (i < 4) r.a[nxt][i] = fa.read(ra, i, RKK);
-    else r.b[nxt][i - 4] = fb.read(rb, i - 4, RKK);
+    if constexpr (i < 4) r.a[nxt][i] = fa.read(stage, i, RKK);
+    else r.b[nxt][i - 4] = fb.read(stage, i - 4, RKK);
   }
   acc[mb][nb] = mx_mfma<kk>(r.a[cur][mb], r.b[cur][nb], acc[mb][nb], r.sa[STG][mb], r.sb[STG][nb]);
   if constexpr (g % 2 == 0) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
   __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
   if constexpr (D > 0) {
     __builtin_amdgcn_sched_barrier(0);
-    dma.issue(JB + g * D / 16, JB + (g + 1) * D / 16);
+    dma.template issue<FAST>(JB + g * D / 16, JB + (g + 1) * D / 16);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
-template <int kk, int RKK, int STG, int JB, int JE, class Ops, int... G>
-__device__ __forceinline__ void mx_substep(f32x16 (&acc)[4][4], MxRegs& r, const char* ra,
-                                           const char* rb, const MxFrag& fa, const MxFrag& fb,
-                                           Ops& dma, std::integer_sequence<int, G...>) {
-  (mx_group<kk, RKK, STG, G, JB, JE>(acc, r, ra, rb, fa, fb, dma), ...);
+template <int kk, int RKK, int STG, int JB, int JE, bool FAST, class Ops, int... G>
+__device__ __forceinline__ void mx_substep(f32x16 (&acc)[4][4], MxRegs& r, const char* stage,
+                                           const MxFrag& fa, const MxFrag& fb, const Ops& dma,
+                                           std::integer_sequence<int, G...>) {
+  (mx_group<kk, RKK, STG, G, JB, JE, FAST>(acc, r, stage, fa, fb, dma), ...);
 }
+
+// The loads of a step: 8 of B's tile (X, which more tiles share in L2), then 8 of A's.
+struct MxLoads {
+  const MxCodeDma& c;
+  const i32x4 &ra, &rb;
+  int va, vb, lim, st;
+  uint32_t la, lb;
+  template <bool FAST>
+  __device__ __forceinline__ void issue(int j0, int j1) const {
+#pragma unroll
+    for (int j = j0; j < j1; ++j) {
+      if (j < 8) c.issue<FAST>(rb, vb, lim, st, j, lb);
+      else c.issue<FAST>(ra, va, lim, st, j - 8, la);
+    }
+  }
+};
 
 // acc[mb][nb] = the 32 x 32 block (32 mb, 32 nb) of the wave's 128 x 128 of A B^T.
 __device__ __forceinline__ void mx_mainloop(f32x16 (&acc)[4][4], char* smem, const MxTile& A,
                                             const MxTile& B) {
-  using S = MxShape;
-  constexpr int D = S::DMA_STAGE, EARLY = D / 2;
+  constexpr int D = 16, EARLY = D / 2;  // loads of a step
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
@@ -379,31 +431,26 @@ __device__ __forceinline__ void mx_mainloop(f32x16 (&acc)[4][4], char* smem, con
     for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[mb][nb][e] = 0.f;
-  const int K = (int)(mx_code_bytes(A.H, kMxFp4) / 2);  // in 2-byte units
-  const int nk = (K + S::BK - 1) / S::BK, nfull = K / S::BK;
-  const TileSrc sa{reinterpret_cast<const uint16_t*>(A.codes), K, A.valid, K, 0};
-  const TileSrc sb{reinterpret_cast<const uint16_t*>(B.codes), K, B.valid, K, 0};
-  typename StageDma<S, true, true>::PA plan_a;
-  typename StageDma<S, true, true>::PB plan_b;
-  plan_a.init(sa, wave);
-  plan_b.init(sb, wave);
-  char* scale_lds = smem + S::PIPE_BYTES;  // buffers of a pair: A's rows, then B's
+  const int blocks = (int)mx_blocks(A.H);  // chunks of a row
+  const int nk = (blocks + 7) / 8;
+  // steps that lie inside K, where every row of both tiles exists (else none)
+  const int nfull = A.valid >= 256 && B.valid >= 256 ? blocks / 8 : 0;
+  char* scale_lds = smem + 4 * MX_TILE_BYTES;  // buffers of a pair: A's rows, then B's
+  MxCodeDma codes;
+  codes.init(A.H, wave);
+  const i32x4 ra = make_rsrc_fixed(A.codes), rb = make_rsrc_fixed(B.codes);
   MxScaleDma da, db;
   da.init(A, wave, scale_lds);
   db.init(B, wave, scale_lds + MX_SCALE_BYTES);
   MxFrag fa, fb;
   fa.init((wave / 2) * 128, lane, 0u, 0u);
-  fb.init((wave % 2) * 128, lane, 2u * S::A_BYTES, (uint32_t)MX_SCALE_BYTES);
-  auto stage_dma = [&](auto fast, int st, int s) {
-    constexpr bool FAST = decltype(fast)::value;
-    StageDma<S, true, true, FAST, true> d;
-    d.pa = &plan_a;
-    d.pb = &plan_b;
-    const bool active = st < nk;
-    const int k0 = (active ? st : 0) * S::BK;
-    d.a = tile_dma<FAST>(sa, plan_a, k0, active, smem + s * S::A_BYTES);
-    d.b = tile_dma<FAST>(sb, plan_b, k0, active, smem + 2 * S::A_BYTES + s * S::B_BYTES);
-    return d;
+  fb.init((wave % 2) * 128, lane, 2u * MX_TILE_BYTES, (uint32_t)MX_SCALE_BYTES);
+  // loads of step st into stage s (A0, A1, B0, B1); a step past K only zero-fills it
+  const uint32_t lds0 = lds_addr_of(smem);
+  auto loads = [&](int st, int s) {
+    const int lim = min(max(blocks - 8 * st, 0), 8);
+    return MxLoads{codes, ra, rb, A.valid, B.valid, lim, lim > 0 ? st : 0,
+                   lds0 + (uint32_t)(s * MX_TILE_BYTES), lds0 + (uint32_t)((2 + s) * MX_TILE_BYTES)};
   };
   using Slow = std::integral_constant<bool, false>;
   using Fast = std::integral_constant<bool, true>;
@@ -421,8 +468,8 @@ __device__ __forceinline__ void mx_mainloop(f32x16 (&acc)[4][4], char* smem, con
   // prologue: the first pair's scales, step 0, and the early loads of step 1
   da.issue(0);
   db.issue(0);
-  stage_dma(Slow(), 0, 0).issue(0, D);
-  stage_dma(Slow(), 1, 1).issue(0, EARLY);
+  loads(0, 0).issue<false>(0, D);
+  loads(1, 1).issue<false>(0, EARLY);
   wait_vmcnt<EARLY>();
   __syncthreads();
 #pragma unroll
@@ -432,17 +479,17 @@ __device__ __forceinline__ void mx_mainloop(f32x16 (&acc)[4][4], char* smem, con
   }
   read_scales(0, 0);
   constexpr auto groups = std::make_integer_sequence<int, 16>();
+  // step kt from stage STG (kt % 2 == STG)
   auto step = [&](auto stg, auto fast, int kt) {
     constexpr int STG = decltype(stg)::value;
-    const char* ca = smem + STG * S::A_BYTES;
-    const char* cb = smem + STG * S::B_BYTES;
-    const char* na = smem + (1 - STG) * S::A_BYTES;
-    const char* nb = smem + (1 - STG) * S::B_BYTES;
+    constexpr bool FAST = decltype(fast)::value;
+    const char* cur = smem + STG * MX_TILE_BYTES;
+    const char* nxt = smem + (1 - STG) * MX_TILE_BYTES;
     {
-      auto dma = stage_dma(fast, kt + 1, 1 - STG);
-      mx_substep<0, 1, STG, EARLY, D>(acc, r, ca, cb, fa, fb, dma, groups);
-      mx_substep<1, 2, STG, 0, 0>(acc, r, ca, cb, fa, fb, dma, groups);
-      mx_substep<2, 3, STG, 0, 0>(acc, r, ca, cb, fa, fb, dma, groups);
+      const auto dma = loads(kt + 1, 1 - STG);
+      mx_substep<0, 1, STG, EARLY, D, FAST>(acc, r, cur, fa, fb, dma, groups);
+      mx_substep<1, 2, STG, 0, 0, FAST>(acc, r, cur, fa, fb, dma, groups);
+      mx_substep<2, 3, STG, 0, 0, FAST>(acc, r, cur, fa, fb, dma, groups);
     }
     // keep the barrier after every MFMA issued so far (the compiler would hoist it)
     __builtin_amdgcn_sched_barrier(0);
@@ -457,8 +504,8 @@ __device__ __forceinline__ void mx_mainloop(f32x16 (&acc)[4][4], char* smem, con
       }
       read_scales(kt + 1, 1 - STG);
       __builtin_amdgcn_sched_barrier(0);
-      auto dma = stage_dma(fast, kt + 2, STG);
-      mx_substep<3, 0, STG, 0, EARLY>(acc, r, na, nb, fa, fb, dma, groups);
+      const auto dma = loads(kt + 2, STG);
+      mx_substep<3, 0, STG, 0, EARLY, FAST>(acc, r, nxt, fa, fb, dma, groups);
     }
   };
   int kt = 0;
@@ -480,8 +527,10 @@ __device__ __forceinline__ void mx_tile_product(f32x16 (&acc)[4][4], char* smem,
                                                 const MxOperand& w, int M, int H, int V, int mt, int vt) {
   const long code_ld = mx_code_bytes(H, kMxFp4);
   const int row0 = mt * 256, col0 = vt * 256;
-  const MxTile A{w.codes + col0 * code_ld, w.scales + vt * w.layout.tile_stride, V - col0, H};
-  const MxTile B{x.codes + row0 * code_ld, x.scales + mt * x.layout.tile_stride, M - row0, H};
+  const MxTile A{w.codes + col0 * code_ld, w.scales + vt * w.layout.tile_stride,
+                 (uint32_t)w.layout.row_stride, (uint32_t)w.layout.quad_stride, V - col0, H};
+  const MxTile B{x.codes + row0 * code_ld, x.scales + mt * x.layout.tile_stride,
+                 (uint32_t)x.layout.row_stride, (uint32_t)x.layout.quad_stride, M - row0, H};
   mx_mainloop(acc, smem, A, B);
 }
 
