@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["flce_kernels.hip", "norm_kernels.hip", "mx_quant_kernels.hip",
-           "mx_head_kernels.hip", "flce_api.cpp", "ops_api.cpp"]
+           "mx_stream_kernels.hip", "mx_tile_kernels.hip", "flce_api.cpp", "ops_api.cpp"]
 LIB = os.path.join(HERE, "libflce.so")
 ARCH = "gfx950"
 

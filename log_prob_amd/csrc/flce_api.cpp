@@ -767,9 +767,25 @@ size_t mx_x_bytes(int64_t M, int64_t rows, int64_t H) {
   return mx_x_codes_bytes(rows, H) + mx_scales_bytes(rows, H, !mx_streams(M));
 }
 
+// Partials of a forward wave of `rows` rows: n_vt vocabulary tiles (256 columns, or the rows
+// of W that a workgroup streams) of `pad` tokens, in 2 or 3 arrays; then the tile queues'
+// counters.
+struct MxParts {
+  int64_t n_vt, pad;
+  size_t array, total;
+};
+MxParts mx_parts(int64_t M, int64_t rows, int64_t V, bool ent) {
+  MxParts p;
+  p.n_vt = cdiv(V, mx_streams(M) ? flce::mx_stream_rows(int(M), int(V)) : int(flce::kFwdTileN));
+  p.pad = mx_streams(M) ? rows : cdiv(rows, kTile) * kTile;
+  p.array = align_up(size_t(p.n_vt) * size_t(p.pad) * sizeof(float));
+  p.total = (ent ? 3 : 2) * p.array + (rows > 0 ? flce::kQueueBytes : 0);
+  return p;
+}
+
 // Bytes of a forward wave of `rows` of the call's M rows: W's scales, X's copy, the partials.
 size_t mx_wave_bytes(int64_t M, int64_t rows, int64_t H, int64_t V, bool ent) {
-  return mx_w_bytes(M, H, V) + mx_x_bytes(M, rows, H) + fwd_layout(rows, V, ent).total;
+  return mx_w_bytes(M, H, V) + mx_x_bytes(M, rows, H) + mx_parts(M, rows, V, ent).total;
 }
 
 // Tallest wave that fits in `bytes` (all M rows, or a multiple of 256); 0 if none does.
@@ -797,14 +813,15 @@ flce_status_t check_mx_call(const void* X, const void* W_codes, const void* W_sc
   return FLCE_OK;
 }
 
-// Quantise rows [r0, r0 + rows) of X to ws, its scales laid out for the call's kernels.
+// Quantise rows [r0, r0 + rows) of X to ws, its scales laid out for the call's kernels, and
+// zero the 8 counters at `clear` (if not nullptr).
 hipError_t mx_quantize_x(const void* X, int64_t r0, int64_t rows, int64_t H, bool stream_form, char* ws,
-                         flce::MxOperand* x, hipStream_t stream) {
+                         unsigned long long* clear, flce::MxOperand* x, hipStream_t stream) {
   uint8_t* codes = reinterpret_cast<uint8_t*>(ws);
   uint8_t* scales = codes + mx_x_codes_bytes(rows, H);
   *x = flce::MxOperand{codes, scales, stream_form ? flce::mx_row_major(H) : flce::mx_tiled(H)};
   const flce::MxQuantArgs q{static_cast<const uint16_t*>(X) + r0 * H, long(H), nullptr, 0, codes,
-                            scales, long(rows), long(H), x->layout};
+                            scales, long(rows), long(H), x->layout, clear};
   return flce::launch_mx_quantize(q, flce::kBf16, flce::kMxFp4, true, stream);
 }
 
@@ -864,7 +881,7 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
   flce::MxOperand x, w;
   hipError_t e = mx_weights(W_codes, W_scales, M, H, V, ws, &w, stream);
   if (e != hipSuccess) return hip_fail(e, "scale layout kernel launch");
-  e = mx_quantize_x(X, 0, M, H, mx_streams(M), ws + mx_w_bytes(M, H, V), &x, stream);
+  e = mx_quantize_x(X, 0, M, H, mx_streams(M), ws + mx_w_bytes(M, H, V), nullptr, &x, stream);
   if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
   // one launch covers up to max_wave_rows(V) rows (the dispatch limit)
   const int64_t rows = max_wave_rows(V);
@@ -880,10 +897,10 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
     a.out = static_cast<char*>(out) + r0 * ldo * (out_dtype == FLCE_BF16 ? 2 : 4);
     a.ldo = long(ldo);
     a.out_dtype = out_dtype;
-    a.stream = mx_streams(M);
     a.n_mt = int(cdiv(a.M, flce::kFwdTileM));
     a.n_vt = int(cdiv(V, flce::kFwdTileN));
-    e = flce::launch_mx_logits(a, stream);
+    e = mx_streams(M) ? flce::launch_mx_stream_logits(a, stream)
+                      : flce::launch_mx_tile_logits(a, stream);
     if (e != hipSuccess) return hip_fail(e, "4-bit logits kernel launch");
   }
   return ok();
@@ -919,23 +936,34 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
   ws += mx_w_bytes(M, H, V);
   for (int64_t r0 = 0; r0 < M; r0 += rows) {
     const int64_t mw = M - r0 < rows ? M - r0 : rows;
-    const FwdLayout L = fwd_layout(mw, V, ent);
+    const MxParts L = mx_parts(M, mw, V, ent);
     char* part = ws + mx_x_bytes(M, mw, H);
     flce::MxFwdArgs a{};
     a.w = w;
-    a.f = tile_args(nullptr, nullptr, targets + r0, mw, H, V, 0, ignore_index, scale, ent, L, part);
-    a.stream = mx_streams(M);
-    e = mx_quantize_x(X, r0, mw, H, a.stream, ws, &a.x, stream);
+    a.targets = targets + r0;
+    a.M = int(mw);
+    a.H = int(H);
+    a.V = int(V);
+    a.ignore_index = ignore_index;
+    a.scale = scale;
+    a.n_mt = int(cdiv(mw, flce::kFwdTileM));
+    a.n_vt = int(L.n_vt);
+    a.tile_stride = mx_streams(M) ? 1 : long(L.pad);
+    a.token_stride = mx_streams(M) ? long(L.n_vt) : 1;
+    a.part_m = reinterpret_cast<float*>(part);
+    a.part_s = reinterpret_cast<float*>(part + L.array);
+    a.part_u = ent ? reinterpret_cast<float*>(part + 2 * L.array) : nullptr;
+    a.logprob = logprob + r0;
+    a.lse = lse + r0;
+    a.entropy = ent ? entropy + r0 : nullptr;
+    flce::TileQueue tq{};
+    tq.ctr = reinterpret_cast<unsigned long long*>(part + L.total - flce::kQueueBytes);
+    e = mx_quantize_x(X, r0, mw, H, mx_streams(M), ws, tq.ctr, &a.x, stream);
     if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
-    e = flce::launch_mx_target_logit(a, stream);  // zeroes the queue counters
-    if (e != hipSuccess) return hip_fail(e, "4-bit target logit kernel launch");
-    e = flce::launch_mx_fwd_tile(a, ent, stream);
+    e = mx_streams(M) ? flce::launch_mx_stream_fwd(a, stream) : flce::launch_mx_tile_fwd(a, tq, stream);
     if (e != hipSuccess) return hip_fail(e, "4-bit forward kernel launch");
-    const flce::FwdMergeArgs b =
-        merge_args_single(targets + r0, mw, V, ignore_index, ent, logprob + r0, lse + r0,
-                          ent ? entropy + r0 : nullptr, L, part);
-    e = flce::launch_fwd_merge(b, ent, stream);
-    if (e != hipSuccess) return hip_fail(e, "forward merge kernel launch");
+    e = flce::launch_mx_merge(a, stream);
+    if (e != hipSuccess) return hip_fail(e, "4-bit merge kernel launch");
   }
   return ok();
 }

@@ -30,6 +30,8 @@ __device__ __forceinline__ long scale_at(const MxScaleLayout& l, long b) {
 // t + TPR, ... of it.  A row's codes end with a whole block, so quads stay whole.
 template <class T, int FMT, bool VEC>
 __global__ __launch_bounds__(THREADS) void mx_quantize_kernel(MxQuantArgs p, int tpr) {
+  if (p.clear && blockIdx.x == 0 && threadIdx.x < 8)
+    __hip_atomic_store(&p.clear[threadIdx.x], 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   const int t = threadIdx.x & (tpr - 1), rows = THREADS / tpr;
   const long blocks = mx_blocks(p.cols), chunks = 4 * blocks;
   const long code_ld = mx_code_bytes(p.cols, FMT), quads = mx_scale_bytes(p.cols) / 16;

@@ -1,0 +1,432 @@
+// The head with 4-bit weights for few tokens (gfx950), and the merge of log-prob partials.
+//
+//   z[m, v] = scale * sum_k X[m, k] W[v, k],  X and W in MXFP4
+//
+// With up to 128 tokens the kernel is bound by memory: W's codes and scales are read once.
+// They come through a ring of LDS stages by direct-to-LDS loads, 128 contiguous bytes of a row
+// for 8 lanes, two stages ahead of the products (loaded straight into the matrix
+// instruction's registers, 16 bytes a lane from 32 rows at once, one token over 151936 x 2048
+// took 60 us).  Two workgroups of four waves share a compute unit.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx_mfma.h"
+
+namespace flce {
+
+namespace {
+
+// A workgroup of RW x KW = 4 waves takes 32 RW vocabulary rows; wave (rw, kw) multiplies rows
+// 32 rw .. + 31 over every KW-th 256 K, and the KW partial products meet in LDS at the end
+// (fewer rows a workgroup where the vocabulary is too small to fill the chip otherwise).  XR
+// token rows are staged (8, or 32 TB).
+template <int RW_, int KW_, int XR_>
+struct StreamCfg {
+  static constexpr int RW = RW_, KW = KW_, XR = XR_;
+  static constexpr int TB = XR <= 32 ? 1 : XR / 32;       // 32-token blocks
+  static constexpr int ROWS = 32 * RW, NS = 3;            // vocabulary rows; stages
+  static constexpr int W_BYTES = KW * ROWS * 128, X_BYTES = KW * XR * 128;
+  static constexpr int STAGE = W_BYTES + X_BYTES;
+  static constexpr int W_LOADS = W_BYTES / 4096;                       // a wave, 1 KiB each
+  static constexpr int X_LOADS = (X_BYTES + 4095) / 4096;
+  static constexpr int LOADS = W_LOADS + X_LOADS;
+  // scales: 64 bytes of a row (8 steps) at a time, double-buffered
+  static constexpr int SCALE_ROWS = ROWS + (XR < 16 ? 16 : XR);
+  static constexpr int SCALE_BUF = SCALE_ROWS * 64;
+  static constexpr int SCALE_LOADS = (SCALE_ROWS / 16 + 3) / 4;        // a wave, at most
+  static constexpr int LDS = NS * STAGE + 2 * SCALE_BUF;
+  static constexpr int MB = 1, NB = TB;  // as lane_col_max and lane_col_sums name them
+  static_assert(RW * KW == 4 && W_BYTES == 16384, "four waves");
+  static_assert(LDS <= 160 * 1024, "LDS");
+};
+
+// acc[0][tb]: the wave's 32 vocabulary rows x token block tb, as (A = W, B = X) for the
+// log-probs (a lane then holds 16 vocabulary rows of one token) and as (A = X, B = W) for the
+// logits (a lane holds one vocabulary column, so a store covers 128 contiguous bytes of a
+// row).  Summed over the KW waves of the same rows, in order, in the waves with kw = 0.
+template <class C, bool LOGITS>
+__device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* smem, const MxOperand& x,
+                                               const MxOperand& w, int M, int H, int V, int v0) {
+  constexpr int RW = C::RW, KW = C::KW, TB = C::TB, NS = C::NS;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rw = wave % RW, kw = wave / RW;
+  const uint32_t ld = (uint32_t)mx_code_bytes(H, kMxFp4);
+  const int blocks = (int)mx_blocks(H), steps = (blocks + 7) / 8, nk = (steps + KW - 1) / KW;
+  const uint32_t lds0 = lds_addr_of(smem);
+  const i32x4 wr = make_rsrc_fixed(w.codes + (long)v0 * ld), xr = make_rsrc_fixed(x.codes);
+  const int wvalid = V - v0;
+
+  // loads of stage k (steps KW k .. + KW - 1): load i covers rows 8 (i % n) .. + 7 of step
+  // KW k + i / n; lane l row l / 8, the chunk whose position is l % 8
+  const int lr = lane >> 3, lp = lane & 7;
+  auto issue = [&](int k, int slot) {
+    const uint32_t st = lds0 + (uint32_t)(slot * C::STAGE);
+#pragma unroll
+    for (int q = 0; q < C::W_LOADS; ++q) {
+      const int i = wave * C::W_LOADS + q, sub = i / (C::ROWS / 8), r = 8 * (i % (C::ROWS / 8)) + lr;
+      const int b = 8 * (KW * k + sub) + (lp ^ mx_swz(r));
+      const bool ok = r < wvalid && b < blocks;
+      dma16<0>(wr, ok ? (uint32_t)r * ld + 16u * (uint32_t)b : OOB_OFFSET, 0u, st + 1024u * (uint32_t)i);
+    }
+#pragma unroll
+    for (int q = 0; q < C::X_LOADS; ++q) {
+      const int i = wave * C::X_LOADS + q, sub = i / (C::XR / 8), r = 8 * (i % (C::XR / 8)) + lr;
+      const int b = 8 * (KW * k + sub) + (lp ^ mx_swz(r));
+      const bool ok = r < M && b < blocks;
+      // (fewer loads than waves: the waves without one repeat it with nothing to bring)
+      if (C::X_BYTES >= 4096 || i < C::X_BYTES / 1024)
+        dma16<0>(xr, ok ? (uint32_t)r * ld + 16u * (uint32_t)b : OOB_OFFSET, 0u,
+                 st + (uint32_t)C::W_BYTES + 1024u * (uint32_t)i);
+      else
+        dma16<0>(xr, OOB_OFFSET, 0u, lds0 + (uint32_t)(C::NS * C::STAGE + 2 * C::SCALE_BUF));
+    }
+  };
+  // scales of steps 8 c .. 8 c + 7: lane l row l / 4, 16-byte piece l % 4
+  const int pieces = (int)(mx_scale_bytes(H) / 16);
+  const i32x4 ws = make_rsrc_fixed(w.scales + mx_scale_row(w.layout, v0)), xs = make_rsrc_fixed(x.scales);
+  const uint32_t sld = (uint32_t)mx_scale_bytes(H);
+  auto issue_scales = [&](int c) {
+    const uint32_t buf = lds0 + (uint32_t)(NS * C::STAGE + (c & 1) * C::SCALE_BUF);
+#pragma unroll
+    for (int q = 0; q < C::SCALE_LOADS; ++q) {
+      const int i = 4 * q + wave;  // wave-uniform
+      if (i < C::SCALE_ROWS / 16) {
+        const bool is_w = i < C::ROWS / 16;
+        const int r = 16 * (is_w ? i : i - C::ROWS / 16) + (lane >> 2), p = 4 * c + (lane & 3);
+        const bool ok = r < (is_w ? wvalid : M) && p < pieces;
+        dma16<0>(is_w ? ws : xs, ok ? (uint32_t)r * sld + 16u * (uint32_t)p : OOB_OFFSET, 0u,
+                 buf + 1024u * (uint32_t)i);
+      }
+    }
+  };
+
+  // fragments: the wave's row of W and of each token block (rows past XR repeat earlier ones)
+  const int half = lane >> 5, r = lane & 31;
+  uint32_t wf[4], xf[4];
+  const int xrow = r & (C::XR - 1);
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk) {
+    wf[kk] = (uint32_t)(kw * C::ROWS * 128 + (32 * rw + r) * 128 + (((4 * half + kk) ^ mx_swz(r)) << 4));
+    xf[kk] = (uint32_t)(C::W_BYTES + kw * C::XR * 128 + xrow * 128 + (((4 * half + kk) ^ mx_swz(xrow)) << 4));
+  }
+  const uint32_t wsf = (uint32_t)((32 * rw + r) * 64 + 4 * half);
+  const uint32_t xsf = (uint32_t)((C::ROWS + xrow) * 64 + 4 * half);
+#pragma unroll
+  for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[0][tb][e] = 0.f;
+
+  issue_scales(0);
+#pragma unroll
+  for (int k = 0; k < NS - 1; ++k) issue(k, k);
+  int slot = 0;
+  for (int k = 0; k < nk; ++k) {
+    // stage k has landed (the loads of the NS - 2 stages after it may be in flight), and
+    // every wave is done with stage k - 1, whose slot the next loads take
+    wait_vmcnt<C::LOADS*(NS - 2)>();
+    __syncthreads();
+    const int c = KW * k / 8;
+    if (KW * k % 8 == 0) issue_scales(c + 1);
+    issue(k + NS - 1, slot == 0 ? NS - 1 : slot - 1);
+    const char* st = smem + slot * C::STAGE;
+    const char* sb = smem + NS * C::STAGE + (c & 1) * C::SCALE_BUF + 8 * ((KW * k + kw) & 7);
+    const int sw = *reinterpret_cast<const int*>(sb + wsf);
+    u32x4 wv[4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) wv[kk] = *reinterpret_cast<const u32x4*>(st + wf[kk]);
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) {
+      const int sx = *reinterpret_cast<const int*>(sb + xsf + 2048 * tb);
+      u32x4 xv[4];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) xv[kk] = *reinterpret_cast<const u32x4*>(st + xf[kk] + 4096 * tb);
+      if constexpr (LOGITS) {
+        acc[0][tb] = mx_mfma<0>(xv[0], wv[0], acc[0][tb], sx, sw);
+        acc[0][tb] = mx_mfma<1>(xv[1], wv[1], acc[0][tb], sx, sw);
+        acc[0][tb] = mx_mfma<2>(xv[2], wv[2], acc[0][tb], sx, sw);
+        acc[0][tb] = mx_mfma<3>(xv[3], wv[3], acc[0][tb], sx, sw);
+      } else {
+        acc[0][tb] = mx_mfma<0>(wv[0], xv[0], acc[0][tb], sw, sx);
+        acc[0][tb] = mx_mfma<1>(wv[1], xv[1], acc[0][tb], sw, sx);
+        acc[0][tb] = mx_mfma<2>(wv[2], xv[2], acc[0][tb], sw, sx);
+        acc[0][tb] = mx_mfma<3>(wv[3], xv[3], acc[0][tb], sw, sx);
+      }
+    }
+    slot = slot == NS - 1 ? 0 : slot + 1;
+  }
+  // the zero fills of the stages past the end must land before the LDS is used again
+  wait_vmcnt<0>();
+  __syncthreads();
+  if constexpr (KW > 1) {
+    float* join = reinterpret_cast<float*>(smem);  // [kw - 1][rw][tb][e][lane]
+    if (kw > 0) {
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          join[(((kw - 1) * RW + rw) * TB + tb) * 1024 + 64 * e + lane] = acc[0][tb][e];
+    }
+    __syncthreads();
+    if (kw == 0) {
+#pragma unroll
+      for (int j = 0; j < KW - 1; ++j)
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[0][tb][e] += join[((j * RW + rw) * TB + tb) * 1024 + 64 * e + lane];
+    }
+  }
+}
+
+// The staging LDS, and a kilobyte that loads with nothing to bring may zero.
+template <class C>
+constexpr int stream_lds = C::LDS + (C::X_BYTES < 4096 ? 1024 : 0);
+
+template <class C, class T>
+__global__ __launch_bounds__(256) void mx_stream_logits_kernel(MxLogitsArgs p) {
+  __shared__ __attribute__((aligned(1024))) char smem[stream_lds<C>];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int v0 = (int)blockIdx.x * C::ROWS;
+  f32x16 acc[1][C::TB];
+  stream_product<C, true>(acc, smem, p.x, p.w, p.M, p.H, p.V, v0);
+  const int v = v0 + 32 * (wave % C::RW) + (lane & 31);
+  if (wave / C::RW != 0 || v >= p.V) return;
+  typename T::mem* out = static_cast<typename T::mem*>(p.out) + v;
+#pragma unroll
+  for (int tb = 0; tb < C::TB; ++tb)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int m = 32 * tb + acc_row(lane, e);
+      if (m < p.M) out[(long)m * p.ldo] = T::from_f32(p.scale * acc[0][tb][e]);
+    }
+}
+
+// Partials of the workgroup's vocabulary rows: maximum, then the shifted sums, each over the
+// lane's 16 rows, the two half-waves and the RW waves.
+template <class C, bool ENT>
+__global__ __launch_bounds__(256) void mx_stream_fwd_kernel(MxFwdArgs p) {
+  constexpr int RW = C::RW, TB = C::TB, TT = 32 * TB;
+  __shared__ __attribute__((aligned(1024))) char smem[stream_lds<C>];
+  static_assert((3 * RW + (C::KW - 1) * RW * 32) * TT * 4 <= C::LDS, "epilogue buffers");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rw = wave % RW, kw = wave / RW, lc = lane & 31;
+  const int v0 = (int)blockIdx.x * C::ROWS;
+  f32x16 acc[1][TB];
+  stream_product<C, false>(acc, smem, p.x, p.w, p.M, p.H, p.V, v0);
+  // [rw][token] maxima and sums, behind what the KW waves exchanged
+  float* red = reinterpret_cast<float*>(smem) + (C::KW - 1) * RW * TB * 1024;
+  float* comb = red + RW * TT;
+  const float c1 = p.scale * LOG2E, ac1 = fabsf(c1);
+  const int vrows = p.V - v0 - 32 * rw;  // of the wave; those past it are masked
+  if (kw == 0) {
+    float mx[TB];
+    if (c1 >= 0.f) lane_col_max<false, true, C>(acc, lane, vrows, mx);
+    else lane_col_max<true, true, C>(acc, lane, vrows, mx);
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) {
+      const float m = halves_reduce(mx[tb], mx[tb], [](float x, float y) { return max_raw(x, y); });
+      if (lane < 32) red[rw * TT + 32 * tb + lc] = m;
+    }
+  }
+  __syncthreads();
+  if (kw == 0) {
+    float nm2[TB], sv[TB], uv[TB];
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) {
+      float m = red[32 * tb + lc];
+#pragma unroll
+      for (int k = 1; k < RW; ++k) m = fmaxf(m, red[k * TT + 32 * tb + lc]);
+      nm2[tb] = -ac1 * m;
+    }
+    lane_col_sums<ENT, true, C>(acc, lane, vrows, c1, nm2, sv, uv);
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) {
+      const float s = halves_reduce(sv[tb], sv[tb], [](float x, float y) { return x + y; });
+      const float u = halves_reduce(uv[tb], uv[tb], [](float x, float y) { return x + y; });
+      if (lane < 32) {
+        comb[rw * TT + 32 * tb + lc] = s;
+        comb[(RW + rw) * TT + 32 * tb + lc] = u;
+      }
+    }
+  }
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t < TT && t < p.M) {
+    float m = red[t], s = comb[t], u = comb[RW * TT + t];
+#pragma unroll
+    for (int k = 1; k < RW; ++k) {
+      m = fmaxf(m, red[k * TT + t]);
+      s += comb[k * TT + t];
+      u += comb[(RW + k) * TT + t];
+    }
+    const long off = (long)blockIdx.x * p.tile_stride + t * p.token_stride;
+    p.part_m[off] = ac1 * m * LN2;
+    p.part_s[off] = s;
+    if constexpr (ENT) p.part_u[off] = u * LN2;
+  }
+}
+
+// The configuration for a call: `rows` is mx_stream_rows of it.
+template <int XR, class F>
+void with_cfg(int rows, F f) {
+  if (rows == 128) f(StreamCfg<4, 1, XR>());
+  if constexpr (XR <= 64) {
+    if (rows == 64) f(StreamCfg<2, 2, XR>());
+  }
+  if constexpr (XR <= 32) {
+    if (rows == 32) f(StreamCfg<1, 4, XR>());
+  }
+}
+template <class F>
+void with_tokens(int M, int rows, F f) {
+  if (M <= 8) with_cfg<8>(rows, f);
+  else if (M <= 32) with_cfg<32>(rows, f);
+  else if (M <= 64) with_cfg<64>(rows, f);
+  else with_cfg<128>(rows, f);
+}
+
+// ---------------------------------------------------------------------------
+// Merge: per token, the target logit as a dot product of codes, then m* = max m_j,
+// S = sum s_j e^(m_j - m*), U = sum e^(m_j - m*) (u_j + (m_j - m*) s_j) over the vocabulary
+// tiles j; lse = m* + log S, logprob = min(z_t - lse, 0), entropy = max(log S - U / S, 0) (the
+// bounds hold exactly: fp32 rounding can put a value next to one a few ulps past it).
+// ROWS tokens a workgroup: 16 where the tokens of a vocabulary tile are contiguous (64-byte
+// pieces, and a token's tiles over 32 threads), one where its tiles are.
+constexpr int MERGE_THREADS = 512;
+template <int ROWS, bool ENT>
+__global__ __launch_bounds__(MERGE_THREADS) void mx_merge_kernel(MxFwdArgs p) {
+  constexpr int SLICES = MERGE_THREADS / ROWS, WAVES = MERGE_THREADS / 64;
+  __shared__ float sm[2][SLICES][ROWS];
+  __shared__ float zt[ROWS < WAVES ? WAVES : ROWS];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const long row0 = (long)blockIdx.x * ROWS;
+  const long code_ld = mx_code_bytes(p.H, kMxFp4);
+  auto scale = [](const MxOperand& o, long r, int b) {
+    return mx_scale(o.scales[mx_scale_row(o.layout, r) + (b >> 4) * o.layout.quad_stride + (b & 15)]);
+  };
+  // target logits: a wave a token (one token: its blocks over all waves); a block's sum of
+  // code products is exact, its two scales multiply it once
+  for (int i = ROWS == 1 ? 0 : wave; i < ROWS; i += WAVES) {
+    const long row = row0 + i;
+    const int64_t t = row < p.M ? p.targets[row] : -1;
+    float s = 0.f;
+    if (row < p.M && t != p.ignore_index && t >= 0 && t < p.V) {
+      for (int b = ROWS == 1 ? (int)threadIdx.x : lane; b < (int)mx_blocks(p.H);
+           b += ROWS == 1 ? MERGE_THREADS : 64) {
+        const u32x4 xc = *reinterpret_cast<const u32x4*>(p.x.codes + row * code_ld + 16l * b);
+        const u32x4 wc = *reinterpret_cast<const u32x4*>(p.w.codes + t * code_ld + 16l * b);
+        float d = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float xv[8], wv[8];
+          mx_decode<kMxFp4>(u32x2_t{xc[k], 0u}, 127u, xv);
+          mx_decode<kMxFp4>(u32x2_t{wc[k], 0u}, 127u, wv);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d = fmaf(xv[j], wv[j], d);
+        }
+        s = fmaf(d * scale(p.x, row, b), scale(p.w, t, b), s);
+      }
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+    if (lane == 0) zt[ROWS == 1 ? wave : i] = s * p.scale;
+  }
+  const int lr = threadIdx.x % ROWS, sl = threadIdx.x / ROWS;
+  const long row = row0 + lr;
+  const bool live = row < p.M;
+  const float* pm = p.part_m + row * p.token_stride;
+  const float* ps = p.part_s + row * p.token_stride;
+  float m = -INFINITY;
+  if (live) {
+#pragma unroll 4
+    for (int j = sl; j < p.n_vt; j += SLICES) m = fmaxf(m, pm[j * p.tile_stride]);
+  }
+  sm[0][sl][lr] = m;
+  __syncthreads();
+#pragma unroll
+  for (int n = SLICES / 2; n > 0; n /= 2) {
+    if (sl < n) sm[0][sl][lr] = fmaxf(sm[0][sl][lr], sm[0][sl + n][lr]);
+    __syncthreads();
+  }
+  const float top = sm[0][0][lr];
+  __syncthreads();
+  float S = 0.f, U = 0.f;
+  if (live) {
+#pragma unroll 4
+    for (int j = sl; j < p.n_vt; j += SLICES) {
+      const float dm = pm[j * p.tile_stride] - top;
+      const float a = __expf(dm), s = ps[j * p.tile_stride];
+      S += s * a;
+      if constexpr (ENT) U += a * (p.part_u[row * p.token_stride + j * p.tile_stride] + dm * s);
+    }
+  }
+  sm[0][sl][lr] = S;
+  sm[1][sl][lr] = U;
+  __syncthreads();
+#pragma unroll
+  for (int n = SLICES / 2; n > 0; n /= 2) {
+    if (sl < n) {
+      sm[0][sl][lr] += sm[0][sl + n][lr];
+      if constexpr (ENT) sm[1][sl][lr] += sm[1][sl + n][lr];
+    }
+    __syncthreads();
+  }
+  if (sl != 0 || !live) return;
+  const float logS = logf(sm[0][0][lr]);
+  const int64_t t = p.targets[row];
+  const bool valid = t != p.ignore_index && t >= 0 && t < p.V;
+  float z = zt[lr];
+  if constexpr (ROWS == 1) {
+#pragma unroll
+    for (int k = 1; k < WAVES; ++k) z += zt[k];
+  }
+  p.lse[row] = top + logS;
+  p.logprob[row] = valid ? fminf(z - (top + logS), 0.f) : 0.f;
+  if constexpr (ENT) p.entropy[row] = valid ? fmaxf(logS - sm[1][0][lr] / sm[0][0][lr], 0.f) : 0.f;
+}
+
+}  // namespace
+
+// Fewer vocabulary rows a workgroup, with the waves sharing K instead, where 128 would leave
+// less than one and a half workgroups a compute unit (as far as the staged tokens fit).
+int mx_stream_rows(int M, int V) {
+  if (M > 64 || (V + 127) / 128 >= 384) return 128;
+  if (M > 32 || (V + 63) / 64 >= 384) return 64;
+  return 32;
+}
+
+hipError_t launch_mx_stream_logits(const MxLogitsArgs& a, hipStream_t s) {
+  const int rows = mx_stream_rows(a.M, a.V);
+  const unsigned g = (unsigned)(((int64_t)a.V + rows - 1) / rows);
+  with_tokens(a.M, rows, [&](auto cfg) {
+    using C = decltype(cfg);
+    if (a.out_dtype == kBf16) mx_stream_logits_kernel<C, Bf16><<<g, 256, 0, s>>>(a);
+    else mx_stream_logits_kernel<C, F32><<<g, 256, 0, s>>>(a);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_stream_fwd(const MxFwdArgs& a, hipStream_t s) {
+  with_tokens(a.M, mx_stream_rows(a.M, a.V), [&](auto cfg) {
+    using C = decltype(cfg);
+    if (a.part_u) mx_stream_fwd_kernel<C, true><<<(unsigned)a.n_vt, 256, 0, s>>>(a);
+    else mx_stream_fwd_kernel<C, false><<<(unsigned)a.n_vt, 256, 0, s>>>(a);
+  });
+  return hipGetLastError();
+}
+
+template <int ROWS>
+static void merge_rows(const MxFwdArgs& a, hipStream_t s) {
+  const unsigned g = (unsigned)(((long)a.M + ROWS - 1) / ROWS);
+  if (a.part_u) mx_merge_kernel<ROWS, true><<<g, MERGE_THREADS, 0, s>>>(a);
+  else mx_merge_kernel<ROWS, false><<<g, MERGE_THREADS, 0, s>>>(a);
+}
+
+hipError_t launch_mx_merge(const MxFwdArgs& a, hipStream_t s) {
+  if (a.tile_stride == 1) merge_rows<1>(a, s);
+  else merge_rows<16>(a, s);
+  return hipGetLastError();
+}
+
+}  // namespace flce

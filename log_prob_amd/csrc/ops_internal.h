@@ -99,6 +99,7 @@ struct MxQuantArgs {
   long rows;
   long cols;
   MxScaleLayout layout;
+  unsigned long long* clear;  // quantise: 8 counters to zero for a later launch, or nullptr
 };
 hipError_t launch_mx_quantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s);
@@ -120,18 +121,34 @@ struct MxLogitsArgs {
   void* out;               // [M, V] logits
   long ldo;
   int out_dtype;
-  int n_mt, n_vt;
-  bool stream;
+  int n_mt, n_vt;          // 256 x 256 tiles (the tile kernel)
 };
-hipError_t launch_mx_logits(const MxLogitsArgs& a, hipStream_t s);
-// Log-prob partials: f holds the outputs and sizes (f.X and f.W unused).
+
+// Log-prob partials: entry (vocabulary tile j, token m) of each array at j * tile_stride +
+// m * token_stride.
 struct MxFwdArgs {
   MxOperand x, w;
-  FwdTileArgs f;
-  bool stream;             // the kernel for few tokens: chosen for the whole call, so that a
-                           // token wave does not change its rows' bits
+  const int64_t* targets;
+  int M, H, V;
+  int64_t ignore_index;
+  float scale;
+  int n_mt, n_vt;          // n_vt: vocabulary tiles that leave partials
+  long tile_stride, token_stride;
+  float* part_m;
+  float* part_s;
+  float* part_u;           // nullptr without entropy
+  float* logprob;
+  float* lse;
+  float* entropy;
 };
-hipError_t launch_mx_fwd_tile(const MxFwdArgs& a, bool entropy, hipStream_t s);
-hipError_t launch_mx_target_logit(const MxFwdArgs& a, hipStream_t s);
+
+// The kernels for few tokens: vocabulary rows a workgroup takes, for a call of M tokens.
+int mx_stream_rows(int M, int V);
+hipError_t launch_mx_stream_logits(const MxLogitsArgs& a, hipStream_t s);
+hipError_t launch_mx_stream_fwd(const MxFwdArgs& a, hipStream_t s);
+hipError_t launch_mx_tile_logits(const MxLogitsArgs& a, hipStream_t s);
+hipError_t launch_mx_tile_fwd(const MxFwdArgs& a, TileQueue tq, hipStream_t s);
+// Target logits and the merge of the partials into logprob, lse and entropy.
+hipError_t launch_mx_merge(const MxFwdArgs& a, hipStream_t s);
 
 }  // namespace flce

@@ -161,7 +161,16 @@ def test_mx_workspace():
     # X's copy: 32 bytes of codes and 16 of scales a row, each part rounded up to 256
     lo, fw = flce.mxfp4_workspace_query(4, 64, 100)
     assert lo == 512
-    assert fw == 512 + flce.workspace_query(4, 64, 100, True)[0]
+    # the partials of 4 workgroups of 32 vocabulary rows for 4 tokens, 3 arrays, and counters
+    assert fw == 512 + 3 * 256 + 256
+    # larger calls: 256-column tiles of 256-row multiples; whole scale tiles of X
+    lo, fw = flce.mxfp4_workspace_query(300, 64, 1000, False)
+    assert lo == 300 * 32 + 128 + 512 * 16
+    assert fw == lo + 2 * 4 * 4 * 512 + 256
+    # and past 2.5e11 products a copy of W's scales
+    lo, _ = flce.mxfp4_workspace_query(4096, 4096, 32768)
+    assert lo == 32768 * 128 + 4096 * (2048 + 128)
+    lo, fw = flce.mxfp4_workspace_query(4, 64, 100)
     assert flce.mxfp4_workspace_query(0, 64, 100) == (0, 0)
     assert mx_forward(wb=fw - 1) == TOO_SMALL and logits(wb=lo - 1) == TOO_SMALL
     assert mx_forward(M=0, X=None, t=None, lp=None, lse=None, en=None, work=None, wb=0) == 0
