@@ -292,7 +292,8 @@ void with_tokens(int M, int rows, F f) {
 // tiles j; lse = m* + log S, logprob = min(z_t - lse, 0), entropy = max(log S - U / S, 0) (the
 // bounds hold exactly: fp32 rounding can put a value next to one a few ulps past it).
 // ROWS tokens a workgroup: 16 where the tokens of a vocabulary tile are contiguous (64-byte
-// pieces, and a token's tiles over 32 threads), one where its tiles are.
+// pieces, and a token's tiles over 32 threads), or 4 where that would leave most of the chip
+// idle; one where a token's tiles are contiguous.
 constexpr int MERGE_THREADS = 512;
 template <int ROWS, bool ENT>
 __global__ __launch_bounds__(MERGE_THREADS) void mx_merge_kernel(MxFwdArgs p) {
@@ -425,6 +426,7 @@ static void merge_rows(const MxFwdArgs& a, hipStream_t s) {
 
 hipError_t launch_mx_merge(const MxFwdArgs& a, hipStream_t s) {
   if (a.tile_stride == 1) merge_rows<1>(a, s);
+  else if (a.M <= 1024) merge_rows<4>(a, s);
   else merge_rows<16>(a, s);
   return hipGetLastError();
 }

@@ -253,10 +253,11 @@ __device__ __forceinline__ void mx_mainloop(f32x16 (&acc)[4][4], char* smem, con
     step(Stage0(), Fast(), kt);
     step(Stage1(), Fast(), kt + 1);
   }
-  for (; kt < nk; kt += 2) {
+  for (; kt + 1 < nk; kt += 2) {
     step(Stage0(), Slow(), kt);
     step(Stage1(), Slow(), kt + 1);
   }
+  if (kt < nk) step(Stage0(), Slow(), kt);
   // the zero fills issued under the last steps must land before the caller reuses LDS
   wait_vmcnt<0>();
   __syncthreads();
@@ -336,7 +337,7 @@ __global__ __launch_bounds__(256, 1) void mx_tile_logits_kernel(MxLogitsArgs p) 
         const int r = it * RPI + lane / CH, c = lane % CH;
         const u32x4 v = *reinterpret_cast<const u32x4*>(slice + r * RB + ((c ^ (r & (CH - 1))) << 4));
         const int t = t0 + 32 * nb + r, col = v0 + c * (16 / ES);
-        if (t < p.M && col < p.V) *reinterpret_cast<u32x4*>(out + (long)t * p.ldo + col) = v;
+        if (t < p.M && col < p.V) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out + (long)t * p.ldo + col));
       }
     } else {
       for (int it = 0; it < 64; ++it) {
