@@ -1,0 +1,270 @@
+"""The operators around the head as they are used together: a training step through norm,
+head and loss; scoring and sampling with a 4-bit head; captured graphs and streams."""
+import numpy as np
+import pytest
+
+from oracle import flce_ref as ref
+from oracle import ops_ref as ops
+from synth import inputs
+from tests import gpu_util as gu
+from tests import ops_util as ou
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+
+
+def norm_case(M, H, seed, dtype="float32"):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    x = (2 * n(M, H) + 0.5 * n(M, 1)).to(getattr(torch, dtype))
+    return x, 1 + 0.1 * n(H), 0.1 * n(H)
+
+
+@pytest.mark.parametrize("checkpoint", [None, "mxfp8", "mxint8"])
+def test_training_step(checkpoint):
+    """An fp32 residual stream through norm and head to the mean NLL, all by autograd; dx,
+    dweight, dbias against the fp64 chain (the norm's output and the head's gradient in bf16,
+    as the head has them) within the head's own tolerance."""
+    import torch
+    from log_prob_amd import autograd
+    M, H, V = 700, 264, 1500
+    c = inputs.make_case("together", 501, M, H, V, ignore_frac=0.1, grad_mode="none")
+    _, W, t, _, _ = gu.to_dev(c)
+    x, w, b = (v.requires_grad_() for v in norm_case(M, H, 3))
+    y = autograd.layer_norm(x, w, b, EPS, torch.bfloat16, checkpoint)
+    lp = autograd.linear_logprob(y, W, t, c.ignore_index)
+    n = int((t != c.ignore_index).sum())
+    (-lp.sum() / n).backward()
+
+    x64 = ou.np64(x)
+    y64, mean, rstd = ops.layer_norm(x64, ou.np64(w), ou.np64(b), EPS)
+    ybits = torch.from_numpy(y64).float().bfloat16()
+    glp = np.full(M, -1.0 / n, np.float32)
+    dy, _ = ref.backward(gu.bf16_bits(ybits), c.W, c.targets, c.ignore_index, 1.0, glp, None)
+    seen = x64 if checkpoint is None else ops.rounded(x64, checkpoint)
+    want = ops.layer_norm_grad(dy, seen, mean, rstd, ou.np64(w))
+    for name, got, r in zip(("dx", "dweight", "dbias"), (x.grad, w.grad, b.grad), want):
+        assert got.dtype == torch.float32
+        assert gu.rel_max(ou.np64(got), r) <= gu.GRAD_RTOL, name
+    assert lp.shape == (M,) and float(lp.detach().max()) <= 0
+
+
+@pytest.mark.parametrize("checkpoint", [None, "mxint8"])
+def test_layer_norm_autograd(checkpoint):
+    """Three axes, an expanded gradient, parameters that need none."""
+    import torch
+    from log_prob_amd import autograd, flce
+    x, w, b = norm_case(24, 136, 5, "bfloat16")
+    x = x.view(2, 3, 4, 136).requires_grad_()
+    w = w.bfloat16().requires_grad_()
+    y = autograd.layer_norm(x, w, b.bfloat16(), EPS, checkpoint=checkpoint)
+    assert y.shape == x.shape and y.dtype == torch.bfloat16
+    y.sum().backward()   # the gradient is one element, expanded
+    rows = x.detach().view(-1, 136)
+    _, mean, rstd, *kept = flce.layer_norm_forward(rows, w, b.bfloat16(), EPS, checkpoint=checkpoint)
+    dx, dw, _ = flce.layer_norm_backward(torch.ones_like(rows), kept[0] if kept else rows, mean, rstd, w)
+    assert torch.equal(x.grad.view(-1, 136), dx) and torch.equal(w.grad, dw)
+    # without parameters, and with a bias alone
+    z = autograd.layer_norm(x, None, None, EPS, checkpoint=checkpoint)
+    z.float().square().sum().backward()
+    bias = b.bfloat16().requires_grad_()
+    autograd.layer_norm(x.detach(), None, bias, EPS, checkpoint=checkpoint).sum().backward()
+    assert bias.grad.dtype == torch.bfloat16 and (bias.grad == 24).all()
+
+
+def test_layer_norm_gradient_against_differences():
+    """The gradient along random directions against central differences of the fp64 norm."""
+    import torch
+    from log_prob_amd import autograd
+    x, w, b = norm_case(5, 40, 6)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dy = torch.randn(5, 40, generator=gen, device="cuda")
+    args = [v.requires_grad_() for v in (x, w, b)]
+    (autograd.layer_norm(*args, EPS) * dy).sum().backward()
+    f = lambda *a: float((ops.layer_norm(*a, EPS)[0] * ou.np64(dy)).sum())
+    rng = np.random.default_rng(2)
+    base = [ou.np64(v) for v in args]
+    h = 1e-5
+    for k, v in enumerate(args):
+        d = rng.standard_normal(base[k].shape)
+        lo, hi = list(base), list(base)
+        lo[k], hi[k] = base[k] - h * d, base[k] + h * d
+        want = (f(*hi) - f(*lo)) / (2 * h)
+        got = float((ou.np64(v.grad) * d).sum())
+        # fp32 gradients of about 40 roundings each; differences good to h^2
+        scale = float(np.abs(ou.np64(v.grad) * d).sum())
+        assert abs(got - want) <= 64 * ou.U32 * scale + 1e-7 * abs(want) + 1e-7
+
+
+def test_scoring_and_sampling():
+    """A step of a rollout: norm, then logits of the last token and log-probs of the batch with
+    the 4-bit head, and the policy loss on them; the log-probs against the fp64 chain."""
+    import torch
+    from log_prob_amd import flce
+    M, H, V = 300, 264, 1300
+    x, w, b = norm_case(M, H, 7, "bfloat16")
+    w, b = w.bfloat16(), b.bfloat16()
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    W = flce.mx_quantize((torch.randn(V, H, generator=gen, device="cuda") / H ** 0.5).bfloat16(), "mxfp4")
+    t = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    y, _, _ = flce.layer_norm_forward(x, w, b, EPS)
+    old, lse, _ = flce.mxfp4_forward(y, W, t)
+    z = flce.mxfp4_logits(y, W, out_dtype=torch.float32)
+    last = flce.mxfp4_logits(y[-1:].contiguous(), W, out_dtype=torch.float32)
+    # one softmax, two ways to it: sums of 264 products in different orders
+    Wv = ou.np64(flce.mx_dequantize(W, torch.float32))
+    Xv = ops.rounded(ou.np64(y), "mxfp4")
+    e = (H + 2) * 2 * ou.U32 * (np.abs(Xv) @ np.abs(Wv).T)
+    assert (np.abs(ou.np64(last)[0] - ou.np64(z)[-1]) <= 2 * e[-1]).all()
+    want = ops.fp4_forward(ou.np64(y), Wv, t.cpu().numpy())
+    assert np.abs(ou.np64(old) - want["logprob"]).max() <= gu.FWD_ATOL
+    assert np.abs(ou.np64(lse) - want["lse"]).max() <= gu.FWD_ATOL
+    adv = torch.randn(M, generator=gen, device="cuda")
+    per_tok, clipped, out = flce.policy_loss_reduce(old, old, adv, t, V)
+    assert torch.equal(per_tok, -adv) and not clipped.any()   # the same policy: ratio 1
+
+
+@pytest.mark.parametrize("M,H,V", [(40, 264, 1500), (300, 264, 1500), (4096, 256, 32800)],
+                         ids=["stream", "tile", "queued_tiles"])
+def test_graph_replays_match_eager(M, H, V):
+    """A training step around the head and a pass of the 4-bit head in one captured graph,
+    replayed with eager work and synchronisation between."""
+    import torch
+    from log_prob_amd import flce
+    x, w, b = norm_case(M, H, 9)
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    W = (torch.randn(V, H, generator=gen, device="cuda") / H ** 0.5).bfloat16()
+    t = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    cb, sb = flce.mx_sizes(H, "mxint8")
+    fb, sf = flce.mx_sizes(H, "mxfp4")
+    u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device="cuda")
+    f32 = lambda *s: torch.empty(*s, device="cuda")
+    y = torch.empty(M, H, dtype=torch.bfloat16, device="cuda")
+    kept = flce.MXTensor(u8(M, cb), u8(M, sb), "mxint8", H)
+    Wq = flce.MXTensor(u8(V, fb), u8(V, sf), "mxfp4", H)
+    mean, rstd, lp, lse, g = (f32(M) for _ in range(5))
+    qlp, qlse, qent = (f32(M) for _ in range(3))
+    red = torch.empty(3, dtype=torch.float64, device="cuda")
+    dy, dW = torch.empty_like(y), torch.empty_like(W)
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty_like(b)
+    z = torch.empty(M, V, dtype=torch.bfloat16, device="cuda")
+    ws = u8(max(*flce.workspace_query(M, H, V, False), *flce.mxfp4_workspace_query(M, H, V),
+                flce.layer_norm_backward_workspace(M, H)))
+    outs = (y, kept.codes, kept.scales, Wq.codes, Wq.scales, mean, rstd, lp, lse, red, dy, dW, dx, dw,
+            db, z, qlp, qlse, qent)
+
+    def step():
+        flce.layer_norm_forward(x, w, b, EPS, checkpoint="mxint8", out=(y, mean, rstd, kept))
+        flce.forward(y, W, t, compute_entropy=False, workspace=ws, out=(lp, lse, None))
+        flce.nll_reduce(lp, t, V, out=red)
+        flce.nll_mean_grad(t, V, red, out=g)
+        flce.backward(y, W, t, lse, None, g, workspace=ws, out=(dy, dW))
+        flce.layer_norm_backward(dy, kept, mean, rstd, w, dx_dtype=x.dtype, workspace=ws, out=(dx, dw, db))
+        flce.mx_quantize(W, "mxfp4", out=Wq)
+        flce.mxfp4_logits(y, Wq, workspace=ws, out=z)
+        flce.mxfp4_forward(y, Wq, t, workspace=ws, out=(qlp, qlse, qent))
+
+    step()
+    torch.cuda.synchronize()
+    want = [v.clone() for v in outs]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(4):
+        for v in outs:
+            v.zero_()
+        ws.fill_(0xFF)
+        junk = (x @ x.T).sum()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, (a, r) in enumerate(zip(outs, want)):
+            assert torch.equal(a, r), f"replay {i}: output {k} differs"
+        del junk
+
+
+def test_two_streams_side_by_side():
+    """The same calls on two streams at once, each with its own outputs and workspaces."""
+    import torch
+    from log_prob_amd import flce
+    M, H, V = 600, 520, 3000
+    sets = []
+    for seed in (20, 21):
+        x, w, b = norm_case(M, H, seed, "bfloat16")
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        W = flce.mx_quantize(torch.randn(V, H, generator=gen, device="cuda").bfloat16(), "mxfp4")
+        sets.append((x, w.bfloat16(), b.bfloat16(), W, torch.randint(0, V, (M,), generator=gen, device="cuda")))
+
+    def work(x, w, b, W, t):
+        y, mean, rstd, kept = flce.layer_norm_forward(x, w, b, EPS, checkpoint="mxfp8")
+        out = flce.mxfp4_forward(y, W, t)
+        few = flce.mxfp4_logits(y[:9].contiguous(), W)
+        return (y, few, *out, *flce.layer_norm_backward(y, kept, mean, rstd, w))
+
+    want = [work(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = []
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                got.append(work(*s))
+        torch.cuda.synchronize()
+        for g, r in zip(got, want):
+            for a, e in zip(g, r):
+                assert torch.equal(a, e)
+
+
+def test_refusals():
+    import torch
+    from log_prob_amd import flce
+    x, w, b = norm_case(4, 64, 11)
+    y, mean, rstd = flce.layer_norm_forward(x, w, b)
+    dy = torch.randn_like(y)
+    with pytest.raises(TypeError):
+        flce.layer_norm_forward(x.half(), w.half(), b.half())
+    with pytest.raises(TypeError):
+        flce.layer_norm_forward(x, w, b.bfloat16())
+    with pytest.raises(ValueError):
+        flce.layer_norm_forward(x, w[:63], b)
+    with pytest.raises(ValueError):
+        flce.layer_norm_forward(x, w[::2], b)
+    with pytest.raises(ValueError):
+        flce.layer_norm_forward(x.t(), None, None)
+    with pytest.raises(ValueError):
+        flce.layer_norm_forward(x[0].expand(4, 64), w, b)
+    with pytest.raises(ValueError):
+        flce.layer_norm_forward(x.view(2, 2, 64), w, b)
+    with pytest.raises(ValueError):
+        flce.layer_norm_forward(x, w, b, checkpoint="mxfp4")
+    with pytest.raises(ValueError):
+        flce.layer_norm_forward(x, w.cpu(), b)
+    for bad in (lambda: flce.layer_norm_forward(x.bfloat16(), w, b, out_dtype=torch.float32),
+                lambda: flce.layer_norm_forward(x, w, b, eps=-1.0),
+                lambda: flce.layer_norm_backward(dy, x.bfloat16(), mean, rstd, w),
+                lambda: flce.layer_norm_backward(dy, x, mean, rstd, w,
+                                                 workspace=torch.empty(100, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(flce.FlceError):
+            bad()
+    with pytest.raises(ValueError):
+        flce.layer_norm_backward(dy, x[:3], mean, rstd, w)
+    with pytest.raises(ValueError):
+        flce.layer_norm_backward(dy, x, mean[:3], rstd, w)
+    with pytest.raises(TypeError):
+        flce.layer_norm_backward(dy, x, mean, rstd, w, dx_dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        flce.layer_norm_backward(dy, flce.mx_quantize(x, "mxfp4"), mean, rstd, w)
+    with pytest.raises(ValueError):
+        flce.mx_dequantize(flce.mx_quantize(x, "mxfp8")._replace(cols=65))
+    with pytest.raises(TypeError):
+        flce.mx_dequantize(flce.mx_quantize(x, "mxfp8"), torch.float16)
+    with pytest.raises(TypeError):
+        flce.mx_quantize(x.half(), "mxfp8")
