@@ -495,31 +495,37 @@ class MXTensor(NamedTuple):
     cols: int
 
 
+_DTYPE_IDS = {}   # torch dtype -> flce_dtype_t
+
+
 def _dtype_id(t, name) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return 0
-    if t.dtype == torch.float32:
-        return 1
-    raise TypeError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    d = _DTYPE_IDS.get(t.dtype)
+    if d is None:
+        import torch
+        _DTYPE_IDS.update({torch.bfloat16: 0, torch.float32: 1})
+        d = _DTYPE_IDS.get(t.dtype)
+        if d is None:
+            raise TypeError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    return d
 
 
 def _rows(t, name, dev, shape=None):
     """Check a matrix whose rows are contiguous; returns its row stride."""
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
     if t.device != dev:
         raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
     m, h = t.shape
-    if h > 1 and t.stride(1) != 1:
+    if shape is not None and shape != (m, h):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {(m, h)}")
+    ld, one = t.stride()
+    if one != 1 and h > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     if m <= 1:
         return h
-    if t.stride(0) < h:
+    if ld < h:
         raise ValueError(f"{name}: rows overlap")
-    return t.stride(0)
+    return ld
 
 
 def _on_gpu(t, name):
@@ -529,12 +535,13 @@ def _on_gpu(t, name):
 
 
 def _vector(t, name, dev, dtype, n):
+    if t.dtype == dtype and t.device == dev and t.shape == (n,) and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {n} contiguous elements, got shape {tuple(t.shape)}")
+    raise ValueError(f"{name}: expected {n} contiguous elements, got shape {tuple(t.shape)}")
 
 
 def _launch(dev, fn, *args):
@@ -582,13 +589,15 @@ def _mx_check(q, name, dev, f, rows, cols):
     if q.cols != cols:
         raise ValueError(f"{name}: expected {cols} columns, got {q.cols}")
     for part, t, n in (("codes", q.codes, cb), ("scales", q.scales, sb)):
+        if (t.dtype == torch.uint8 and t.device == dev and t.shape == (rows, n)
+                and t.is_contiguous()):
+            continue
         if t.dtype != torch.uint8:
             raise TypeError(f"{name}.{part}: expected uint8, got {t.dtype}")
         if t.device != dev:
             raise ValueError(f"{name}.{part}: expected a tensor on {dev}, got {t.device}")
-        if tuple(t.shape) != (rows, n) or not t.is_contiguous():
-            raise ValueError(f"{name}.{part}: expected contiguous shape {(rows, n)}, got "
-                             f"{tuple(t.shape)}")
+        raise ValueError(f"{name}.{part}: expected contiguous shape {(rows, n)}, got "
+                         f"{tuple(t.shape)}")
 
 
 def mx_quantize(x, fmt: str, out: Optional[MXTensor] = None) -> MXTensor:
@@ -627,16 +636,17 @@ def mx_dequantize(q: MXTensor, dtype=None, out=None):
 
 def _params(weight, bias, dev, h):
     """The parameters' common element type (bf16 without any)."""
-    pd = None
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is None:
-            continue
-        d = _dtype_id(t, name)
-        if pd is not None and d != pd:
+    first = bias if weight is None else weight
+    if first is None:
+        return 0
+    pd = _dtype_id(first, "weight" if first is weight else "bias")
+    if weight is not None:
+        _vector(weight, "weight", dev, first.dtype, h)
+    if bias is not None:
+        if bias.dtype != first.dtype:
             raise TypeError("weight and bias must have the same dtype")
-        pd = d
-        _vector(t, name, dev, t.dtype, h)
-    return 0 if pd is None else pd
+        _vector(bias, "bias", dev, first.dtype, h)
+    return pd
 
 
 def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out_dtype=None,
@@ -655,7 +665,12 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out_dtype=N
     f = _MX_NONE if checkpoint is None else _mx_format(checkpoint, ("mxfp8", "mxint8"))
     kept = None
     if out is None:
-        y = torch.empty((m, h), dtype=x.dtype if out_dtype is None else out_dtype, device=dev)
+        if (out_dtype is None or out_dtype == x.dtype) and ldx == h:
+            y, yd = torch.empty_like(x), xd
+        else:
+            y = torch.empty((m, h), dtype=x.dtype if out_dtype is None else out_dtype, device=dev)
+            yd = _dtype_id(y, "y")
+        ldy = h
         mean = torch.empty(m, dtype=torch.float32, device=dev)
         rstd = torch.empty(m, dtype=torch.float32, device=dev)
         if checkpoint is not None:
@@ -671,7 +686,7 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out_dtype=N
             if kept.fmt != checkpoint:
                 raise ValueError(f"checkpoint: expected format {checkpoint}, got {kept.fmt}")
             _mx_check(kept, "checkpoint", dev, f, m, h)
-    yd, ldy = _dtype_id(y, "y"), _rows(y, "y", dev, (m, h))
+        yd, ldy = _dtype_id(y, "y"), _rows(y, "y", dev, (m, h))
     codes, scales = (None, None) if kept is None else (kept.codes.data_ptr(), kept.scales.data_ptr())
     _launch(dev, load().flce_layer_norm_forward, x.data_ptr(), xd, ldx, _ptr(weight), _ptr(bias),
             pd, m, h, eps, y.data_ptr(), yd, ldy, mean.data_ptr(), rstd.data_ptr(), f, codes, scales)
@@ -712,7 +727,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx_dtype=None, need_para
     _vector(mean, "mean", dev, torch.float32, m)
     _vector(rstd, "rstd", dev, torch.float32, m)
     if weight is not None:
-        _params(weight, None, dev, h)
+        _vector(weight, "weight", dev, weight.dtype, h)
         if param_dtype is not None and param_dtype != weight.dtype:
             raise TypeError(f"param_dtype: expected weight's {weight.dtype}, got {param_dtype}")
         param_dtype = weight.dtype
@@ -732,7 +747,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx_dtype=None, need_para
             if t is not None:
                 _vector(t, name, dev, param_dtype, h)
     dxd, lddx = _dtype_id(dx, "dx"), _rows(dx, "dx", dev, (m, h))
-    pd = {torch.bfloat16: 0, torch.float32: 1}.get(param_dtype)
+    pd = _DTYPE_IDS.get(param_dtype)
     if pd is None:
         raise TypeError(f"param_dtype: expected bfloat16 or float32, got {param_dtype}")
     if workspace is None:
