@@ -38,36 +38,75 @@ struct F32 {
   static __device__ __forceinline__ float from_f32(float f) { return f; }
 };
 
-// Elements [col, col + 8) of a row of `cols` elements.  VEC: col + 8 <= cols or col >= cols,
-// and the row is 16-byte aligned; otherwise element by element.  Elements past the row are 0.
+// 16 bytes at the alignment of an element: one access all the same (the device allows
+// unaligned ones; element by element, rows of an odd length took 3.5 times as long).
+typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4_t u32x4_a4 __attribute__((aligned(4)));
+typedef f32x4_t f32x4_a4 __attribute__((aligned(4)));
+
+// Elements [col, col + 8) of a row of `cols` elements, as they come from memory (so that loads
+// can be in flight at few registers' cost) and as floats; elements past the row are 0.  VEC:
+// col + 8 <= cols or col >= cols, and the row is 16-byte aligned.  Otherwise at any alignment;
+// a row's last, partial chunk is fetched as the last 8 elements of the row and moved into place
+// by value(), so that it costs no access of its own.  Rows shorter than 8 go one by one.
 template <class T, bool VEC>
-__device__ __forceinline__ void load8(const typename T::mem* row, long col, long cols, float (&v)[8]) {
-  if constexpr (VEC) {
-    if (col < cols) {
-      if constexpr (sizeof(typename T::mem) == 2) {
-        const u32x4_t u = *reinterpret_cast<const u32x4_t*>(row + col);
+struct Chunk8 {
+  static constexpr bool HALF = sizeof(typename T::mem) == 2;
+  u32x4_t u[HALF ? 1 : 2];
+  __device__ __forceinline__ void load(const typename T::mem* row, long col, long cols) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[2 * i] = bf16_lo(u[i]);
-          v[2 * i + 1] = bf16_hi(u[i]);
-        }
+    for (int k = 0; k < (HALF ? 1 : 2); ++k) u[k] = u32x4_t{0u, 0u, 0u, 0u};
+    if (col >= cols) return;
+    if constexpr (VEC) {
+#pragma unroll
+      for (int k = 0; k < (HALF ? 1 : 2); ++k)
+        u[k] = *reinterpret_cast<const u32x4_t*>(row + col + 4 * k);
+    } else if (cols >= 8) {
+      const typename T::mem* at = row + (col < cols - 8 ? col : cols - 8);
+      if constexpr (HALF) {
+        u[0] = *reinterpret_cast<const u32x4_a2*>(at);
       } else {
-        const f32x4_t a = *reinterpret_cast<const f32x4_t*>(row + col);
-        const f32x4_t b = *reinterpret_cast<const f32x4_t*>(row + col + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = a[i];
-          v[4 + i] = b[i];
-        }
+        u[0] = *reinterpret_cast<const u32x4_a4*>(at);
+        u[1] = *reinterpret_cast<const u32x4_a4*>(at + 4);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        if (i >= cols) break;
+        if constexpr (HALF) u[0][i / 2] |= (uint32_t)row[i] << (16 * (i & 1));
+        else u[i / 4][i & 3] = __float_as_uint(row[i]);
+      }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = col + i < cols ? T::to_f32(row[col + i]) : 0.f;
   }
+  __device__ __forceinline__ void value(long col, long cols, float (&v)[8]) const {
+    if constexpr (HALF) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo(u[0][i]);
+        v[2 * i + 1] = bf16_hi(u[0][i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i / 4][i & 3]);
+    }
+    if constexpr (!VEC) {
+      const long over = col + 8 - cols;  // elements of the chunk past the row
+      if (over > 0 && over < 8 && cols >= 8) {
+#pragma unroll
+        for (int bit = 4; bit > 0; bit /= 2)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = (over & bit) ? (i + bit < 8 ? v[i + bit] : 0.f) : v[i];
+      }
+    }
+  }
+};
+
+template <class T, bool VEC>
+__device__ __forceinline__ void load8(const typename T::mem* row, long col, long cols, float (&v)[8]) {
+  Chunk8<T, VEC> c;
+  c.load(row, col, cols);
+  c.value(col, cols, v);
 }
 
 template <class T, bool VEC>
@@ -83,6 +122,14 @@ __device__ __forceinline__ void store8(typename T::mem* row, long col, long cols
         *reinterpret_cast<f32x4_t*>(row + col) = a;
         *reinterpret_cast<f32x4_t*>(row + col + 4) = b;
       }
+    }
+  } else if (col + 8 <= cols) {
+    if constexpr (sizeof(typename T::mem) == 2) {
+      *reinterpret_cast<u32x4_a2*>(row + col) = u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                        pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    } else {
+      *reinterpret_cast<f32x4_a4*>(row + col) = f32x4_t{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4_a4*>(row + col + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
     }
   } else {
 #pragma unroll

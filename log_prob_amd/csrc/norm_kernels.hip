@@ -175,44 +175,17 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void norm_fwd_kernel(NormFwdAr
   }
 }
 
-// Eight elements of a row as they come from memory, so that a row can be fetched while the
-// one before it is worked on at few registers' cost; value() makes floats of them.
-template <class T, bool VEC>
-struct Chunk {
-  float v[8];
-  __device__ __forceinline__ void load(const typename T::mem* row, int col, int H) {
-    load8<T, VEC>(row, col, H, v);
-  }
-  __device__ __forceinline__ void value(float (&o)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = v[i];
-  }
-};
-template <>
-struct Chunk<Bf16, true> {
-  u32x4_t u;
-  __device__ __forceinline__ void load(const uint16_t* row, int col, int H) {
-    u = u32x4_t{0u, 0u, 0u, 0u};
-    if (col < H) u = *reinterpret_cast<const u32x4_t*>(row + col);
-  }
-  __device__ __forceinline__ void value(float (&o)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = bf16_lo(u[i]);
-      o[2 * i + 1] = bf16_hi(u[i]);
-    }
-  }
-};
-
 // The backward's view of the input: a matrix of T, or its 8-bit checkpoint.
 struct Saved {};
 template <class TX, bool VEC>
 struct Input {
-  Chunk<TX, VEC> c;
+  Chunk8<TX, VEC> c;
   __device__ __forceinline__ void load(const NormBwdArgs& p, long row, int col) {
     c.load(static_cast<const typename TX::mem*>(p.x) + row * p.ldx, col, p.H);
   }
-  __device__ __forceinline__ void value(const NormBwdArgs&, float (&o)[8]) const { c.value(o); }
+  __device__ __forceinline__ void value(const NormBwdArgs& p, int col, float (&o)[8]) const {
+    c.value(col, p.H, o);
+  }
 };
 template <bool VEC>
 struct Input<Saved, VEC> {
@@ -227,7 +200,7 @@ struct Input<Saved, VEC> {
       byte = p.scales[row * scale_ld + (col >> 5)];
     }
   }
-  __device__ __forceinline__ void value(const NormBwdArgs& p, float (&o)[8]) const {
+  __device__ __forceinline__ void value(const NormBwdArgs& p, int, float (&o)[8]) const {
     if (p.fmt == kMxFp8)
       mx_decode<kMxFp8>(r, byte, o);
     else
@@ -255,7 +228,7 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void norm_bwd_kernel(NormBwdAr
   const float rh = 1.f / (float)H;
   struct Row {
     Input<TX, VEC> x[CH];
-    Chunk<TY, VEC> dy[CH];
+    Chunk8<TY, VEC> dy[CH];
     float mean, rstd;
     __device__ __forceinline__ void load(const NormBwdArgs& p, long row, int t) {
       const typename TY::mem* dyr = static_cast<const typename TY::mem*>(p.dy) + row * p.lddy;
@@ -279,8 +252,8 @@ __global__ __launch_bounds__(NT == 64 ? 256 : NT) void norm_bwd_kernel(NormBwdAr
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      cur.x[c].value(p, x[c]);
-      cur.dy[c].value(g[c]);
+      cur.x[c].value(p, 8 * (t + NT * c), x[c]);
+      cur.dy[c].value(8 * (t + NT * c), H, g[c]);
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c)
@@ -418,7 +391,7 @@ __global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormBwdArgs p) {
     for (int col = 8 * t; col < H; col += 8 * WIDE) {
       Input<TX, VEC> in;
       in.load(p, row, col);
-      in.value(p, x);
+      in.value(p, col, x);
       load8<TY, VEC>(dy, col, H, g);
       load_param<VEC>(p.weight, p.param_dtype, col, H, 1.f, w);
       if (first) {
@@ -446,7 +419,7 @@ __global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormBwdArgs p) {
     for (int col = 8 * t; col < H; col += 8 * WIDE) {
       Input<TX, VEC> in;
       in.load(p, row, col);
-      in.value(p, x);
+      in.value(p, col, x);
       load8<TY, VEC>(dy, col, H, g);
       load_param<VEC>(p.weight, p.param_dtype, col, H, 1.f, w);
 #pragma unroll
