@@ -27,20 +27,26 @@ namespace flce {
 
 namespace {
 
-// The sum over the 64 lanes of a wave, in every lane.
+// The sum over the LANES (16, 32 or 64) neighbouring lanes of a row, in every one of them.
 template <int CTRL>
 __device__ __forceinline__ float dpp_sum(float v) {
   return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
 }
-__device__ __forceinline__ float wave_sum(float v) {
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
   v = dpp_sum<0xB1>(v);   // lane ^ 1
   v = dpp_sum<0x4E>(v);   // lane ^ 2
   v = dpp_sum<0x141>(v);  // the other quad of 8 lanes (half-row mirror)
   v = dpp_sum<0x140>(v);  // the other 8 lanes of 16 (row mirror)
-  v += __shfl_xor(v, 16);
-  v += __shfl_xor(v, 32);
+  if constexpr (LANES > 16) v += __shfl_xor(v, 16);
+  if constexpr (LANES > 32) v += __shfl_xor(v, 32);
   return v;
 }
+
+// Threads of a workgroup for rows of NT threads, and rows it holds: those of a wave or less
+// need no barrier and share a workgroup of four waves.
+constexpr int threads_of(int nt) { return nt <= 64 ? 256 : nt; }
+constexpr int rows_of(int nt) { return threads_of(nt) / nt; }
 
 // Sums of N <= 2 values over the NT threads that share a row (in every thread).  More than
 // one wave meet in LDS; `buf` (2 x NT / 64 x 2 floats) alternates halves, so that one barrier
@@ -53,7 +59,7 @@ struct RowSum {
   template <int N>
   __device__ __forceinline__ void operator()(float (&v)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+    for (int i = 0; i < N; ++i) v[i] = lanes_sum<NT < 64 ? NT : 64>(v[i]);
     if constexpr (NT > 64) {
       constexpr int W = NT / 64;
       float* b = buf + turn * (2 * W);
@@ -107,9 +113,9 @@ __device__ __forceinline__ void save8(const float (&v)[8], int col, uint8_t* cod
 
 // Rows of H <= 8 NT CH elements, NT threads a row.
 template <class TX, class TY, int NT, int CH, bool VEC>
-__global__ __launch_bounds__(NT == 64 ? 256 : NT) void norm_fwd_kernel(NormFwdArgs p) {
-  constexpr int ROWS = NT == 64 ? 4 : 1;  // a row of its own for a wave; no barrier then
-  __shared__ float red[4 * (NT / 64)];
+__global__ __launch_bounds__(threads_of(NT)) void norm_fwd_kernel(NormFwdArgs p) {
+  constexpr int ROWS = rows_of(NT);
+  __shared__ float red[4 * ((NT + 63) / 64)];
   const int t = threadIdx.x % NT, H = p.H;
   RowSum<NT> sum{red};
   float w[CH][8], b[CH][8];
@@ -210,11 +216,11 @@ struct Input<Saved, VEC> {
 
 // Rows of H <= 8 NT CH elements; group g of the launch takes rows g, g + groups, ..., with
 // the next row's loads in flight under the work on this one, and leaves the column sums of
-// its rows.  Rows that share a workgroup (NT = 64) join their sums in LDS first, in order.
+// its rows.  Rows that share a workgroup join their sums in LDS first, in order.
 template <class TX, class TY, class TD, int NT, int CH, bool VEC>
-__global__ __launch_bounds__(NT == 64 ? 256 : NT) void norm_bwd_kernel(NormBwdArgs p) {
-  constexpr int ROWS = NT == 64 ? 4 : 1;  // a row of its own for a wave; no barrier then
-  __shared__ float red[4 * (NT / 64)];
+__global__ __launch_bounds__(threads_of(NT)) void norm_bwd_kernel(NormBwdArgs p) {
+  constexpr int ROWS = rows_of(NT);
+  __shared__ float red[4 * ((NT + 63) / 64)];
   __shared__ float join[ROWS > 1 ? 16 * NT * CH : 1];
   const int t = threadIdx.x % NT, slot = threadIdx.x / NT, H = p.H;
   RowSum<NT> sum{red};
@@ -479,7 +485,11 @@ void fwd_rows(const NormFwdArgs& a, hipStream_t s) {
     const long most = (long)kComputeUnits * groups_per_unit;
     return (unsigned)(need < most ? need : most);
   };
-  if (a.H <= 512)
+  if (a.H <= 128)
+    norm_fwd_kernel<TX, TY, 16, 1, VEC><<<grid(16, 16), 256, 0, s>>>(a);
+  else if (a.H <= 256)
+    norm_fwd_kernel<TX, TY, 32, 1, VEC><<<grid(8, 16), 256, 0, s>>>(a);
+  else if (a.H <= 512)
     norm_fwd_kernel<TX, TY, 64, 1, VEC><<<grid(4, 16), 256, 0, s>>>(a);
   else if (a.H <= 1024)
     norm_fwd_kernel<TX, TY, 128, 1, VEC><<<grid(1, 32), 128, 0, s>>>(a);
@@ -498,7 +508,11 @@ void fwd_rows(const NormFwdArgs& a, hipStream_t s) {
 template <class TX, class TY, class TD, bool VEC>
 void bwd_rows(const NormBwdArgs& a, hipStream_t s) {
   const unsigned g = (unsigned)a.groups;
-  if (a.H <= 512)
+  if (a.H <= 128)
+    norm_bwd_kernel<TX, TY, TD, 16, 1, VEC><<<g, 256, 0, s>>>(a);
+  else if (a.H <= 256)
+    norm_bwd_kernel<TX, TY, TD, 32, 1, VEC><<<g, 256, 0, s>>>(a);
+  else if (a.H <= 512)
     norm_bwd_kernel<TX, TY, TD, 64, 1, VEC><<<g, 256, 0, s>>>(a);
   else if (a.H <= 1024)
     norm_bwd_kernel<TX, TY, TD, 64, 2, VEC><<<g, 256, 0, s>>>(a);
@@ -530,7 +544,7 @@ void fwd_vec(const NormFwdArgs& a, bool vec, hipStream_t s) {
 // 65535 x 1024 77, 78, -, 88; 32767 x 2048 110, 77, 79, 84, and from the checkpoint 111, 74,
 // 67, 70; 16384 x 4096 77, 82, 91; 8192 x 8192 84, 91).  Past one a unit each has 16 turns.
 int norm_bwd_groups(long M, int H) {
-  const long rows = H <= 1024 ? 4 : 1;
+  const long rows = H <= 128 ? 16 : H <= 256 ? 8 : H <= 1024 ? 4 : 1;
   const long most = kComputeUnits * (H <= 512 ? 2 : H <= 1024 ? 1 : H <= 2048 ? 3 : 1);
   const long need = (M + rows - 1) / rows;
   const long shared = need / 16 > kComputeUnits ? need / 16 : kComputeUnits;

@@ -33,8 +33,8 @@ def pack_scales(exps):
 
 def norm_depth(H):
     """Additions a value passes through in a row's sum: a thread holds at most H / 64 of the
-    elements (the narrowest kernel gives a row to 64 threads), then the lanes and waves."""
-    return H / 64 + 32
+    elements, or 8 in the rows of fewer threads, then the lanes and waves."""
+    return H / 64 + 40
 
 
 def norm_forward_bounds(x, weight, bias, eps, y, mean, rstd, half):
