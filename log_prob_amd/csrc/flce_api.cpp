@@ -764,6 +764,7 @@ size_t mx_w_bytes(int64_t M, int64_t H, int64_t V) {
 }
 // X's copy of `rows` of the call's M rows.
 size_t mx_x_bytes(int64_t M, int64_t rows, int64_t H) {
+  if (flce::mx_stream_owns(M, H)) return 0;
   return mx_x_codes_bytes(rows, H) + mx_scales_bytes(rows, H, !mx_streams(M));
 }
 
@@ -863,7 +864,9 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
   if (out_dtype != FLCE_BF16 && out_dtype != FLCE_FP32)
     return fail(FLCE_ERR_INVALID_VALUE, "unknown element type");
   if (M == 0) return ok();
-  if (!out || !workspace) return fail(FLCE_ERR_INVALID_VALUE, "NULL pointer among out, workspace");
+  const size_t need = mx_w_bytes(M, H, V) + mx_x_bytes(M, M, H);
+  if (!out || (!workspace && need > 0))
+    return fail(FLCE_ERR_INVALID_VALUE, "NULL pointer among out, workspace");
   if (ldo < V)
     return fail(FLCE_ERR_INVALID_VALUE, "out: row stride %lld is below its %lld columns",
                 (long long)ldo, (long long)V);
@@ -873,15 +876,15 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
     return fail(FLCE_ERR_UNSUPPORTED, "out must be naturally aligned");
   if (!aligned(workspace, kAlign))
     return fail(FLCE_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
-  const size_t need = mx_w_bytes(M, H, V) + mx_x_bytes(M, M, H);
+  const uint16_t* own = flce::mx_stream_owns(M, H) ? static_cast<const uint16_t*>(X) : nullptr;
   if (workspace_bytes < need)
     return fail(FLCE_ERR_WORKSPACE_TOO_SMALL, "logits need %zu workspace bytes, got %zu", need,
                 workspace_bytes);
   char* ws = static_cast<char*>(workspace);
-  flce::MxOperand x, w;
+  flce::MxOperand x{}, w;
   hipError_t e = mx_weights(W_codes, W_scales, M, H, V, ws, &w, stream);
   if (e != hipSuccess) return hip_fail(e, "scale layout kernel launch");
-  e = mx_quantize_x(X, 0, M, H, mx_streams(M), ws + mx_w_bytes(M, H, V), nullptr, &x, stream);
+  if (!own) e = mx_quantize_x(X, 0, M, H, mx_streams(M), ws + mx_w_bytes(M, H, V), nullptr, &x, stream);
   if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
   // one launch covers up to max_wave_rows(V) rows (the dispatch limit)
   const int64_t rows = max_wave_rows(V);
@@ -889,6 +892,7 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
     flce::MxLogitsArgs a{};
     a.x = flce::MxOperand{x.codes + r0 * flce::mx_code_bytes(H, flce::kMxFp4),
                           x.scales + r0 / 256 * x.layout.tile_stride, x.layout};
+    a.X = own;
     a.w = w;
     a.M = int(M - r0 < rows ? M - r0 : rows);
     a.H = int(H);
@@ -958,8 +962,12 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
     a.entropy = ent ? entropy + r0 : nullptr;
     flce::TileQueue tq{};
     tq.ctr = reinterpret_cast<unsigned long long*>(part + L.total - flce::kQueueBytes);
-    e = mx_quantize_x(X, r0, mw, H, mx_streams(M), ws, tq.ctr, &a.x, stream);
-    if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
+    if (flce::mx_stream_owns(M, H)) {
+      a.X = static_cast<const uint16_t*>(X);
+    } else {
+      e = mx_quantize_x(X, r0, mw, H, mx_streams(M), ws, tq.ctr, &a.x, stream);
+      if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
+    }
     e = mx_streams(M) ? flce::launch_mx_stream_fwd(a, stream) : flce::launch_mx_tile_fwd(a, tq, stream);
     if (e != hipSuccess) return hip_fail(e, "4-bit forward kernel launch");
     e = flce::launch_mx_merge(a, stream);

@@ -19,10 +19,13 @@ namespace {
 // A workgroup of RW x KW = 4 waves takes 32 RW vocabulary rows; wave (rw, kw) multiplies rows
 // 32 rw .. + 31 over every KW-th 256 K, and the KW partial products meet in LDS at the end
 // (fewer rows a workgroup where the vocabulary is too small to fill the chip otherwise).  XR
-// token rows are staged (8, or 32 TB).
+// token rows are staged (8, or 32 TB); or none (XR = 0): the few tokens of a decoding step are
+// quantised by every workgroup for itself while its first rows of W are on their way, which
+// spares the launch that would do it (at most kMxOwnBytes of codes).
 template <int RW_, int KW_, int XR_>
 struct StreamCfg {
   static constexpr int RW = RW_, KW = KW_, XR = XR_;
+  static constexpr bool OWN = XR == 0;
   static constexpr int TB = XR <= 32 ? 1 : XR / 32;       // 32-token blocks
   static constexpr int ROWS = 32 * RW, NS = 3;            // vocabulary rows; stages
   static constexpr int W_BYTES = KW * ROWS * 128, X_BYTES = KW * XR * 128;
@@ -31,10 +34,11 @@ struct StreamCfg {
   static constexpr int X_LOADS = (X_BYTES + 4095) / 4096;
   static constexpr int LOADS = W_LOADS + X_LOADS;
   // scales: 64 bytes of a row (8 steps) at a time, double-buffered
-  static constexpr int SCALE_ROWS = ROWS + (XR < 16 ? 16 : XR);
+  static constexpr int SCALE_ROWS = ROWS + (OWN ? 0 : XR < 16 ? 16 : XR);
   static constexpr int SCALE_BUF = SCALE_ROWS * 64;
   static constexpr int SCALE_LOADS = (SCALE_ROWS / 16 + 3) / 4;        // a wave, at most
-  static constexpr int LDS = NS * STAGE + 2 * SCALE_BUF;
+  static constexpr int OWN_AT = NS * STAGE + 2 * SCALE_BUF;            // own codes, then scales
+  static constexpr int LDS = OWN_AT + (OWN ? kMxOwnBytes + kMxOwnBytes / 8 : 0);
   static constexpr int MB = 1, NB = TB;  // as lane_col_max and lane_col_sums name them
   static_assert(RW * KW == 4 && W_BYTES == 16384, "four waves");
   static_assert(LDS <= 160 * 1024, "LDS");
@@ -45,8 +49,9 @@ struct StreamCfg {
 // logits (a lane holds one vocabulary column, so a store covers 128 contiguous bytes of a
 // row).  Summed over the KW waves of the same rows, in order, in the waves with kw = 0.
 template <class C, bool LOGITS>
-__device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* smem, const MxOperand& x,
-                                               const MxOperand& w, int M, int H, int V, int v0) {
+__device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* smem, const uint16_t* X,
+                                               const MxOperand& x, const MxOperand& w, int M, int H,
+                                               int V, int v0) {
   constexpr int RW = C::RW, KW = C::KW, TB = C::TB, NS = C::NS;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -69,17 +74,19 @@ __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* sm
       const bool ok = r < wvalid && b < blocks;
       dma16<0>(wr, ok ? (uint32_t)r * ld + 16u * (uint32_t)b : OOB_OFFSET, 0u, st + 1024u * (uint32_t)i);
     }
+    if constexpr (!C::OWN) {
 #pragma unroll
-    for (int q = 0; q < C::X_LOADS; ++q) {
-      const int i = wave * C::X_LOADS + q, sub = i / (C::XR / 8), r = 8 * (i % (C::XR / 8)) + lr;
-      const int b = 8 * (KW * k + sub) + (lp ^ mx_swz(r));
-      const bool ok = r < M && b < blocks;
-      // (fewer loads than waves: the waves without one repeat it with nothing to bring)
-      if (C::X_BYTES >= 4096 || i < C::X_BYTES / 1024)
-        dma16<0>(xr, ok ? (uint32_t)r * ld + 16u * (uint32_t)b : OOB_OFFSET, 0u,
-                 st + (uint32_t)C::W_BYTES + 1024u * (uint32_t)i);
-      else
-        dma16<0>(xr, OOB_OFFSET, 0u, lds0 + (uint32_t)(C::NS * C::STAGE + 2 * C::SCALE_BUF));
+      for (int q = 0; q < C::X_LOADS; ++q) {
+        const int i = wave * C::X_LOADS + q, sub = i / (C::XR / 8), r = 8 * (i % (C::XR / 8)) + lr;
+        const int b = 8 * (KW * k + sub) + (lp ^ mx_swz(r));
+        const bool ok = r < M && b < blocks;
+        // (fewer loads than waves: the waves without one repeat it with nothing to bring)
+        if (C::X_BYTES >= 4096 || i < C::X_BYTES / 1024)
+          dma16<0>(xr, ok ? (uint32_t)r * ld + 16u * (uint32_t)b : OOB_OFFSET, 0u,
+                   st + (uint32_t)C::W_BYTES + 1024u * (uint32_t)i);
+        else
+          dma16<0>(xr, OOB_OFFSET, 0u, lds0 + (uint32_t)(C::NS * C::STAGE + 2 * C::SCALE_BUF));
+      }
     }
   };
   // scales of steps 8 c .. 8 c + 7: lane l row l / 4, 16-byte piece l % 4
@@ -95,7 +102,7 @@ __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* sm
         const bool is_w = i < C::ROWS / 16;
         const int r = 16 * (is_w ? i : i - C::ROWS / 16) + (lane >> 2), p = 4 * c + (lane & 3);
         const bool ok = r < (is_w ? wvalid : M) && p < pieces;
-        dma16<0>(is_w ? ws : xs, ok ? (uint32_t)r * sld + 16u * (uint32_t)p : OOB_OFFSET, 0u,
+        dma16<0>(C::OWN || is_w ? ws : xs, ok ? (uint32_t)r * sld + 16u * (uint32_t)p : OOB_OFFSET, 0u,
                  buf + 1024u * (uint32_t)i);
       }
     }
@@ -104,14 +111,18 @@ __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* sm
   // fragments: the wave's row of W and of each token block (rows past XR repeat earlier ones)
   const int half = lane >> 5, r = lane & 31;
   uint32_t wf[4], xf[4];
-  const int xrow = r & (C::XR - 1);
+  const int xrow = C::OWN ? (r < M ? r : 0) : r & (C::XR - 1);
+  const int own_ld = 128 * KW * nk;  // bytes of a row of own codes: every step, and an 8th of scales
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
     wf[kk] = (uint32_t)(kw * C::ROWS * 128 + (32 * rw + r) * 128 + (((4 * half + kk) ^ mx_swz(r)) << 4));
-    xf[kk] = (uint32_t)(C::W_BYTES + kw * C::XR * 128 + xrow * 128 + (((4 * half + kk) ^ mx_swz(xrow)) << 4));
+    xf[kk] = C::OWN ? (uint32_t)(C::OWN_AT + xrow * own_ld + 128 * kw + ((4 * half + kk) << 4))
+                    : (uint32_t)(C::W_BYTES + kw * C::XR * 128 + xrow * 128 +
+                                 (((4 * half + kk) ^ mx_swz(xrow)) << 4));
   }
   const uint32_t wsf = (uint32_t)((32 * rw + r) * 64 + 4 * half);
-  const uint32_t xsf = (uint32_t)((C::ROWS + xrow) * 64 + 4 * half);
+  const uint32_t xsf = C::OWN ? (uint32_t)(C::OWN_AT + kMxOwnBytes + xrow * (own_ld / 16) + 8 * kw + 4 * half)
+                              : (uint32_t)((C::ROWS + xrow) * 64 + 4 * half);
 #pragma unroll
   for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
@@ -120,6 +131,19 @@ __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* sm
   issue_scales(0);
 #pragma unroll
   for (int k = 0; k < NS - 1; ++k) issue(k, k);
+  if constexpr (C::OWN) {
+    // thread t takes chunks of 8 elements t, t + 256, ...; whole steps, zeros past H (the first
+    // barrier of the loop publishes them)
+    const int chunks = own_ld / 4;
+    for (int i = threadIdx.x; i < M * chunks; i += 256) {
+      const int m = i / chunks, c = i - m * chunks;
+      float v[8];
+      load8<Bf16, true>(X + (long)m * H, 8 * c, H, v);
+      const uint32_t byte = mx_scale_byte<kMxFp4>(v);
+      *reinterpret_cast<uint32_t*>(smem + C::OWN_AT + 4 * i) = mx_encode<kMxFp4>(v, byte).x;
+      if ((c & 3) == 0) smem[C::OWN_AT + kMxOwnBytes + i / 4] = (char)byte;
+    }
+  }
   int slot = 0;
   for (int k = 0; k < nk; ++k) {
     // stage k has landed (the loads of the NS - 2 stages after it may be in flight), and
@@ -137,10 +161,12 @@ __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* sm
     for (int kk = 0; kk < 4; ++kk) wv[kk] = *reinterpret_cast<const u32x4*>(st + wf[kk]);
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb) {
-      const int sx = *reinterpret_cast<const int*>(sb + xsf + 2048 * tb);
+      const int sx = *reinterpret_cast<const int*>(C::OWN ? smem + xsf + 8 * KW * k : sb + xsf + 2048 * tb);
       u32x4 xv[4];
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) xv[kk] = *reinterpret_cast<const u32x4*>(st + xf[kk] + 4096 * tb);
+      for (int kk = 0; kk < 4; ++kk)
+        xv[kk] = *reinterpret_cast<const u32x4*>(C::OWN ? smem + xf[kk] + 128 * KW * k
+                                                        : st + xf[kk] + 4096 * tb);
       if constexpr (LOGITS) {
         acc[0][tb] = mx_mfma<0>(xv[0], wv[0], acc[0][tb], sx, sw);
         acc[0][tb] = mx_mfma<1>(xv[1], wv[1], acc[0][tb], sx, sw);
@@ -181,7 +207,7 @@ __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* sm
 
 // The staging LDS, and a kilobyte that loads with nothing to bring may zero.
 template <class C>
-constexpr int stream_lds = C::LDS + (C::X_BYTES < 4096 ? 1024 : 0);
+constexpr int stream_lds = C::LDS + (!C::OWN && C::X_BYTES < 4096 ? 1024 : 0);
 
 template <class C, class T>
 __global__ __launch_bounds__(256) void mx_stream_logits_kernel(MxLogitsArgs p) {
@@ -189,7 +215,7 @@ __global__ __launch_bounds__(256) void mx_stream_logits_kernel(MxLogitsArgs p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int v0 = (int)blockIdx.x * C::ROWS;
   f32x16 acc[1][C::TB];
-  stream_product<C, true>(acc, smem, p.x, p.w, p.M, p.H, p.V, v0);
+  stream_product<C, true>(acc, smem, p.X, p.x, p.w, p.M, p.H, p.V, v0);
   const int v = v0 + 32 * (wave % C::RW) + (lane & 31);
   if (wave / C::RW != 0 || v >= p.V) return;
   typename T::mem* out = static_cast<typename T::mem*>(p.out) + v;
@@ -213,7 +239,7 @@ __global__ __launch_bounds__(256) void mx_stream_fwd_kernel(MxFwdArgs p) {
   const int rw = wave % RW, kw = wave / RW, lc = lane & 31;
   const int v0 = (int)blockIdx.x * C::ROWS;
   f32x16 acc[1][TB];
-  stream_product<C, false>(acc, smem, p.x, p.w, p.M, p.H, p.V, v0);
+  stream_product<C, false>(acc, smem, p.X, p.x, p.w, p.M, p.H, p.V, v0);
   // [rw][token] maxima and sums, behind what the KW waves exchanged
   float* red = reinterpret_cast<float*>(smem) + (C::KW - 1) * RW * TB * 1024;
   float* comb = red + RW * TT;
@@ -279,8 +305,9 @@ void with_cfg(int rows, F f) {
   }
 }
 template <class F>
-void with_tokens(int M, int rows, F f) {
-  if (M <= 8) with_cfg<8>(rows, f);
+void with_tokens(int M, int H, int rows, F f) {
+  if (mx_stream_owns(M, H)) with_cfg<0>(rows, f);
+  else if (M <= 8) with_cfg<8>(rows, f);
   else if (M <= 32) with_cfg<32>(rows, f);
   else if (M <= 64) with_cfg<64>(rows, f);
   else with_cfg<128>(rows, f);
@@ -312,7 +339,22 @@ __global__ __launch_bounds__(MERGE_THREADS) void mx_merge_kernel(MxFwdArgs p) {
     const long row = row0 + i;
     const int64_t t = row < p.M ? p.targets[row] : -1;
     float s = 0.f;
-    if (row < p.M && t != p.ignore_index && t >= 0 && t < p.V) {
+    const bool valid = row < p.M && t != p.ignore_index && t >= 0 && t < p.V;
+    if (ROWS == 1 && valid && p.X) {
+      // X not quantised beforehand: a chunk of 8 elements a thread
+      for (int c = threadIdx.x; c < 4 * (int)mx_blocks(p.H); c += MERGE_THREADS) {
+        float v[8], xv[8], wv[8];
+        load8<Bf16, true>(p.X + row * p.H, 8 * c, p.H, v);
+        const uint32_t byte = mx_scale_byte<kMxFp4>(v);
+        mx_decode<kMxFp4>(mx_encode<kMxFp4>(v, byte), 127u, xv);
+        mx_decode<kMxFp4>(u32x2_t{*reinterpret_cast<const uint32_t*>(p.w.codes + t * code_ld + 4l * c), 0u},
+                          127u, wv);
+        float d = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d = fmaf(xv[j], wv[j], d);
+        s = fmaf(d * mx_scale(byte), scale(p.w, t, c >> 2), s);
+      }
+    } else if (valid) {
       for (int b = ROWS == 1 ? (int)threadIdx.x : lane; b < (int)mx_blocks(p.H);
            b += ROWS == 1 ? MERGE_THREADS : 64) {
         const u32x4 xc = *reinterpret_cast<const u32x4*>(p.x.codes + row * code_ld + 16l * b);
@@ -400,7 +442,7 @@ int mx_stream_rows(int M, int V) {
 hipError_t launch_mx_stream_logits(const MxLogitsArgs& a, hipStream_t s) {
   const int rows = mx_stream_rows(a.M, a.V);
   const unsigned g = (unsigned)(((int64_t)a.V + rows - 1) / rows);
-  with_tokens(a.M, rows, [&](auto cfg) {
+  with_tokens(a.M, a.H, rows, [&](auto cfg) {
     using C = decltype(cfg);
     if (a.out_dtype == kBf16) mx_stream_logits_kernel<C, Bf16><<<g, 256, 0, s>>>(a);
     else mx_stream_logits_kernel<C, F32><<<g, 256, 0, s>>>(a);
@@ -409,7 +451,7 @@ hipError_t launch_mx_stream_logits(const MxLogitsArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_mx_stream_fwd(const MxFwdArgs& a, hipStream_t s) {
-  with_tokens(a.M, mx_stream_rows(a.M, a.V), [&](auto cfg) {
+  with_tokens(a.M, a.H, mx_stream_rows(a.M, a.V), [&](auto cfg) {
     using C = decltype(cfg);
     if (a.part_u) mx_stream_fwd_kernel<C, true><<<(unsigned)a.n_vt, 256, 0, s>>>(a);
     else mx_stream_fwd_kernel<C, false><<<(unsigned)a.n_vt, 256, 0, s>>>(a);

@@ -114,7 +114,14 @@ struct MxOperand {
 };
 // Scales of `rows` rows from row-major to the tile kernels' form (whole 256-row tiles).
 hipError_t launch_mx_turn_scales(const uint8_t* src, uint8_t* dst, long rows, long cols, hipStream_t s);
+// A decoding step's tokens are quantised by the product's workgroups themselves where their
+// codes (rows padded to 1024 K) take at most kMxOwnBytes.
+constexpr int kMxOwnBytes = 8192;
+constexpr bool mx_stream_owns(int64_t M, int64_t H) {
+  return M <= 8 && M * ((mx_blocks(H) + 31) / 32 * 512) <= kMxOwnBytes;
+}
 struct MxLogitsArgs {
+  const uint16_t* X;       // bf16 [M, H], if mx_stream_owns (x is then unused); else nullptr
   MxOperand x, w;
   int M, H, V;
   float scale;
@@ -127,6 +134,7 @@ struct MxLogitsArgs {
 // Log-prob partials: entry (vocabulary tile j, token m) of each array at j * tile_stride +
 // m * token_stride.
 struct MxFwdArgs {
+  const uint16_t* X;       // as in MxLogitsArgs
   MxOperand x, w;
   const int64_t* targets;
   int M, H, V;

@@ -82,7 +82,12 @@ def check_forward(X, W, t, scale, label, ent=True, **kw):
 SHAPES = [(1, 8, 1), (1, 32, 40), (2, 24, 33), (1, 256, 1000), (3, 248, 255), (5, 264, 256),
           (31, 40, 257), (32, 512, 300), (33, 520, 513), (64, 1000, 1003), (65, 768, 700),
           (127, 136, 2000), (128, 1032, 511), (129, 2056, 260), (200, 64, 5003), (256, 288, 1024),
-          (257, 544, 769), (300, 4096, 530), (513, 320, 1500), (1, 8192, 777), (700, 128, 50257)]
+          (257, 544, 769), (300, 4096, 530), (513, 320, 1500), (1, 8192, 777), (700, 128, 50257),
+          # few tokens, quantised by the product itself or beforehand, over vocabularies that
+          # give a workgroup 32, 64 and 128 rows
+          (8, 2048, 1400), (8, 2080, 500), (7, 4096, 300), (2, 8200, 100), (1, 16392, 70),
+          (5, 520, 25000), (8, 2568, 24600), (30, 264, 25001), (50, 136, 24999), (1, 264, 50257),
+          (8, 520, 50000), (8, 3080, 49200), (20, 136, 50257), (64, 136, 50000), (100, 72, 50257)]
 
 
 @pytest.mark.parametrize("M,H,V", SHAPES)

@@ -123,13 +123,13 @@ def test_binding_refuses_host_tensors_and_wrong_types():
 
 
 def logits(**kw):
-    a = dict(X=P, wc=P, ws=P, M=4, H=64, V=100, scale=1.0, out=P, od=0, ldo=100, work=P, wb=1 << 20)
+    a = dict(X=P, wc=P, ws=P, M=20, H=64, V=100, scale=1.0, out=P, od=0, ldo=100, work=P, wb=1 << 20)
     a.update(kw)
     return status("flce_mx_logits", *a.values(), None)
 
 
 def mx_forward(**kw):
-    a = dict(X=P, wc=P, ws=P, t=P, M=4, H=64, V=100, ignore=-100, scale=1.0, ent=1, lp=P, lse=P, en=P,
+    a = dict(X=P, wc=P, ws=P, t=P, M=20, H=64, V=100, ignore=-100, scale=1.0, ent=1, lp=P, lse=P, en=P,
              work=P, wb=1 << 24)
     a.update(kw)
     return status("flce_mx_forward", *a.values(), None)
@@ -158,20 +158,22 @@ def test_mx_forward(want, kw):
 
 
 def test_mx_workspace():
-    # X's copy: 32 bytes of codes and 16 of scales a row, each part rounded up to 256
+    # a decoding step's tokens need no copy of their own, only the partials of the forward: 4
+    # workgroups of 32 vocabulary rows for 4 tokens, 3 arrays, and counters
     lo, fw = flce.mxfp4_workspace_query(4, 64, 100)
-    assert lo == 512
-    # the partials of 4 workgroups of 32 vocabulary rows for 4 tokens, 3 arrays, and counters
-    assert fw == 512 + 3 * 256 + 256
+    assert (lo, fw) == (0, 3 * 256 + 256)
+    assert mx_forward(M=4, wb=fw - 1) == TOO_SMALL
+    # more tokens do: 32 bytes of codes and 16 of scales a row, each part rounded up to 256
+    lo, fw = flce.mxfp4_workspace_query(20, 64, 100)
+    assert lo == 768 + 512 and fw == lo + 3 * 512 + 256
+    assert mx_forward(M=20, wb=fw - 1) == TOO_SMALL and logits(M=20, wb=lo - 1) == TOO_SMALL
     # larger calls: 256-column tiles of 256-row multiples; whole scale tiles of X
     lo, fw = flce.mxfp4_workspace_query(300, 64, 1000, False)
-    assert lo == 300 * 32 + 128 + 512 * 16
+    assert lo == 9728 + 512 * 16
     assert fw == lo + 2 * 4 * 4 * 512 + 256
     # and past 2.5e11 products a copy of W's scales
     lo, _ = flce.mxfp4_workspace_query(4096, 4096, 32768)
     assert lo == 32768 * 128 + 4096 * (2048 + 128)
-    lo, fw = flce.mxfp4_workspace_query(4, 64, 100)
     assert flce.mxfp4_workspace_query(0, 64, 100) == (0, 0)
-    assert mx_forward(wb=fw - 1) == TOO_SMALL and logits(wb=lo - 1) == TOO_SMALL
     assert mx_forward(M=0, X=None, t=None, lp=None, lse=None, en=None, work=None, wb=0) == 0
     assert logits(M=0, X=None, out=None, work=None, wb=0) == 0
