@@ -954,6 +954,7 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
     a.n_vt = int(L.n_vt);
     a.tile_stride = mx_streams(M) ? 1 : long(L.pad);
     a.token_stride = mx_streams(M) ? long(L.n_vt) : 1;
+    a.call_M = long(M);
     a.part_m = reinterpret_cast<float*>(part);
     a.part_s = reinterpret_cast<float*>(part + L.array);
     a.part_u = ent ? reinterpret_cast<float*>(part + 2 * L.array) : nullptr;

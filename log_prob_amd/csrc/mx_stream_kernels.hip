@@ -466,9 +466,11 @@ static void merge_rows(const MxFwdArgs& a, hipStream_t s) {
   else mx_merge_kernel<ROWS, false><<<g, MERGE_THREADS, 0, s>>>(a);
 }
 
+// The whole call's tokens choose the kernel, for its order of summation: waves of any height
+// then give the same bits.
 hipError_t launch_mx_merge(const MxFwdArgs& a, hipStream_t s) {
   if (a.tile_stride == 1) merge_rows<1>(a, s);
-  else if (a.M <= 1024) merge_rows<4>(a, s);
+  else if (a.call_M <= 1024) merge_rows<4>(a, s);
   else merge_rows<16>(a, s);
   return hipGetLastError();
 }

@@ -142,6 +142,7 @@ struct MxFwdArgs {
   float scale;
   int n_mt, n_vt;          // n_vt: vocabulary tiles that leave partials
   long tile_stride, token_stride;
+  long call_M;             // rows of the whole call, of which M are this wave
   float* part_m;
   float* part_s;
   float* part_u;           // nullptr without entropy

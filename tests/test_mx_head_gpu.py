@@ -151,7 +151,7 @@ def test_output_strides(M, V, pad, shift, dtype):
     assert (buf[shift:shift + M * (V + pad)].view(M, V + pad)[:, V:] == 7.0).all()
 
 
-@pytest.mark.parametrize("H,V,M", [(264, 1700, 1000), (512, 300, 520)])
+@pytest.mark.parametrize("H,V,M", [(264, 1700, 1000), (512, 300, 520), (72, 20000, 2500)])
 def test_waves_give_the_same_bits(H, V, M):
     """Any workspace from one 256-row wave up; stale and guard bytes do not matter."""
     import torch

@@ -191,6 +191,41 @@ def test_graph_replays_match_eager(M, H, V):
         del junk
 
 
+@pytest.mark.parametrize("checkpoint", [None, "mxfp8"])
+def test_captured_autograd_replays(checkpoint):
+    """Forward and backward of the autograd norm in one captured graph, with no eager graph of
+    its leaves alive; inputs changed between the replays."""
+    import torch
+    from log_prob_amd import autograd
+    x, w, b = (v.requires_grad_() for v in norm_case(37, 264, 12))
+    dy = torch.randn(37, 264, device="cuda")
+
+    def step():
+        y = autograd.layer_norm(x, w, b, EPS, checkpoint=checkpoint)
+        return (y.detach(), *torch.autograd.grad(y, (x, w, b), dy))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for _ in range(4):
+        with torch.no_grad():
+            x.add_(0.25)
+            dy.mul_(-1.5)
+        for v in outs:
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [v.clone() for v in outs]
+        for a, r in zip(got, step()):
+            assert torch.equal(a, r)
+
+
 def test_two_streams_side_by_side():
     """The same calls on two streams at once, each with its own outputs and workspaces."""
     import torch
