@@ -751,21 +751,39 @@ size_t mx_scales_bytes(int64_t rows, int64_t H, bool tiled) {
   return align_up(size_t(tiled ? cdiv(rows, kTile) * kTile : rows) * size_t(flce::mx_scale_bytes(H)));
 }
 
-// Calls past kMxStreamTokens tokens run the tile kernels.  Those read scales fastest in their
-// own form, and X's are written so; turning W's costs a launch and a pass over them (3 to 8
-// us), which calls of this size win back (M=H=4096, V=128256: 1081 -> 1036 us; M=257, H=1600,
-// V=50257: 54 -> 58 us).
-bool mx_streams(int64_t M) { return M <= flce::kMxStreamTokens; }
+// Whether a call runs the kernels that stream W past a tile of tokens, or those of 256 x 256
+// tiles.  Up to kMxStreamTokens tokens always; past them where it takes less time by a model of
+// both (in 0.01 us, `steps` of 256 K): rounds of one large tile a compute unit, against the
+// smaller tiles that a unit runs two at a time, or 64-token ones where all are resident at once
+// (us, against large tiles: logits of 400 tokens, H=4096, V=4000 16 against 30; of 257, H=1600,
+// V=50257 35 against 44; of 400, H=2048, V=151936 146 against 104).  Over 724 timings (129 to
+// 16384 tokens, H 512 to 8192, V 300 to 128256) the choice costs 0.4% of the better kernel's
+// time on average, large tiles throughout 22%; past the sizes timed it takes the large tiles.
+bool mx_streams(int64_t M, int64_t H, int64_t V) {
+  if (M <= flce::kMxStreamTokens) return true;
+  const int64_t steps = cdiv(H, 256), large = cdiv(M, 256) * cdiv(V, 256);
+  if (large > 2048) return false;
+  const int64_t large_time = cdiv(large, 256) * (1100 + 120 * steps);
+  if (cdiv(M, 64) * cdiv(V, 128) <= flce::kMxStreamResident) return 200 + 55 * steps < large_time;
+  const int64_t rows = cdiv(M, 128), tiles = rows * cdiv(V, 128) * (rows * 96 >= M ? 7 : 8);
+  return (tiles > 2048 ? tiles : 2048) * (300 + 55 * steps) < 2048 * large_time;
+}
+// Partials with a token's vocabulary tiles side by side: a merge workgroup a token, until the
+// tokens outnumber the workgroups that run at once.
+bool mx_token_major(int64_t M, int64_t H, int64_t V) { return M <= 1024 && mx_streams(M, H, V); }
+// The large tiles' kernels read scales fastest in a form of their own, and X's are written so;
+// turning W's costs a launch and a pass over them (3 to 8 us), which calls of this size win
+// back (M=H=4096, V=128256: 1081 -> 1036 us; M=257, H=1600, V=50257: 54 -> 58 us).
 bool mx_turns(int64_t M, int64_t H, int64_t V) {
-  return M >= 2048 && double(M) * double(H) * double(V) >= 2.5e11;
+  return M >= 2048 && double(M) * double(H) * double(V) >= 2.5e11 && !mx_streams(M, H, V);
 }
 size_t mx_w_bytes(int64_t M, int64_t H, int64_t V) {
   return mx_turns(M, H, V) ? mx_scales_bytes(V, H, true) : 0;
 }
 // X's copy of `rows` of the call's M rows.
-size_t mx_x_bytes(int64_t M, int64_t rows, int64_t H) {
+size_t mx_x_bytes(int64_t M, int64_t rows, int64_t H, int64_t V) {
   if (flce::mx_stream_owns(M, H)) return 0;
-  return mx_x_codes_bytes(rows, H) + mx_scales_bytes(rows, H, !mx_streams(M));
+  return mx_x_codes_bytes(rows, H) + mx_scales_bytes(rows, H, !mx_streams(M, H, V));
 }
 
 // Partials of a forward wave of `rows` rows: n_vt vocabulary tiles (256 columns, or the rows
@@ -775,10 +793,10 @@ struct MxParts {
   int64_t n_vt, pad;
   size_t array, total;
 };
-MxParts mx_parts(int64_t M, int64_t rows, int64_t V, bool ent) {
+MxParts mx_parts(int64_t M, int64_t rows, int64_t H, int64_t V, bool ent) {
   MxParts p;
-  p.n_vt = cdiv(V, mx_streams(M) ? flce::mx_stream_rows(int(M), int(V)) : int(flce::kFwdTileN));
-  p.pad = mx_streams(M) ? rows : cdiv(rows, kTile) * kTile;
+  p.n_vt = cdiv(V, mx_streams(M, H, V) ? flce::mx_stream_rows(long(M), int(V)) : int(flce::kFwdTileN));
+  p.pad = mx_token_major(M, H, V) ? rows : cdiv(rows, kTile) * kTile;
   p.array = align_up(size_t(p.n_vt) * size_t(p.pad) * sizeof(float));
   p.total = (ent ? 3 : 2) * p.array + (rows > 0 ? flce::kQueueBytes : 0);
   return p;
@@ -786,7 +804,7 @@ MxParts mx_parts(int64_t M, int64_t rows, int64_t V, bool ent) {
 
 // Bytes of a forward wave of `rows` of the call's M rows: W's scales, X's copy, the partials.
 size_t mx_wave_bytes(int64_t M, int64_t rows, int64_t H, int64_t V, bool ent) {
-  return mx_w_bytes(M, H, V) + mx_x_bytes(M, rows, H) + mx_parts(M, rows, V, ent).total;
+  return mx_w_bytes(M, H, V) + mx_x_bytes(M, rows, H, V) + mx_parts(M, rows, H, V, ent).total;
 }
 
 // Tallest wave that fits in `bytes` (all M rows, or a multiple of 256); 0 if none does.
@@ -847,7 +865,7 @@ flce_status_t flce_mx_workspace_query(int64_t M, int64_t H, int64_t V, int compu
     return fail(FLCE_ERR_INVALID_VALUE, "compute_entropy must be 0 or 1");
   flce_status_t st = check_shape(M, H, V);
   if (st != FLCE_OK) return st;
-  if (logits_bytes) *logits_bytes = mx_w_bytes(M, H, V) + mx_x_bytes(M, M, H);
+  if (logits_bytes) *logits_bytes = mx_w_bytes(M, H, V) + mx_x_bytes(M, M, H, V);
   if (fwd_bytes) {
     const int64_t cap = max_wave_rows(V);
     *fwd_bytes = mx_wave_bytes(M, M < cap ? M : cap, H, V, compute_entropy == 1);
@@ -864,7 +882,7 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
   if (out_dtype != FLCE_BF16 && out_dtype != FLCE_FP32)
     return fail(FLCE_ERR_INVALID_VALUE, "unknown element type");
   if (M == 0) return ok();
-  const size_t need = mx_w_bytes(M, H, V) + mx_x_bytes(M, M, H);
+  const size_t need = mx_w_bytes(M, H, V) + mx_x_bytes(M, M, H, V);
   if (!out || (!workspace && need > 0))
     return fail(FLCE_ERR_INVALID_VALUE, "NULL pointer among out, workspace");
   if (ldo < V)
@@ -884,7 +902,7 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
   flce::MxOperand x{}, w;
   hipError_t e = mx_weights(W_codes, W_scales, M, H, V, ws, &w, stream);
   if (e != hipSuccess) return hip_fail(e, "scale layout kernel launch");
-  if (!own) e = mx_quantize_x(X, 0, M, H, mx_streams(M), ws + mx_w_bytes(M, H, V), nullptr, &x, stream);
+  if (!own) e = mx_quantize_x(X, 0, M, H, mx_streams(M, H, V), ws + mx_w_bytes(M, H, V), nullptr, &x, stream);
   if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
   // one launch covers up to max_wave_rows(V) rows (the dispatch limit)
   const int64_t rows = max_wave_rows(V);
@@ -901,10 +919,11 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
     a.out = static_cast<char*>(out) + r0 * ldo * (out_dtype == FLCE_BF16 ? 2 : 4);
     a.ldo = long(ldo);
     a.out_dtype = out_dtype;
+    a.call_M = long(M);
     a.n_mt = int(cdiv(a.M, flce::kFwdTileM));
     a.n_vt = int(cdiv(V, flce::kFwdTileN));
-    e = mx_streams(M) ? flce::launch_mx_stream_logits(a, stream)
-                      : flce::launch_mx_tile_logits(a, stream);
+    e = mx_streams(M, H, V) ? flce::launch_mx_stream_logits(a, stream)
+                            : flce::launch_mx_tile_logits(a, stream);
     if (e != hipSuccess) return hip_fail(e, "4-bit logits kernel launch");
   }
   return ok();
@@ -940,8 +959,8 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
   ws += mx_w_bytes(M, H, V);
   for (int64_t r0 = 0; r0 < M; r0 += rows) {
     const int64_t mw = M - r0 < rows ? M - r0 : rows;
-    const MxParts L = mx_parts(M, mw, V, ent);
-    char* part = ws + mx_x_bytes(M, mw, H);
+    const MxParts L = mx_parts(M, mw, H, V, ent);
+    char* part = ws + mx_x_bytes(M, mw, H, V);
     flce::MxFwdArgs a{};
     a.w = w;
     a.targets = targets + r0;
@@ -952,8 +971,8 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
     a.scale = scale;
     a.n_mt = int(cdiv(mw, flce::kFwdTileM));
     a.n_vt = int(L.n_vt);
-    a.tile_stride = mx_streams(M) ? 1 : long(L.pad);
-    a.token_stride = mx_streams(M) ? long(L.n_vt) : 1;
+    a.tile_stride = mx_token_major(M, H, V) ? 1 : long(L.pad);
+    a.token_stride = mx_token_major(M, H, V) ? long(L.n_vt) : 1;
     a.call_M = long(M);
     a.part_m = reinterpret_cast<float*>(part);
     a.part_s = reinterpret_cast<float*>(part + L.array);
@@ -966,10 +985,10 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
     if (flce::mx_stream_owns(M, H)) {
       a.X = static_cast<const uint16_t*>(X);
     } else {
-      e = mx_quantize_x(X, r0, mw, H, mx_streams(M), ws, tq.ctr, &a.x, stream);
+      e = mx_quantize_x(X, r0, mw, H, mx_streams(M, H, V), ws, tq.ctr, &a.x, stream);
       if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
     }
-    e = mx_streams(M) ? flce::launch_mx_stream_fwd(a, stream) : flce::launch_mx_tile_fwd(a, tq, stream);
+    e = mx_streams(M, H, V) ? flce::launch_mx_stream_fwd(a, stream) : flce::launch_mx_tile_fwd(a, tq, stream);
     if (e != hipSuccess) return hip_fail(e, "4-bit forward kernel launch");
     e = flce::launch_mx_merge(a, stream);
     if (e != hipSuccess) return hip_fail(e, "4-bit merge kernel launch");

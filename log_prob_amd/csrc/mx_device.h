@@ -138,6 +138,23 @@ __device__ __forceinline__ void store8(typename T::mem* row, long col, long cols
   }
 }
 
+// The first n of 16 bytes' elements to any element's address: one access where all of them count.
+template <class T>
+__device__ __forceinline__ void store_entries(typename T::mem* to, u32x4_t d, int n) {
+  constexpr int E = 16 / (int)sizeof(typename T::mem);
+  if (n >= E) {
+    if constexpr (E == 8) *reinterpret_cast<u32x4_a2*>(to) = d;
+    else *reinterpret_cast<u32x4_a4*>(to) = d;
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (i < n) {
+        if constexpr (E == 8) to[i] = (uint16_t)(d[i / 2] >> (16 * (i & 1)));
+        else to[i] = __uint_as_float(d[i]);
+      }
+  }
+}
+
 // Largest of the quad's values.
 __device__ __forceinline__ uint32_t quad_max(uint32_t a) {
   uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)a, 0xB1, 0xf, 0xf, true);

@@ -4,9 +4,11 @@
 //
 // With up to 128 tokens the kernel is bound by memory: W's codes and scales are read once.
 // They come through a ring of LDS stages by direct-to-LDS loads, 128 contiguous bytes of a row
-// for 8 lanes, two stages ahead of the products (loaded straight into the matrix
-// instruction's registers, 16 bytes a lane from 32 rows at once, one token over 151936 x 2048
-// took 60 us).  Two workgroups of four waves share a compute unit.
+// for 8 lanes, ahead of the products (loaded straight into the matrix instruction's registers,
+// 16 bytes a lane from 32 rows at once, one token over 151936 x 2048 took 60 us).  Two
+// workgroups of four waves share a compute unit, so a stage has 32 KiB at most (one workgroup
+// and three stages for 128 tokens: 65 us over 151936 x 2048 instead of 48).  More tokens run in
+// tiles of up to 128, bound by the loads to LDS and the reads from it.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -27,22 +29,35 @@ struct StreamCfg {
   static constexpr int RW = RW_, KW = KW_, XR = XR_;
   static constexpr bool OWN = XR == 0;
   static constexpr int TB = XR <= 32 ? 1 : XR / 32;       // 32-token blocks
-  static constexpr int ROWS = 32 * RW, NS = 3;            // vocabulary rows; stages
+  static constexpr int ROWS = 32 * RW;                    // vocabulary rows
   static constexpr int W_BYTES = KW * ROWS * 128, X_BYTES = KW * XR * 128;
   static constexpr int STAGE = W_BYTES + X_BYTES;
+  static constexpr int NS = XR > 64 ? 2 : 3;              // stages
   static constexpr int W_LOADS = W_BYTES / 4096;                       // a wave, 1 KiB each
   static constexpr int X_LOADS = (X_BYTES + 4095) / 4096;
   static constexpr int LOADS = W_LOADS + X_LOADS;
-  // scales: 64 bytes of a row (8 steps) at a time, double-buffered
+  // scales: SP 16-byte pieces of a row (of two steps each) at a time, double-buffered
+  static constexpr int SP = XR >= 64 ? 1 : 4, SCALE_STEPS = 2 * SP, SCALE_LD = 16 * SP;
+  static constexpr int LOAD_ROWS = 64 / SP;                            // rows of a load
   static constexpr int SCALE_ROWS = ROWS + (OWN ? 0 : XR < 16 ? 16 : XR);
-  static constexpr int SCALE_BUF = SCALE_ROWS * 64;
-  static constexpr int SCALE_LOADS = (SCALE_ROWS / 16 + 3) / 4;        // a wave, at most
+  static constexpr int SCALE_BUF = (SCALE_ROWS + LOAD_ROWS - 1) / LOAD_ROWS * 1024;
+  static constexpr int SCALE_LOADS = (SCALE_BUF / 1024 + 3) / 4;       // a wave, at most
   static constexpr int OWN_AT = NS * STAGE + 2 * SCALE_BUF;            // own codes, then scales
   static constexpr int LDS = OWN_AT + (OWN ? kMxOwnBytes + kMxOwnBytes / 8 : 0);
   static constexpr int MB = 1, NB = TB;  // as lane_col_max and lane_col_sums name them
   static_assert(RW * KW == 4 && W_BYTES == 16384, "four waves");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
+
+// Order of a step's products: one product a time, each but the last block's with a read of the
+// next block's (and its scales first).
+template <int... I>
+__device__ __forceinline__ void among(std::integer_sequence<int, I...>) {
+  constexpr int N = (int)sizeof...(I);
+  ((I < N - 4 ? __builtin_amdgcn_sched_group_barrier(0x100, I % 4 == 0 ? 2 : 1, 0) : (void)0,
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0)),
+   ...);
+}
 
 // acc[0][tb]: the wave's 32 vocabulary rows x token block tb, as (A = W, B = X) for the
 // log-probs (a lane then holds 16 vocabulary rows of one token) and as (A = X, B = W) for the
@@ -51,7 +66,7 @@ struct StreamCfg {
 template <class C, bool LOGITS>
 __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* smem, const uint16_t* X,
                                                const MxOperand& x, const MxOperand& w, int M, int H,
-                                               int V, int v0) {
+                                               int V, int v0, int m0) {
   constexpr int RW = C::RW, KW = C::KW, TB = C::TB, NS = C::NS;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -59,8 +74,9 @@ __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* sm
   const uint32_t ld = (uint32_t)mx_code_bytes(H, kMxFp4);
   const int blocks = (int)mx_blocks(H), steps = (blocks + 7) / 8, nk = (steps + KW - 1) / KW;
   const uint32_t lds0 = lds_addr_of(smem);
-  const i32x4 wr = make_rsrc_fixed(w.codes + (long)v0 * ld), xr = make_rsrc_fixed(x.codes);
+  const i32x4 wr = make_rsrc_fixed(w.codes + (long)v0 * ld), xr = make_rsrc_fixed(x.codes + (long)m0 * ld);
   const int wvalid = V - v0;
+  M -= m0;
 
   // loads of stage k (steps KW k .. + KW - 1): load i covers rows 8 (i % n) .. + 7 of step
   // KW k + i / n; lane l row l / 8, the chunk whose position is l % 8
@@ -89,20 +105,22 @@ __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* sm
       }
     }
   };
-  // scales of steps 8 c .. 8 c + 7: lane l row l / 4, 16-byte piece l % 4
+  // scales of SCALE_STEPS steps, chunk c: lane l row l / SP, 16-byte piece l % SP
   const int pieces = (int)(mx_scale_bytes(H) / 16);
-  const i32x4 ws = make_rsrc_fixed(w.scales + mx_scale_row(w.layout, v0)), xs = make_rsrc_fixed(x.scales);
+  const i32x4 ws = make_rsrc_fixed(w.scales + mx_scale_row(w.layout, v0)), xs = make_rsrc_fixed(x.scales + mx_scale_row(x.layout, m0));
   const uint32_t sld = (uint32_t)mx_scale_bytes(H);
   auto issue_scales = [&](int c) {
     const uint32_t buf = lds0 + (uint32_t)(NS * C::STAGE + (c & 1) * C::SCALE_BUF);
 #pragma unroll
     for (int q = 0; q < C::SCALE_LOADS; ++q) {
       const int i = 4 * q + wave;  // wave-uniform
-      if (i < C::SCALE_ROWS / 16) {
-        const bool is_w = i < C::ROWS / 16;
-        const int r = 16 * (is_w ? i : i - C::ROWS / 16) + (lane >> 2), p = 4 * c + (lane & 3);
-        const bool ok = r < (is_w ? wvalid : M) && p < pieces;
-        dma16<0>(C::OWN || is_w ? ws : xs, ok ? (uint32_t)r * sld + 16u * (uint32_t)p : OOB_OFFSET, 0u,
+      if (i < C::SCALE_BUF / 1024) {
+        const int r = C::LOAD_ROWS * i + lane / C::SP, p = C::SP * c + lane % C::SP;
+        // (a load's rows are all of W or all of X)
+        const bool is_w = C::LOAD_ROWS * i < C::ROWS;
+        const int rr = is_w ? r : r - C::ROWS;
+        const bool ok = rr < (is_w ? wvalid : M) && p < pieces;
+        dma16<0>(C::OWN || is_w ? ws : xs, ok ? (uint32_t)rr * sld + 16u * (uint32_t)p : OOB_OFFSET, 0u,
                  buf + 1024u * (uint32_t)i);
       }
     }
@@ -120,9 +138,9 @@ __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* sm
                     : (uint32_t)(C::W_BYTES + kw * C::XR * 128 + xrow * 128 +
                                  (((4 * half + kk) ^ mx_swz(xrow)) << 4));
   }
-  const uint32_t wsf = (uint32_t)((32 * rw + r) * 64 + 4 * half);
+  const uint32_t wsf = (uint32_t)((32 * rw + r) * C::SCALE_LD + 4 * half);
   const uint32_t xsf = C::OWN ? (uint32_t)(C::OWN_AT + kMxOwnBytes + xrow * (own_ld / 16) + 8 * kw + 4 * half)
-                              : (uint32_t)((C::ROWS + xrow) * 64 + 4 * half);
+                              : (uint32_t)((C::ROWS + xrow) * C::SCALE_LD + 4 * half);
 #pragma unroll
   for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
@@ -150,35 +168,42 @@ __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* sm
     // every wave is done with stage k - 1, whose slot the next loads take
     wait_vmcnt<C::LOADS*(NS - 2)>();
     __syncthreads();
-    const int c = KW * k / 8;
-    if (KW * k % 8 == 0) issue_scales(c + 1);
+    const int c = KW * k / C::SCALE_STEPS;
+    if (KW * k % C::SCALE_STEPS == 0) issue_scales(c + 1);
     issue(k + NS - 1, slot == 0 ? NS - 1 : slot - 1);
     const char* st = smem + slot * C::STAGE;
-    const char* sb = smem + NS * C::STAGE + (c & 1) * C::SCALE_BUF + 8 * ((KW * k + kw) & 7);
+    const char* sb = smem + NS * C::STAGE + (c & 1) * C::SCALE_BUF + 8 * ((KW * k + kw) & (C::SCALE_STEPS - 1));
     const int sw = *reinterpret_cast<const int*>(sb + wsf);
-    u32x4 wv[4];
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) wv[kk] = *reinterpret_cast<const u32x4*>(st + wf[kk]);
-#pragma unroll
-    for (int tb = 0; tb < TB; ++tb) {
-      const int sx = *reinterpret_cast<const int*>(C::OWN ? smem + xsf + 8 * KW * k : sb + xsf + 2048 * tb);
-      u32x4 xv[4];
+    u32x4 wv[4], xv[2][4];
+    int sx[2];
+    auto read_x = [&](int tb) {
+      sx[tb & 1] =
+          *reinterpret_cast<const int*>(C::OWN ? smem + xsf + 8 * KW * k : sb + xsf + 32 * C::SCALE_LD * tb);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        xv[kk] = *reinterpret_cast<const u32x4*>(C::OWN ? smem + xf[kk] + 128 * KW * k
-                                                        : st + xf[kk] + 4096 * tb);
-      if constexpr (LOGITS) {
-        acc[0][tb] = mx_mfma<0>(xv[0], wv[0], acc[0][tb], sx, sw);
-        acc[0][tb] = mx_mfma<1>(xv[1], wv[1], acc[0][tb], sx, sw);
-        acc[0][tb] = mx_mfma<2>(xv[2], wv[2], acc[0][tb], sx, sw);
-        acc[0][tb] = mx_mfma<3>(xv[3], wv[3], acc[0][tb], sx, sw);
-      } else {
-        acc[0][tb] = mx_mfma<0>(wv[0], xv[0], acc[0][tb], sw, sx);
-        acc[0][tb] = mx_mfma<1>(wv[1], xv[1], acc[0][tb], sw, sx);
-        acc[0][tb] = mx_mfma<2>(wv[2], xv[2], acc[0][tb], sw, sx);
-        acc[0][tb] = mx_mfma<3>(wv[3], xv[3], acc[0][tb], sw, sx);
-      }
+        xv[tb & 1][kk] = *reinterpret_cast<const u32x4*>(C::OWN ? smem + xf[kk] + 128 * KW * k
+                                                                : st + xf[kk] + 4096 * tb);
+    };
+    auto product = [&](auto kk, int tb) {
+      constexpr int K = decltype(kk)::value;
+      const int b = tb & 1;
+      acc[0][tb] = LOGITS ? mx_mfma<K>(xv[b][K], wv[K], acc[0][tb], sx[b], sw)
+                          : mx_mfma<K>(wv[K], xv[b][K], acc[0][tb], sw, sx[b]);
+    };
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) wv[kk] = *reinterpret_cast<const u32x4*>(st + wf[kk]);
+    read_x(0);
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) {
+      if (tb + 1 < TB) read_x(tb + 1);
+      product(std::integral_constant<int, 0>(), tb);
+      product(std::integral_constant<int, 1>(), tb);
+      product(std::integral_constant<int, 2>(), tb);
+      product(std::integral_constant<int, 3>(), tb);
     }
+    // the first block's ten reads, then each block's products among the reads of the next
+    __builtin_amdgcn_sched_group_barrier(0x100, 10, 0);
+    among(std::make_integer_sequence<int, 4 * TB>());
     slot = slot == NS - 1 ? 0 : slot + 1;
   }
   // the zero fills of the stages past the end must land before the LDS is used again
@@ -205,6 +230,17 @@ __device__ __forceinline__ void stream_product(f32x16 (&acc)[1][C::TB], char* sm
   }
 }
 
+// The vocabulary rows and tokens of a workgroup.
+template <class C>
+__device__ __forceinline__ void stream_coords(int M, int V, int& mt, int& vt) {
+  mt = 0;
+  vt = (int)blockIdx.x;
+  if constexpr (C::XR >= 64) {
+    const int n_mt = (M + 32 * C::TB - 1) / (32 * C::TB), n_vt = (V + C::ROWS - 1) / C::ROWS;
+    tile_coords((int)blockIdx.x, n_mt * n_vt, n_mt, n_vt, FWD_GROUP_M, mt, vt);
+  }
+}
+
 // The staging LDS, and a kilobyte that loads with nothing to bring may zero.
 template <class C>
 constexpr int stream_lds = C::LDS + (!C::OWN && C::X_BYTES < 4096 ? 1024 : 0);
@@ -213,19 +249,43 @@ template <class C, class T>
 __global__ __launch_bounds__(256) void mx_stream_logits_kernel(MxLogitsArgs p) {
   __shared__ __attribute__((aligned(1024))) char smem[stream_lds<C>];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int v0 = (int)blockIdx.x * C::ROWS;
+  int mt, vt;
+  stream_coords<C>(p.M, p.V, mt, vt);
+  const int v0 = vt * C::ROWS, m0 = mt * 32 * C::TB;
   f32x16 acc[1][C::TB];
-  stream_product<C, true>(acc, smem, p.X, p.x, p.w, p.M, p.H, p.V, v0);
-  const int v = v0 + 32 * (wave % C::RW) + (lane & 31);
-  if (wave / C::RW != 0 || v >= p.V) return;
-  typename T::mem* out = static_cast<typename T::mem*>(p.out) + v;
-#pragma unroll
-  for (int tb = 0; tb < C::TB; ++tb)
+  stream_product<C, true>(acc, smem, p.X, p.x, p.w, p.M, p.H, p.V, v0, m0);
+  typename T::mem* out = static_cast<typename T::mem*>(p.out);
+  if constexpr (C::XR < 64) {
+    const int v = v0 + 32 * (wave % C::RW) + (lane & 31);
+    if (wave / C::RW != 0 || v >= p.V) return;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const int m = 32 * tb + acc_row(lane, e);
-      if (m < p.M) out[(long)m * p.ldo] = T::from_f32(p.scale * acc[0][tb][e]);
+      const int m = m0 + acc_row(lane, e);
+      if (m < p.M) out[(long)m * p.ldo + v] = T::from_f32(p.scale * acc[0][0][e]);
     }
+  } else {
+    // many tokens: through LDS to rows of ROWS entries, 16 bytes a lane
+    constexpr int ES = (int)sizeof(typename T::mem), LD = C::ROWS * ES + 16, E = 16 / ES, CH = C::ROWS / E;
+    constexpr int JOIN = (C::KW - 1) * C::RW * C::TB * 4096;  // what the KW waves exchanged
+    static_assert(JOIN + 32 * C::TB * LD <= C::LDS, "staging");
+    char* tile = smem + JOIN;
+    if (wave / C::RW == 0) {
+#pragma unroll
+      for (int tb = 0; tb < C::TB; ++tb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          *reinterpret_cast<typename T::mem*>(tile + (32 * tb + acc_row(lane, e)) * LD +
+                                              (32 * (wave % C::RW) + (lane & 31)) * ES) =
+              T::from_f32(p.scale * acc[0][tb][e]);
+    }
+    __syncthreads();
+    const int rows = p.M - m0 < 32 * C::TB ? p.M - m0 : 32 * C::TB;
+    for (int i = threadIdx.x; i < rows * CH; i += 256) {
+      const int r = i / CH, c = i % CH, v = v0 + c * E;
+      const u32x4 d = *reinterpret_cast<const u32x4*>(tile + r * LD + 16 * c);
+      if (v < p.V) store_entries<T>(out + (long)(m0 + r) * p.ldo + v, d, p.V - v);
+    }
+  }
 }
 
 // Partials of the workgroup's vocabulary rows: maximum, then the shifted sums, each over the
@@ -237,9 +297,11 @@ __global__ __launch_bounds__(256) void mx_stream_fwd_kernel(MxFwdArgs p) {
   static_assert((3 * RW + (C::KW - 1) * RW * 32) * TT * 4 <= C::LDS, "epilogue buffers");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rw = wave % RW, kw = wave / RW, lc = lane & 31;
-  const int v0 = (int)blockIdx.x * C::ROWS;
+  int mt, vt;
+  stream_coords<C>(p.M, p.V, mt, vt);
+  const int v0 = vt * C::ROWS, m0 = mt * TT;
   f32x16 acc[1][TB];
-  stream_product<C, false>(acc, smem, p.X, p.x, p.w, p.M, p.H, p.V, v0);
+  stream_product<C, false>(acc, smem, p.X, p.x, p.w, p.M, p.H, p.V, v0, m0);
   // [rw][token] maxima and sums, behind what the KW waves exchanged
   float* red = reinterpret_cast<float*>(smem) + (C::KW - 1) * RW * TB * 1024;
   float* comb = red + RW * TT;
@@ -278,7 +340,7 @@ __global__ __launch_bounds__(256) void mx_stream_fwd_kernel(MxFwdArgs p) {
   }
   __syncthreads();
   const int t = threadIdx.x;
-  if (t < TT && t < p.M) {
+  if (t < TT && m0 + t < p.M) {
     float m = red[t], s = comb[t], u = comb[RW * TT + t];
 #pragma unroll
     for (int k = 1; k < RW; ++k) {
@@ -286,14 +348,17 @@ __global__ __launch_bounds__(256) void mx_stream_fwd_kernel(MxFwdArgs p) {
       s += comb[k * TT + t];
       u += comb[(RW + k) * TT + t];
     }
-    const long off = (long)blockIdx.x * p.tile_stride + t * p.token_stride;
+    const long off = (long)vt * p.tile_stride + (m0 + t) * p.token_stride;
     p.part_m[off] = ac1 * m * LN2;
     p.part_s[off] = s;
     if constexpr (ENT) p.part_u[off] = u * LN2;
   }
 }
 
-// The configuration for a call: `rows` is mx_stream_rows of it.
+// The configuration for M tokens of a call that takes `rows` vocabulary rows a workgroup
+// (mx_stream_rows); own: X has not been quantised.  Tiles of 64 tokens, three stages deep, where
+// all are resident at once; else of 96 or 128, of two stages, which load less for each product
+// (300 x 4096 x 4000 logits: 15 against 19 us; 600 x 1600 x 50257: 72 against 59 us).
 template <int XR, class F>
 void with_cfg(int rows, F f) {
   if (rows == 128) f(StreamCfg<4, 1, XR>());
@@ -305,11 +370,13 @@ void with_cfg(int rows, F f) {
   }
 }
 template <class F>
-void with_tokens(int M, int H, int rows, F f) {
-  if (mx_stream_owns(M, H)) with_cfg<0>(rows, f);
+void with_tokens(int M, int V, bool own, int rows, F f) {
+  if (own) with_cfg<0>(rows, f);
   else if (M <= 8) with_cfg<8>(rows, f);
   else if (M <= 32) with_cfg<32>(rows, f);
-  else if (M <= 64) with_cfg<64>(rows, f);
+  else if (M <= 64 || rows == 64 || (V + 127) / 128 * (int64_t)((M + 63) / 64) <= kMxStreamResident)
+    with_cfg<64>(rows, f);
+  else if ((M + 127) / 128 * 96 >= M) with_cfg<96>(rows, f);
   else with_cfg<128>(rows, f);
 }
 
@@ -431,30 +498,34 @@ __global__ __launch_bounds__(MERGE_THREADS) void mx_merge_kernel(MxFwdArgs p) {
 
 }  // namespace
 
-// Fewer vocabulary rows a workgroup, with the waves sharing K instead, where 128 would leave
-// less than one and a half workgroups a compute unit (as far as the staged tokens fit).
-int mx_stream_rows(int M, int V) {
-  if (M > 64 || (V + 127) / 128 >= 384) return 128;
+// Fewer vocabulary rows a workgroup, with the waves sharing K instead, where 128 (and 64
+// tokens) would leave less than one and a half workgroups a compute unit, as far as the staged
+// tokens fit.  Of the whole call, for the order of summation.
+int mx_stream_rows(long M, int V) {
+  const int64_t n_mt = (M + 63) / 64;
+  if ((V + 127) / 128 * n_mt >= 384) return 128;
   if (M > 32 || (V + 63) / 64 >= 384) return 64;
   return 32;
 }
 
 hipError_t launch_mx_stream_logits(const MxLogitsArgs& a, hipStream_t s) {
-  const int rows = mx_stream_rows(a.M, a.V);
+  const int rows = mx_stream_rows(a.call_M, a.V);
   const unsigned g = (unsigned)(((int64_t)a.V + rows - 1) / rows);
-  with_tokens(a.M, a.H, rows, [&](auto cfg) {
+  with_tokens(a.M, a.V, a.X != nullptr, rows, [&](auto cfg) {
     using C = decltype(cfg);
-    if (a.out_dtype == kBf16) mx_stream_logits_kernel<C, Bf16><<<g, 256, 0, s>>>(a);
-    else mx_stream_logits_kernel<C, F32><<<g, 256, 0, s>>>(a);
+    const unsigned n = g * (unsigned)((a.M + 32 * C::TB - 1) / (32 * C::TB));
+    if (a.out_dtype == kBf16) mx_stream_logits_kernel<C, Bf16><<<n, 256, 0, s>>>(a);
+    else mx_stream_logits_kernel<C, F32><<<n, 256, 0, s>>>(a);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_mx_stream_fwd(const MxFwdArgs& a, hipStream_t s) {
-  with_tokens(a.M, a.H, mx_stream_rows(a.M, a.V), [&](auto cfg) {
+  with_tokens(a.M, a.V, a.X != nullptr, mx_stream_rows(a.call_M, a.V), [&](auto cfg) {
     using C = decltype(cfg);
-    if (a.part_u) mx_stream_fwd_kernel<C, true><<<(unsigned)a.n_vt, 256, 0, s>>>(a);
-    else mx_stream_fwd_kernel<C, false><<<(unsigned)a.n_vt, 256, 0, s>>>(a);
+    const unsigned n = (unsigned)a.n_vt * (unsigned)((a.M + 32 * C::TB - 1) / (32 * C::TB));
+    if (a.part_u) mx_stream_fwd_kernel<C, true><<<n, 256, 0, s>>>(a);
+    else mx_stream_fwd_kernel<C, false><<<n, 256, 0, s>>>(a);
   });
   return hipGetLastError();
 }

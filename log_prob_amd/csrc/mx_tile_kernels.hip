@@ -342,19 +342,8 @@ __global__ __launch_bounds__(256, 1) void mx_tile_logits_kernel(MxLogitsArgs p) 
       const int t = t0 + 32 * nb + r, col = v0 + c * E;
       typename T::mem* to = out + (long)t * p.ldo + col;
       if (t >= p.M || col >= p.V) continue;
-      if constexpr (VEC) {
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(to));
-      } else if (col + E <= p.V) {
-        if constexpr (ES == 2) *reinterpret_cast<u32x4_a2*>(to) = v;
-        else *reinterpret_cast<u32x4_a4*>(to) = v;
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-          if (col + i < p.V) {
-            if constexpr (ES == 2) to[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
-            else to[i] = __uint_as_float(v[i]);
-          }
-      }
+      if constexpr (VEC) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(to));
+      else store_entries<T>(to, v, p.V - col);
     }
     // the slice's reads have returned before the next 32 tokens overwrite it
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");

@@ -105,8 +105,9 @@ hipError_t launch_mx_quantize(const MxQuantArgs& a, int dtype, int fmt, bool vec
 hipError_t launch_mx_dequantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s);
 
 // The head with 4-bit weights: X and W as MXFP4 codes and scales.  Calls of at most
-// kMxStreamTokens tokens run the kernels that stream W through registers.
-constexpr int64_t kMxStreamTokens = 128;
+// kMxStreamTokens tokens always run the kernels that stream W past the tokens, of which
+// kMxStreamResident workgroups run at once.
+constexpr int64_t kMxStreamTokens = 128, kMxStreamResident = 512;
 struct MxOperand {
   const uint8_t* codes;
   const uint8_t* scales;
@@ -128,6 +129,7 @@ struct MxLogitsArgs {
   void* out;               // [M, V] logits
   long ldo;
   int out_dtype;
+  long call_M;             // rows of the whole call, of which M are this launch
   int n_mt, n_vt;          // 256 x 256 tiles (the tile kernel)
 };
 
@@ -152,7 +154,7 @@ struct MxFwdArgs {
 };
 
 // The kernels for few tokens: vocabulary rows a workgroup takes, for a call of M tokens.
-int mx_stream_rows(int M, int V);
+int mx_stream_rows(long M, int V);
 hipError_t launch_mx_stream_logits(const MxLogitsArgs& a, hipStream_t s);
 hipError_t launch_mx_stream_fwd(const MxFwdArgs& a, hipStream_t s);
 hipError_t launch_mx_tile_logits(const MxLogitsArgs& a, hipStream_t s);

@@ -87,7 +87,11 @@ SHAPES = [(1, 8, 1), (1, 32, 40), (2, 24, 33), (1, 256, 1000), (3, 248, 255), (5
           # give a workgroup 32, 64 and 128 rows
           (8, 2048, 1400), (8, 2080, 500), (7, 4096, 300), (2, 8200, 100), (1, 16392, 70),
           (5, 520, 25000), (8, 2568, 24600), (30, 264, 25001), (50, 136, 24999), (1, 264, 50257),
-          (8, 520, 50000), (8, 3080, 49200), (20, 136, 50257), (64, 136, 50000), (100, 72, 50257)]
+          (8, 520, 50000), (8, 3080, 49200), (20, 136, 50257), (64, 136, 50000), (100, 72, 50257),
+          # more tokens in tiles of 64, 96 and 128, past 1024 tokens, and over vocabularies that
+          # take the 256 x 256 tiles
+          (130, 2056, 1003), (600, 136, 700), (200, 264, 30001), (257, 520, 30000), (400, 264, 33000),
+          (1500, 72, 2000), (512, 72, 32501), (500, 776, 32003), (1000, 520, 16101), (1280, 40, 13001)]
 
 
 @pytest.mark.parametrize("M,H,V", SHAPES)
@@ -98,9 +102,9 @@ def test_shapes(M, H, V):
 
 
 @pytest.mark.parametrize("scale", [1 / 0.7, -0.5, 0.0, 37.0])
-@pytest.mark.parametrize("M", [4, 70, 150, 300])
-def test_scales(M, scale):
-    X, W, t = make(M, 200, 1300, M)
+@pytest.mark.parametrize("M,V", [(4, 1300), (70, 1300), (150, 1300), (300, 40000), (500, 32100)])
+def test_scales(M, V, scale):
+    X, W, t = make(M, 200, V, M)
     check_logits(X, W, scale, f"scale {scale}")
     check_forward(X, W, t, scale, f"scale {scale}")
     check_forward(X, W, t, scale, f"scale {scale}", ent=False)
@@ -120,11 +124,11 @@ def test_rows_of_every_magnitude(M):
                     ou.U32 * (np.abs(z) + e) + e, "magnitudes")
 
 
-@pytest.mark.parametrize("M", [1, 40, 140, 300])
-def test_nonfinite_tokens_stay_in_their_rows(M):
+@pytest.mark.parametrize("M,V", [(1, 700), (40, 700), (140, 700), (300, 40000), (500, 32100)])
+def test_nonfinite_tokens_stay_in_their_rows(M, V):
     import torch
     from log_prob_amd import flce
-    X, W, t = make(M, 264, 700, 8)
+    X, W, t = make(M, 264, V, 8)
     X2 = X.clone()
     X2[M // 2, 100] = float("inf")
     for f in (lambda x: flce.mxfp4_logits(x, W), lambda x: flce.mxfp4_forward(x, W, t.clamp(min=0))[1]):
@@ -136,7 +140,8 @@ def test_nonfinite_tokens_stay_in_their_rows(M):
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("M,V,pad,shift", [(3, 1000, 24, 0), (3, 1001, 0, 0), (300, 1001, 7, 0),
                                            (300, 1000, 8, 8), (260, 515, 0, 1), (300, 999, 1, 3),
-                                           (129, 1000, 4, 0)])
+                                           (129, 1000, 4, 0), (500, 32000, 8, 8), (500, 32001, 7, 0),
+                                           (512, 32003, 1, 3), (300, 40001, 2, 1)])
 def test_output_strides(M, V, pad, shift, dtype):
     """Rows inside wider rows, at any natural alignment; what lies between is left alone."""
     import torch
@@ -151,7 +156,8 @@ def test_output_strides(M, V, pad, shift, dtype):
     assert (buf[shift:shift + M * (V + pad)].view(M, V + pad)[:, V:] == 7.0).all()
 
 
-@pytest.mark.parametrize("H,V,M", [(264, 1700, 1000), (512, 300, 520), (72, 20000, 2500)])
+@pytest.mark.parametrize("H,V,M", [(264, 1700, 1000), (512, 300, 520), (72, 20000, 2500), (264, 16000, 1000),
+                                   (72, 13000, 1280)])
 def test_waves_give_the_same_bits(H, V, M):
     """Any workspace from one 256-row wave up; stale and guard bytes do not matter."""
     import torch
@@ -159,7 +165,21 @@ def test_waves_give_the_same_bits(H, V, M):
     X, W, t = make(M, H, V, 11)
     ref = check_forward(X, W, t, 1.0, "one wave")
     full = flce.mxfp4_workspace_query(M, H, V)[1]
-    least = flce.mxfp4_workspace_query(256, H, V)[1]
+
+    def takes(n):
+        try:
+            flce.mxfp4_forward(X, W, t, IGNORE, workspace=torch.empty(n, dtype=torch.uint8, device="cuda"))
+        except flce.FlceError as err:
+            assert err.status == 3
+            return False
+        return True
+
+    # the smallest workspace that is accepted, a wave of at most 256 rows
+    none, least = 0, full
+    while least - none > 1:
+        mid = (none + least) // 2
+        none, least = (none, mid) if takes(mid) else (mid, least)
+    assert least <= full // 2 + 256
     for n in (full, full - 1, (full + least) // 2, least):
         ws = torch.full((n + 64,), 0xFF, dtype=torch.uint8, device="cuda")
         got = flce.mxfp4_forward(X, W, t, IGNORE, workspace=ws[:n])

@@ -167,10 +167,14 @@ def test_mx_workspace():
     lo, fw = flce.mxfp4_workspace_query(20, 64, 100)
     assert lo == 768 + 512 and fw == lo + 3 * 512 + 256
     assert mx_forward(M=20, wb=fw - 1) == TOO_SMALL and logits(M=20, wb=lo - 1) == TOO_SMALL
-    # larger calls: 256-column tiles of 256-row multiples; whole scale tiles of X
-    lo, fw = flce.mxfp4_workspace_query(300, 64, 1000, False)
-    assert lo == 9728 + 512 * 16
-    assert fw == lo + 2 * 4 * 4 * 512 + 256
+    # past 1024 tokens in small tiles: partials of 256-row multiples
+    lo, fw = flce.mxfp4_workspace_query(1500, 64, 2000, False)
+    assert lo == 1500 * 32 + 128 + 1500 * 16 + 64
+    assert fw == lo + 2 * 4 * 16 * 1536 + 256
+    # 256 x 256 tiles: whole scale tiles of X
+    lo, fw = flce.mxfp4_workspace_query(500, 64, 32000, False)
+    assert lo == 500 * 32 + 128 + 512 * 16
+    assert fw == lo + 2 * 4 * 125 * 512 + 256
     # and past 2.5e11 products a copy of W's scales
     lo, _ = flce.mxfp4_workspace_query(4096, 4096, 32768)
     assert lo == 32768 * 128 + 4096 * (2048 + 128)

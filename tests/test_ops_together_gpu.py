@@ -126,8 +126,9 @@ def test_scoring_and_sampling():
     assert torch.equal(per_tok, -adv) and not clipped.any()   # the same policy: ratio 1
 
 
-@pytest.mark.parametrize("M,H,V", [(40, 264, 1500), (300, 264, 1500), (4096, 256, 32800)],
-                         ids=["stream", "tile", "queued_tiles"])
+@pytest.mark.parametrize("M,H,V", [(6, 264, 1500), (40, 264, 1500), (300, 264, 1500),
+                                   (500, 264, 32100), (4096, 256, 32800)],
+                         ids=["own", "stream", "token_tiles", "tile", "queued_tiles"])
 def test_graph_replays_match_eager(M, H, V):
     """A training step around the head and a pass of the 4-bit head in one captured graph,
     replayed with eager work and synchronisation between."""
