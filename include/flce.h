@@ -440,12 +440,12 @@ flce_status_t flce_layer_norm_backward(const void* dy, int dy_dtype, int64_t ldd
 /*
  * The head with 4-bit weights: W [V, H] as FLCE_MXFP4 codes and scales from
  * flce_mx_quantize, for sampling from a compressed head (logits) and for scoring with a
- * frozen reference model (log-probs).  X [M, H] bf16 is rounded to MXFP4 on the way (into
- * the workspace), so
+ * frozen reference model (log-probs).  X [M, H] bf16 is rounded to MXFP4 on the way, so
  *   z[m, v] = scale * sum_k Q(X)[m, k] W[v, k]
- * with exact products and fp32 accumulation.  Shapes as in flce_workspace_query; X and
- * both parts of W 16-byte aligned.  A row of X that holds an infinity or a NaN gives NaNs
- * in its own outputs.
+ * with exact products and fp32 accumulation, in an order that depends on the shape of the
+ * call (never on the workspace).  Shapes as in flce_workspace_query; X and both parts of W
+ * 16-byte aligned; a vocabulary shard is a slice of W's rows.  A row of X that holds an
+ * infinity or a NaN gives NaNs in its own outputs.
  *
  * flce_mx_logits writes z to out [M, V] (bf16 or fp32, any row stride >= V, naturally
  * aligned).  flce_mx_forward writes logprob, lse and entropy of targets, which never leave
@@ -453,8 +453,7 @@ flce_status_t flce_layer_norm_backward(const void* dy, int dy_dtype, int64_t ldd
  * with z from the 4-bit operands.  Workspaces: 256-byte aligned; flce_mx_workspace_query
  * gives what flce_mx_logits needs and what flce_mx_forward takes all rows at once with (a
  * smaller one, down to one wave of 256 rows, runs in waves; for large calls both hold a copy
- * of W's scale bytes in another order).  M = 0 is accepted and
- * touches nothing.  Not differentiable: the weights are frozen.
+ * of W's scale bytes in another order).  M = 0 is accepted and touches nothing.  Not differentiable: the weights are frozen.
  */
 flce_status_t flce_mx_workspace_query(int64_t M, int64_t H, int64_t V, int compute_entropy,
                                       size_t* logits_bytes, size_t* fwd_bytes);

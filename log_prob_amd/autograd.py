@@ -90,5 +90,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out_dtype=None, che
     bits; y has out_dtype (x's by default).  With checkpoint "mxfp8" or "mxint8" the graph
     keeps an 8-bit copy of x instead of x: y is unchanged, and the gradients are those of the
     copy's values (about half a step of the format from x: 2^-4 relative for "mxfp8", 2^-7 of
-    the largest of 32 neighbours for "mxint8")."""
+    the largest of 32 neighbours for "mxint8").  To capture forward and backward in a graph,
+    first let go of eager results that lead back to the same leaves: torch would make the
+    captured backward wait for their stream."""
     return FusedLayerNorm.apply(x, weight, bias, eps, out_dtype, checkpoint)

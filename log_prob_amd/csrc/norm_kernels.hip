@@ -477,7 +477,8 @@ constexpr int kComputeUnits = 256;
 // the forward gives a thread two (8192 x 8192: 59 us against 75 us with 1024 threads, whose
 // barriers span 16 waves); the backward, with its column sums in registers, does not (88 us
 // against 119 us before its loads ran ahead), but keeps rows of up to 1024 in a wave, without
-// a barrier (65535 x 1024: 79 us against 85 us).  Workgroups stay and walk the rows, so the parameters are read once each.
+// a barrier (65535 x 1024: 79 us against 85 us).  Workgroups stay and walk the rows, so each
+// reads the parameters once.
 template <class TX, class TY, bool VEC>
 void fwd_rows(const NormFwdArgs& a, hipStream_t s) {
   auto grid = [&](int rows_per_group, int groups_per_unit) {

@@ -94,10 +94,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.flce_mx_workspace_query.argtypes = [I64, I64, I64, I, c.POINTER(SZ), c.POINTER(SZ)]
     lib.flce_mx_logits.argtypes = [P, P, P, I64, I64, I64, c.c_float, P, I, I64, P, SZ, P]
     lib.flce_mx_forward.argtypes = [P, P, P, P, I64, I64, I64, I64, c.c_float, I, P, P, P, P, SZ, P]
-    for name in ("flce_mx_workspace_query", "flce_mx_logits", "flce_mx_forward", "flce_mx_sizes", "flce_mx_quantize", "flce_mx_dequantize",
+    for name in ("flce_mx_workspace_query", "flce_mx_logits", "flce_mx_forward",
+                 "flce_mx_sizes", "flce_mx_quantize", "flce_mx_dequantize",
                  "flce_layer_norm_forward", "flce_layer_norm_backward_workspace",
-                 "flce_layer_norm_backward", "flce_nll_reduce", "flce_nll_mean_grad", "flce_policy_loss_reduce",
-                 "flce_policy_loss_grad", "flce_workspace_query",
+                 "flce_layer_norm_backward", "flce_nll_reduce", "flce_nll_mean_grad",
+                 "flce_policy_loss_reduce", "flce_policy_loss_grad", "flce_workspace_query",
                  "flce_forward_workspace_min", "flce_forward_wave_rows",
                  "flce_backward_workspace_min", "flce_backward_chunk_cols",
                  "flce_backward_wave_rows", "flce_backward_schedule", "flce_forward",
