@@ -377,49 +377,64 @@ __global__ __launch_bounds__(WIDE) void norm_fwd_wide_kernel(NormFwdArgs p) {
   }
 }
 
-// Column sums travel through the workgroup's own row of partial sums: cleared by its first
-// row, added to by the others (each element always by the same thread).
+// The backward of such rows reads x and dy once for the column sums and once for dx (with the
+// column sums in the workgroup's row of partial sums, read and written for every row, 3000 x
+// 20000 bf16 took 253 us instead of 141).  Column sums: a thread's 8 columns over the rows of
+// group blockIdx.y.
+template <class TX, class TY, bool VEC>
+__global__ __launch_bounds__(256) void norm_bwd_columns_kernel(NormBwdArgs p) {
+  const int H = p.H, col = 8 * ((int)blockIdx.x * 256 + (int)threadIdx.x);
+  if (col >= H) return;
+  float dw[8], db[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0.f;
+#pragma unroll 4
+  for (long row = blockIdx.y; row < p.M; row += p.groups) {
+    Input<TX, VEC> in;
+    Chunk8<TY, VEC> c;
+    in.load(p, row, col);
+    c.load(static_cast<const typename TY::mem*>(p.dy) + row * p.lddy, col, H);
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    float x[8], dy[8];
+    in.value(p, col, x);
+    c.value(col, H, dy);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dw[i] = fmaf(dy[i], (x[i] - mean) * rstd, dw[i]);
+      db[i] += dy[i];
+    }
+  }
+  float* pw = p.part + (long)blockIdx.y * H;
+  store8<F32, VEC>(pw, col, H, dw);
+  store8<F32, VEC>(pw + (long)p.groups * H, col, H, db);
+}
+
 template <class TX, class TY, class TD, bool VEC>
 __global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormBwdArgs p) {
   __shared__ float red[4 * (WIDE / 64)];
   RowSum<WIDE> sum{red};
   const int t = threadIdx.x, H = p.H;
   const float rh = 1.f / (float)H;
-  float* pw = p.part + (long)blockIdx.x * H;
-  float* pb = pw + (long)p.groups * H;
-  bool first = true;
   for (long row = blockIdx.x; row < p.M; row += gridDim.x) {
     const typename TY::mem* dy = static_cast<const typename TY::mem*>(p.dy) + row * p.lddy;
     typename TD::mem* dx = static_cast<typename TD::mem*>(p.dx) + row * p.lddx;
     const float mean = p.mean[row], rstd = p.rstd[row];
     float s[2] = {0.f, 0.f};
-    float x[8], g[8], w[8], a[8], b[8];
+    float x[8], g[8], w[8];
     for (int col = 8 * t; col < H; col += 8 * WIDE) {
       Input<TX, VEC> in;
       in.load(p, row, col);
       in.value(p, col, x);
       load8<TY, VEC>(dy, col, H, g);
       load_param<VEC>(p.weight, p.param_dtype, col, H, 1.f, w);
-      if (first) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.f;
-      } else {
-        load8<F32, VEC>(pw, col, H, a);
-        load8<F32, VEC>(pb, col, H, b);
-      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float xh = (x[i] - mean) * rstd;
-        a[i] = fmaf(g[i], xh, a[i]);
-        b[i] += g[i];
+        // past the row g is 0, and so is its share of both sums
         g[i] *= w[i];
         s[0] += g[i];
-        s[1] = fmaf(g[i], xh, s[1]);
+        s[1] = fmaf(g[i], (x[i] - mean) * rstd, s[1]);
       }
-      store8<F32, VEC>(pw, col, H, a);
-      store8<F32, VEC>(pb, col, H, b);
     }
-    first = false;
     sum(s);
     const float m0 = s[0] * rh, m1 = s[1] * rh;
     for (int col = 8 * t; col < H; col += 8 * WIDE) {
@@ -436,9 +451,9 @@ __global__ __launch_bounds__(WIDE) void norm_bwd_wide_kernel(NormBwdArgs p) {
 }
 
 // dweight and dbias: the sum of the groups' partial rows, in a fixed order.  A workgroup
-// takes 16 columns (64-byte pieces of the partial rows, so that a few thousand columns fill
-// the chip); 64 slices of threads share the groups and meet in LDS.
-constexpr int REDUCE_COLS = 16, REDUCE_SLICES = 64;
+// takes 32 columns (whole lines of the partial rows; of 16 columns, 2 to 3 us more at H = 8192);
+// 32 slices of threads share the groups and meet in LDS.
+constexpr int REDUCE_COLS = 32, REDUCE_SLICES = 32;
 __global__ __launch_bounds__(REDUCE_COLS * REDUCE_SLICES) void norm_reduce_kernel(NormReduceArgs p) {
   __shared__ float part[REDUCE_SLICES][REDUCE_COLS];
   const int lane = threadIdx.x % REDUCE_COLS, slice = threadIdx.x / REDUCE_COLS;
@@ -523,8 +538,13 @@ void bwd_rows(const NormBwdArgs& a, hipStream_t s) {
     norm_bwd_kernel<TX, TY, TD, 512, 1, VEC><<<g, 512, 0, s>>>(a);
   else if (a.H <= 8192)
     norm_bwd_kernel<TX, TY, TD, 1024, 1, VEC><<<g, 1024, 0, s>>>(a);
-  else
-    norm_bwd_wide_kernel<TX, TY, TD, VEC><<<g, WIDE, 0, s>>>(a);
+  else {
+    // (the columns first: dx may overwrite x or dy)
+    if (a.params)
+      norm_bwd_columns_kernel<TX, TY, VEC><<<dim3((a.H + 2047) / 2048, g), 256, 0, s>>>(a);
+    const long most = 2 * kComputeUnits;
+    norm_bwd_wide_kernel<TX, TY, TD, VEC><<<(unsigned)(a.M < most ? a.M : most), WIDE, 0, s>>>(a);
+  }
 }
 
 template <class TX, class TY, class TD>

@@ -187,6 +187,7 @@ flce_status_t flce_layer_norm_backward(const void* dy, int dy_dtype, int64_t ldd
   a.H = int(H);
   a.dx = dx;
   a.lddx = long(lddx);
+  a.params = dweight || dbias;
   a.part = static_cast<float*>(workspace);
   if (M > 0) {
     const bool vec = H % 8 == 0 && vectors(dy, dy_dtype, lddy) && vectors(dx, dx_dtype, lddx) &&

@@ -56,6 +56,7 @@ struct NormBwdArgs {
   int H;
   void* dx;
   long lddx;
+  bool params;             // whether the partial sums are wanted
   float* part;             // [2][groups][H] partial sums of dweight and dbias
   int groups;              // workgroups of the row kernel = rows of each partial array
 };
