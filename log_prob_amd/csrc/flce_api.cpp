@@ -772,8 +772,9 @@ bool mx_streams(int64_t M, int64_t H, int64_t V) {
 // tokens outnumber the workgroups that run at once.
 bool mx_token_major(int64_t M, int64_t H, int64_t V) { return M <= 1024 && mx_streams(M, H, V); }
 // The large tiles' kernels read scales fastest in a form of their own, and X's are written so;
-// turning W's costs a launch and a pass over them (3 to 8 us), which calls of this size win
-// back (M=H=4096, V=128256: 1081 -> 1036 us; M=257, H=1600, V=50257: 54 -> 58 us).
+// turning W's costs a pass over them beside X's quantisation (a launch of its own before it took
+// 2 to 3 us more), which calls of this size win back (M=H=4096, V=128256: 1081 -> 1036 us;
+// M=1024, H=4096, V=32768: 76 -> 79 us).
 bool mx_turns(int64_t M, int64_t H, int64_t V) {
   return M >= 2048 && double(M) * double(H) * double(V) >= 2.5e11 && !mx_streams(M, H, V);
 }
@@ -832,27 +833,29 @@ flce_status_t check_mx_call(const void* X, const void* W_codes, const void* W_sc
   return FLCE_OK;
 }
 
-// Quantise rows [r0, r0 + rows) of X to ws, its scales laid out for the call's kernels, and
-// zero the 8 counters at `clear` (if not nullptr).
+// Quantise rows [r0, r0 + rows) of X to ws, its scales laid out for the call's kernels, and on
+// the way zero the 8 counters at `clear` (if not nullptr) and re-order W's scales (`turn`).
 hipError_t mx_quantize_x(const void* X, int64_t r0, int64_t rows, int64_t H, bool stream_form, char* ws,
-                         unsigned long long* clear, flce::MxOperand* x, hipStream_t stream) {
+                         unsigned long long* clear, const flce::MxTurn& turn, flce::MxOperand* x,
+                         hipStream_t stream) {
   uint8_t* codes = reinterpret_cast<uint8_t*>(ws);
   uint8_t* scales = codes + mx_x_codes_bytes(rows, H);
   *x = flce::MxOperand{codes, scales, stream_form ? flce::mx_row_major(H) : flce::mx_tiled(H)};
   const flce::MxQuantArgs q{static_cast<const uint16_t*>(X) + r0 * H, long(H), nullptr, 0, codes,
-                            scales, long(rows), long(H), x->layout, clear};
+                            scales, long(rows), long(H), x->layout, clear, turn};
   return flce::launch_mx_quantize(q, flce::kBf16, flce::kMxFp4, true, stream);
 }
 
-// W as the call's kernels read it: as given, or with its scales turned into ws.
-hipError_t mx_weights(const void* W_codes, const void* W_scales, int64_t M, int64_t H, int64_t V,
-                      char* ws, flce::MxOperand* w, hipStream_t stream) {
+// W as the call's kernels read it: as given, or with its scales re-ordered into ws by `turn`,
+// which the first quantisation of X has to do.
+flce::MxOperand mx_weights(const void* W_codes, const void* W_scales, int64_t M, int64_t H, int64_t V,
+                           char* ws, flce::MxTurn* turn) {
+  const uint8_t* codes = static_cast<const uint8_t*>(W_codes);
   const uint8_t* scales = static_cast<const uint8_t*>(W_scales);
-  *w = flce::MxOperand{static_cast<const uint8_t*>(W_codes), scales, flce::mx_row_major(H)};
-  if (!mx_turns(M, H, V)) return hipSuccess;
-  w->scales = reinterpret_cast<uint8_t*>(ws);
-  w->layout = flce::mx_tiled(H);
-  return flce::launch_mx_turn_scales(scales, reinterpret_cast<uint8_t*>(ws), long(V), long(H), stream);
+  *turn = flce::MxTurn{};
+  if (!mx_turns(M, H, V)) return {codes, scales, flce::mx_row_major(H)};
+  *turn = flce::mx_turn(scales, reinterpret_cast<uint8_t*>(ws), V, H);
+  return {codes, turn->dst, flce::mx_tiled(H)};
 }
 
 }  // namespace
@@ -899,10 +902,12 @@ flce_status_t flce_mx_logits(const void* X, const void* W_codes, const void* W_s
     return fail(FLCE_ERR_WORKSPACE_TOO_SMALL, "logits need %zu workspace bytes, got %zu", need,
                 workspace_bytes);
   char* ws = static_cast<char*>(workspace);
-  flce::MxOperand x{}, w;
-  hipError_t e = mx_weights(W_codes, W_scales, M, H, V, ws, &w, stream);
-  if (e != hipSuccess) return hip_fail(e, "scale layout kernel launch");
-  if (!own) e = mx_quantize_x(X, 0, M, H, mx_streams(M, H, V), ws + mx_w_bytes(M, H, V), nullptr, &x, stream);
+  flce::MxTurn turn;
+  const flce::MxOperand w = mx_weights(W_codes, W_scales, M, H, V, ws, &turn);
+  flce::MxOperand x{};
+  hipError_t e = hipSuccess;
+  if (!own)
+    e = mx_quantize_x(X, 0, M, H, mx_streams(M, H, V), ws + mx_w_bytes(M, H, V), nullptr, turn, &x, stream);
   if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
   // one launch covers up to max_wave_rows(V) rows (the dispatch limit)
   const int64_t rows = max_wave_rows(V);
@@ -953,9 +958,9 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
                 "4-bit forward needs at least %zu workspace bytes, got %zu",
                 mx_wave_bytes(M, M < kTile ? M : kTile, H, V, ent), workspace_bytes);
   char* ws = static_cast<char*>(workspace);
-  flce::MxOperand w;
-  hipError_t e = mx_weights(W_codes, W_scales, M, H, V, ws, &w, stream);
-  if (e != hipSuccess) return hip_fail(e, "scale layout kernel launch");
+  flce::MxTurn turn;
+  const flce::MxOperand w = mx_weights(W_codes, W_scales, M, H, V, ws, &turn);
+  hipError_t e = hipSuccess;
   ws += mx_w_bytes(M, H, V);
   for (int64_t r0 = 0; r0 < M; r0 += rows) {
     const int64_t mw = M - r0 < rows ? M - r0 : rows;
@@ -985,7 +990,8 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
     if (flce::mx_stream_owns(M, H)) {
       a.X = static_cast<const uint16_t*>(X);
     } else {
-      e = mx_quantize_x(X, r0, mw, H, mx_streams(M, H, V), ws, tq.ctr, &a.x, stream);
+      e = mx_quantize_x(X, r0, mw, H, mx_streams(M, H, V), ws, tq.ctr, turn, &a.x, stream);
+      turn = flce::MxTurn{};
       if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
     }
     e = mx_streams(M, H, V) ? flce::launch_mx_stream_fwd(a, stream) : flce::launch_mx_tile_fwd(a, tq, stream);

@@ -26,16 +26,33 @@ __device__ __forceinline__ long scale_at(const MxScaleLayout& l, long b) {
   return (b >> 4) * l.quad_stride + (b & 15);
 }
 
+// 16-byte pieces from [rows][quads] to [rows / 256][quads][256]: 8 lanes read 128 contiguous
+// bytes of a row and 8 write 128 of a quad.
+__device__ __forceinline__ void turn_scales(const MxTurn& p, unsigned group) {
+  const u32x4_t* src = reinterpret_cast<const u32x4_t*>(p.src);
+  u32x4_t* dst = reinterpret_cast<u32x4_t*>(p.dst);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, qtiles = (p.quads + 7) / 8;
+  const long n = (p.rows + 7) / 8 * qtiles;
+  for (long i = (long)group * (THREADS / 64) + wave; i < n; i += (long)p.groups * (THREADS / 64)) {
+    const long row = i / qtiles * 8 + lane / 8;
+    const int q = (int)(i % qtiles) * 8 + (lane & 7);
+    if (row < p.rows && q < p.quads)
+      dst[(row >> 8) * (256l * p.quads) + q * 256l + (row & 255)] = src[row * p.quads + q];
+  }
+}
+
 // Rows of TPR threads, THREADS / TPR rows a workgroup; thread t of a row takes chunks t,
 // t + TPR, ... of it.  A row's codes end with a whole block, so quads stay whole.
 template <class T, int FMT, bool VEC>
 __global__ __launch_bounds__(THREADS) void mx_quantize_kernel(MxQuantArgs p, int tpr) {
   if (p.clear && blockIdx.x == 0 && threadIdx.x < 8)
     __hip_atomic_store(&p.clear[threadIdx.x], 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const unsigned groups = gridDim.x - p.turn.groups;
+  if (blockIdx.x >= groups) return turn_scales(p.turn, blockIdx.x - groups);
   const int t = threadIdx.x & (tpr - 1), rows = THREADS / tpr;
   const long blocks = mx_blocks(p.cols), chunks = 4 * blocks;
   const long code_ld = mx_code_bytes(p.cols, FMT), quads = mx_scale_bytes(p.cols) / 16;
-  for (long row = (long)blockIdx.x * rows + threadIdx.x / tpr; row < p.rows; row += (long)gridDim.x * rows) {
+  for (long row = (long)blockIdx.x * rows + threadIdx.x / tpr; row < p.rows; row += (long)groups * rows) {
     const typename T::mem* x = static_cast<const typename T::mem*>(p.x) + row * p.ldx;
     uint8_t* codes = p.codes + row * code_ld;
     uint8_t* scales = p.scales + row_at(p.layout, row);
@@ -84,21 +101,6 @@ __global__ __launch_bounds__(THREADS) void mx_dequantize_kernel(MxQuantArgs p, i
   }
 }
 
-// 16-byte pieces from [rows][quads] to [rows / 256][quads][256]: 8 lanes read 128 contiguous
-// bytes of a row and 8 write 128 of a quad.
-__global__ __launch_bounds__(THREADS) void mx_turn_scales_kernel(const u32x4_t* __restrict__ src,
-                                                                 u32x4_t* __restrict__ dst, long rows,
-                                                                 int quads, int qtiles) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const long n = (rows + 7) / 8 * qtiles;
-  for (long i = (long)blockIdx.x * (THREADS / 64) + wave; i < n; i += (long)gridDim.x * (THREADS / 64)) {
-    const long row = i / qtiles * 8 + lane / 8;
-    const int q = (int)(i % qtiles) * 8 + (lane & 7);
-    if (row < rows && q < quads)
-      dst[(row >> 8) * (256l * quads) + q * 256l + (row & 255)] = src[row * quads + q];
-  }
-}
-
 // Threads a row (a power of two, at least a quad): one chunk each in a small matrix, four in a
 // large one, whose loads are then in flight together (128256 x 4096: 299 us with one or two,
 // 258 us with four; 1 x 4096 and 64 x 4096 gain nothing from fewer threads).
@@ -120,7 +122,7 @@ unsigned grid_of(const MxQuantArgs& a, int tpr, long most) {
 template <class T, int FMT, bool VEC>
 void quantize(const MxQuantArgs& a, hipStream_t s) {
   const int tpr = threads_per_row(a.rows, a.cols);
-  mx_quantize_kernel<T, FMT, VEC><<<grid_of(a, tpr, 16 * 256), THREADS, 0, s>>>(a, tpr);
+  mx_quantize_kernel<T, FMT, VEC><<<grid_of(a, tpr, 16 * 256) + a.turn.groups, THREADS, 0, s>>>(a, tpr);
 }
 template <class T, int FMT, bool VEC>
 void dequantize(const MxQuantArgs& a, hipStream_t s) {
@@ -140,14 +142,6 @@ void dequantize_any(const MxQuantArgs& a, int dtype, bool vec, hipStream_t s) {
 }
 
 }  // namespace
-
-hipError_t launch_mx_turn_scales(const uint8_t* src, uint8_t* dst, long rows, long cols, hipStream_t s) {
-  const int quads = (int)(mx_scale_bytes(cols) / 16), qtiles = (quads + 7) / 8;
-  const long need = ((rows + 7) / 8 * qtiles + 3) / 4;
-  mx_turn_scales_kernel<<<(unsigned)(need < 4096 ? need : 4096), THREADS, 0, s>>>(
-      reinterpret_cast<const u32x4_t*>(src), reinterpret_cast<u32x4_t*>(dst), rows, quads, qtiles);
-  return hipGetLastError();
-}
 
 hipError_t launch_mx_quantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s) {
   if (fmt == kMxFp4) quantize_any<kMxFp4>(a, dtype, vec, s);

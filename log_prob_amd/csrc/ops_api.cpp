@@ -216,7 +216,7 @@ flce_status_t flce_mx_quantize(const void* x, int x_dtype, int64_t ldx, int64_t 
   if ((st = check_mx_buffers(codes, scales)) != FLCE_OK) return st;
   const flce::MxQuantArgs a{x, long(ldx), nullptr, 0, static_cast<uint8_t*>(codes),
                             static_cast<uint8_t*>(scales), long(rows), long(cols),
-                            flce::mx_row_major(cols), nullptr};
+                            flce::mx_row_major(cols), nullptr, {}};
   const bool vec = cols % 8 == 0 && vectors(x, x_dtype, ldx);
   const hipError_t e = flce::launch_mx_quantize(a, x_dtype, format, vec, stream);
   if (e != hipSuccess) return hip_fail(e, "quantisation kernel launch");
@@ -238,7 +238,7 @@ flce_status_t flce_mx_dequantize(const void* codes, const void* scales, int form
   flce::MxQuantArgs a{nullptr, 0, out, long(ldo),
                       const_cast<uint8_t*>(static_cast<const uint8_t*>(codes)),
                       const_cast<uint8_t*>(static_cast<const uint8_t*>(scales)), long(rows),
-                      long(cols), flce::mx_row_major(cols), nullptr};
+                      long(cols), flce::mx_row_major(cols), nullptr, {}};
   const bool vec = cols % 8 == 0 && vectors(out, out_dtype, ldo);
   const hipError_t e = flce::launch_mx_dequantize(a, out_dtype, format, vec, stream);
   if (e != hipSuccess) return hip_fail(e, "dequantisation kernel launch");

@@ -90,6 +90,20 @@ inline MxScaleLayout mx_row_major(int64_t cols) {
 }
 inline MxScaleLayout mx_tiled(int64_t cols) { return {16, 16 * 256, long(256 * mx_scale_bytes(cols))}; }
 
+// Scales of `rows` rows to be written in the tile kernels' form (whole 256-row tiles) by
+// `groups` workgroups of their own.
+struct MxTurn {
+  const uint8_t* src;      // row-major
+  uint8_t* dst;
+  long rows;
+  int quads;               // 16-byte pieces of a row
+  unsigned groups;         // 0: nothing to do
+};
+inline MxTurn mx_turn(const uint8_t* src, uint8_t* dst, int64_t rows, int64_t cols) {
+  const int64_t quads = mx_scale_bytes(cols) / 16, need = ((rows + 7) / 8 * ((quads + 7) / 8) + 3) / 4;
+  return {src, dst, long(rows), int(quads), unsigned(need < 4096 ? need : 4096)};
+}
+
 struct MxQuantArgs {
   const void* x;           // quantise: the matrix; dequantise: unused
   long ldx;
@@ -101,6 +115,7 @@ struct MxQuantArgs {
   long cols;
   MxScaleLayout layout;
   unsigned long long* clear;  // quantise: 8 counters to zero for a later launch, or nullptr
+  MxTurn turn;             // quantise: another matrix's scales on the way
 };
 hipError_t launch_mx_quantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s);
 hipError_t launch_mx_dequantize(const MxQuantArgs& a, int dtype, int fmt, bool vec, hipStream_t s);
@@ -114,8 +129,6 @@ struct MxOperand {
   const uint8_t* scales;
   MxScaleLayout layout;
 };
-// Scales of `rows` rows from row-major to the tile kernels' form (whole 256-row tiles).
-hipError_t launch_mx_turn_scales(const uint8_t* src, uint8_t* dst, long rows, long cols, hipStream_t s);
 // A decoding step's tokens are quantised by the product's workgroups themselves where their
 // codes (rows padded to 1024 K) take at most kMxOwnBytes.
 constexpr int kMxOwnBytes = 8192;
