@@ -514,11 +514,12 @@ def _rows(t, name, dev, shape=None):
     """Check a matrix whose rows are contiguous; returns its row stride."""
     if t.device != dev:
         raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected a matrix, got {t.dim()} dimensions")
-    m, h = t.shape
-    if shape is not None and shape != (m, h):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {(m, h)}")
+    size = t.shape
+    if len(size) != 2:
+        raise ValueError(f"{name}: expected a matrix, got {len(size)} dimensions")
+    if shape is not None and shape != size:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(size)}")
+    m, h = size
     ld, one = t.stride()
     if one != 1 and h > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
@@ -580,8 +581,9 @@ def _mx_row_bytes(cols, f):
 def _mx_empty(rows, cols, fmt, f, dev):
     import torch
     cb, sb = _mx_row_bytes(cols, f)
-    return MXTensor(torch.empty((rows, cb), dtype=torch.uint8, device=dev),
-                    torch.empty((rows, sb), dtype=torch.uint8, device=dev), fmt, cols)
+    # (sizes as plain arguments: torch takes 0.7 us longer over a tuple)
+    return MXTensor(torch.empty(rows, cb, dtype=torch.uint8, device=dev),
+                    torch.empty(rows, sb, dtype=torch.uint8, device=dev), fmt, cols)
 
 
 def _mx_check(q, name, dev, f, rows, cols):
@@ -626,7 +628,7 @@ def mx_dequantize(q: MXTensor, dtype=None, out=None):
     m = q.codes.shape[0]
     _mx_check(q, "q", dev, f, m, q.cols)
     if out is None:
-        out = torch.empty((m, q.cols), dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+        out = torch.empty(m, q.cols, dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out: expected {dtype}, got {out.dtype}")
     od, ldo = _dtype_id(out, "out"), _rows(out, "out", dev, (m, q.cols))
@@ -669,7 +671,7 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out_dtype=N
         if (out_dtype is None or out_dtype == x.dtype) and ldx == h:
             y, yd = torch.empty_like(x), xd
         else:
-            y = torch.empty((m, h), dtype=x.dtype if out_dtype is None else out_dtype, device=dev)
+            y = torch.empty(m, h, dtype=x.dtype if out_dtype is None else out_dtype, device=dev)
             yd = _dtype_id(y, "y")
         ldy = h
         mean = torch.empty(m, dtype=torch.float32, device=dev)
@@ -736,7 +738,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx_dtype=None, need_para
         param_dtype = torch.float32
     dw = db = None
     if out is None:
-        dx = torch.empty((m, h), dtype=dx_dtype, device=dev)
+        dx = torch.empty(m, h, dtype=dx_dtype, device=dev)
         if need_params:
             dw = torch.empty(h, dtype=param_dtype, device=dev)
             db = torch.empty(h, dtype=param_dtype, device=dev)
@@ -801,7 +803,7 @@ def mxfp4_logits(X, W: MXTensor, scale: float = 1.0, out_dtype=None, workspace=N
     import torch
     dev, m, h, v = _mx_head(X, W)
     if out is None:
-        out = torch.empty((m, v), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
+        out = torch.empty(m, v, dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out: expected {out_dtype}, got {out.dtype}")
     od, ldo = _dtype_id(out, "out"), _rows(out, "out", dev, (m, v))
