@@ -1,13 +1,15 @@
-"""Build libflce.so (HIP, gfx950 only) in-tree with hipcc.
+"""Build libflce.so (HIP, gfx950 only) in-tree with hipcc, and its Python binding _binding.so.
 
-    python -m log_prob_amd.build            # -> log_prob_amd/libflce.so
+    python -m log_prob_amd.build            # -> log_prob_amd/libflce.so, log_prob_amd/_binding.so
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -17,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["flce_kernels.hip", "norm_kernels.hip", "mx_quant_kernels.hip",
            "mx_stream_kernels.hip", "mx_tile_kernels.hip", "flce_api.cpp", "ops_api.cpp"]
 LIB = os.path.join(HERE, "libflce.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -38,9 +41,39 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
+def compile_binding(obj: str, verbose: bool) -> str:
+    """The binding's object file; returns torch's library folder."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or shutil.which("g++") is None:
+        raise RuntimeError("the Python binding needs torch and g++")
+    torch = spec.submodule_search_locations[0]
+    include = [os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"],
+               os.path.join(os.path.dirname(os.path.dirname(hipcc())), "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           "-I", os.path.join(ROOT, "include"), *(f for d in include for f in ("-isystem", d)),
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    return os.path.join(torch, "lib")
+
+
+def link_binding(obj: str, torch_lib: str, verbose: bool) -> None:
+    out_tmp = BINDING + ".tmp"
+    cmd = ["g++", "-shared", obj, "-o", out_tmp, "-L", HERE, "-l:libflce.so", "-Wl,-rpath,$ORIGIN",
+           "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(out_tmp, BINDING)
+
+
 def build(verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
     cc = hipcc()
     with tempfile.TemporaryDirectory() as tmp:
+        binding = os.path.join(tmp, "binding.o")
         def compile_one(src):
             obj = os.path.join(tmp, src + ".o")
             cmd = [cc, *HIPCC_FLAGS, *extra_flags, "-I", os.path.join(ROOT, "include"),
@@ -52,6 +85,7 @@ def build(verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
 
         # one compiler process a source, side by side
         with ThreadPoolExecutor(max_workers=min(len(SOURCES), 4)) as pool:
+            torch_lib = pool.submit(compile_binding, binding, verbose) if out == LIB else None
             objs = list(pool.map(compile_one, SOURCES))
         out_tmp = out + ".tmp"
         cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", out_tmp]
@@ -59,6 +93,8 @@ def build(verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
         os.replace(out_tmp, out)
+        if torch_lib is not None:
+            link_binding(binding, torch_lib.result(), verbose)
     return out
 
 

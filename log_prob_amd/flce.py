@@ -496,6 +496,25 @@ class MXTensor(NamedTuple):
     cols: int
 
 
+_native = None
+
+
+def _fast():
+    """The compiled binding of the calls below (csrc/binding.cpp).  Its functions return None
+    where a call is not plain and valid; what follows here then decides, or raises."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (the binding's libraries)
+        load()
+        try:
+            from . import _binding
+        except ImportError as err:
+            raise ImportError("log_prob_amd/_binding.so is missing or does not fit this torch; "
+                              "run `python -m log_prob_amd.build`") from err
+        _native = _binding
+    return _native
+
+
 _DTYPE_IDS = {}   # torch dtype -> flce_dtype_t
 
 
@@ -606,6 +625,10 @@ def _mx_check(q, name, dev, f, rows, cols):
 def mx_quantize(x, fmt: str, out: Optional[MXTensor] = None) -> MXTensor:
     """x [rows, cols] (bf16 or fp32) in a microscaled format: "mxfp4", "mxfp8" or "mxint8"."""
     f = _mx_format(fmt)
+    if out is None:
+        r = _fast().mx_quantize(x, f)
+        if r is not None:
+            return MXTensor(r[0], r[1], fmt, x.shape[1])
     dev = _on_gpu(x, "x")
     xd, ldx = _dtype_id(x, "x"), _rows(x, "x", dev)
     m, h = x.shape
@@ -622,8 +645,12 @@ def mx_quantize(x, fmt: str, out: Optional[MXTensor] = None) -> MXTensor:
 
 def mx_dequantize(q: MXTensor, dtype=None, out=None):
     """The values of a microscaled matrix, as bf16 (the default) or fp32."""
-    import torch
     f = _mx_format(q.fmt)
+    if out is None:
+        r = _fast().mx_dequantize(q.codes, q.scales, f, q.cols, dtype)
+        if r is not None:
+            return r
+    import torch
     dev = _on_gpu(q.codes, "codes")
     m = q.codes.shape[0]
     _mx_check(q, "q", dev, f, m, q.cols)
@@ -660,12 +687,16 @@ def layer_norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out_dtype=N
     x is bf16 or fp32, y has out_dtype (x's by default; bf16 from fp32 is the usual step from
     an fp32 residual stream into the bf16 head), mean and rstd are fp32 [M].  `out` may supply
     the results' buffers."""
+    f = _MX_NONE if checkpoint is None else _mx_format(checkpoint, ("mxfp8", "mxint8"))
+    if out is None:
+        r = _fast().layer_norm_forward(x, weight, bias, eps, out_dtype, f)
+        if r is not None:
+            return r if checkpoint is None else (*r[:3], MXTensor(r[3], r[4], checkpoint, x.shape[1]))
     import torch
     dev = _on_gpu(x, "x")
     xd, ldx = _dtype_id(x, "x"), _rows(x, "x", dev)
     m, h = x.shape
     pd = _params(weight, bias, dev, h)
-    f = _MX_NONE if checkpoint is None else _mx_format(checkpoint, ("mxfp8", "mxint8"))
     kept = None
     if out is None:
         if (out_dtype is None or out_dtype == x.dtype) and ldx == h:
@@ -711,17 +742,23 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx_dtype=None, need_para
     dx has x's dtype (from a checkpoint: dx_dtype, dy's by default), dweight and dbias have
     weight's (without one: param_dtype, fp32 by default), or are None without need_params.
     `out` may supply the three buffers."""
+    saved = isinstance(x, MXTensor)
+    f = _mx_format(x.fmt, ("mxfp8", "mxint8")) if saved else _MX_NONE
+    if out is None and workspace is None and (not saved or (dy.dim() == 2 and x.cols == dy.shape[1])):
+        r = _fast().layer_norm_backward(
+            dy, None if saved else x, x.codes if saved else None, x.scales if saved else None, f,
+            mean, rstd, weight, dx_dtype, bool(need_params), param_dtype)
+        if r is not None:
+            return r
     import torch
     dev = _on_gpu(dy, "dy")
     dyd, lddy = _dtype_id(dy, "dy"), _rows(dy, "dy", dev)
     m, h = dy.shape
-    if isinstance(x, MXTensor):
-        f = _mx_format(x.fmt, ("mxfp8", "mxint8"))
+    if saved:
         _mx_check(x, "x", dev, f, m, h)
         xp, xd, ldx, codes, scales = None, 0, h, x.codes.data_ptr(), x.scales.data_ptr()
         dx_dtype = dy.dtype if dx_dtype is None else dx_dtype
     else:
-        f = _MX_NONE
         xd, ldx = _dtype_id(x, "x"), _rows(x, "x", dev, (m, h))
         xp, codes, scales = x.data_ptr(), None, None
         if dx_dtype is not None and dx_dtype != x.dtype:
@@ -772,6 +809,11 @@ def mxfp4_workspace_query(M: int, H: int, V: int, compute_entropy: bool = True) 
     return lo.value, fw.value
 
 
+def _plain_head(X, W) -> bool:
+    return (isinstance(W, MXTensor) and W.fmt == "mxfp4" and X.dim() == 2
+            and W.cols == X.shape[1])
+
+
 def _mx_head(X, W):
     """Checks shared by the calls of the 4-bit head; returns (device, M, H, V)."""
     import torch
@@ -800,6 +842,10 @@ def mxfp4_logits(X, W: MXTensor, scale: float = 1.0, out_dtype=None, workspace=N
     """scale * Q(X) W^T [M, V] for a head W in MXFP4, as bf16 (the default) or fp32.
 
     X [M, H] bf16 is rounded to MXFP4 on the way; sums are in fp32."""
+    if out is None and workspace is None and _plain_head(X, W):
+        r = _fast().mxfp4_logits(X, W.codes, W.scales, scale, out_dtype)
+        if r is not None:
+            return r
     import torch
     dev, m, h, v = _mx_head(X, W)
     if out is None:
@@ -819,6 +865,11 @@ def mxfp4_forward(X, W: MXTensor, targets, ignore_index: int = -100, scale: floa
     """forward() with a head in MXFP4: (logprob, lse, entropy-or-None) as fp32 [M] tensors.
 
     X [M, H] bf16 is rounded to MXFP4 on the way.  Not differentiable."""
+    if out is None and workspace is None and _plain_head(X, W):
+        r = _fast().mxfp4_forward(X, W.codes, W.scales, targets, ignore_index, scale,
+                                  bool(compute_entropy))
+        if r is not None:
+            return r
     import torch
     dev, m, h, v = _mx_head(X, W)
     _vector(targets, "targets", dev, torch.int64, m)

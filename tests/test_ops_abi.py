@@ -111,6 +111,19 @@ def test_empty_calls_touch_nothing():
     assert status("flce_mx_dequantize", None, None, 0, 0, 32, None, 0, 32, None) == 0
 
 
+def test_compiled_binding_declines_host_tensors():
+    import torch
+    nat = flce._fast()
+    x, v = torch.zeros(2, 32), torch.zeros(2)
+    u = torch.zeros(2, 16, dtype=torch.uint8)
+    assert nat.layer_norm_forward(x, None, None, 1e-5, None, -1) is None
+    assert nat.layer_norm_backward(x, x, None, None, -1, v, v, None, None, True, None) is None
+    assert nat.mx_quantize(x, 0) is None and nat.mx_dequantize(u, u, 0, 32, None) is None
+    assert nat.mxfp4_logits(x.bfloat16(), u, u, 1.0, None) is None
+    assert nat.mxfp4_forward(x.bfloat16(), u, u, v.long(), -100, 1.0, True) is None
+    assert nat.mx_quantize() is None and nat.mx_quantize(1, 2, 3) is None
+
+
 def test_binding_refuses_host_tensors_and_wrong_types():
     import torch
     x = torch.zeros(2, 32)

@@ -259,6 +259,106 @@ def test_two_streams_side_by_side():
                 assert torch.equal(a, e)
 
 
+def test_plain_calls_and_given_buffers_agree():
+    """The compiled binding of plain calls against the way that takes the results' buffers."""
+    import torch
+    from log_prob_amd import flce
+    nat = flce._fast()
+    gen = torch.Generator(device="cuda").manual_seed(30)
+    u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device="cuda")
+    f32 = lambda *s: torch.empty(*s, device="cuda")
+    same = lambda a, b: all(torch.equal(u, v) and u.dtype == v.dtype for u, v in zip(a, b))
+    for M, H, xd, yd, fmt in ((1, 264, "float32", "bfloat16", None), (7, 1000, "bfloat16", "bfloat16", "mxint8"),
+                              (3, 33, "float32", "float32", "mxfp8"), (0, 64, "bfloat16", "bfloat16", None)):
+        x, w, b = norm_case(max(M, 1), 2 * H, 31, xd)
+        x, w, b = x[:M, :H], w[:H], b[:H]   # rows inside wider rows
+        xd, yd = getattr(torch, xd), getattr(torch, yd)
+        f = -1 if fmt is None else flce.MX_FORMATS[fmt]
+        y, mean, rstd = torch.empty(M, H, dtype=yd, device="cuda"), f32(M), f32(M)
+        kept = flce._mx_empty(M, H, fmt or "mxfp8", flce.MX_FORMATS[fmt or "mxfp8"], x.device)
+        out = (y, mean, rstd) + ((kept,) if fmt else ())
+        flce.layer_norm_forward(x, w, b, EPS, checkpoint=fmt, out=out)
+        got = nat.layer_norm_forward(x, w, b, EPS, yd, f)
+        assert got is not None and same(got, (y, mean, rstd) + ((kept.codes, kept.scales) if fmt else ()))
+        dy = torch.randn(M, H, generator=gen, device="cuda").to(yd)
+        src = kept if fmt else x
+        dx, dw, db = torch.empty(M, H, dtype=xd, device="cuda"), f32(H), f32(H)
+        flce.layer_norm_backward(dy, src, mean, rstd, w, dx_dtype=xd, out=(dx, dw, db))
+        got = nat.layer_norm_backward(dy, None if fmt else x, kept.codes if fmt else None,
+                                      kept.scales if fmt else None, f, mean, rstd, w, xd, True, None)
+        assert got is not None and same(got, (dx, dw, db))
+        got = nat.layer_norm_backward(dy, None if fmt else x, kept.codes if fmt else None,
+                                      kept.scales if fmt else None, f, mean, rstd, w, xd, False, None)
+        assert torch.equal(got[0], dx) and got[1] is None and got[2] is None
+        for name, f in flce.MX_FORMATS.items():
+            q = flce._mx_empty(M, H, name, f, x.device)
+            flce.mx_quantize(x, name, out=q)
+            assert same(nat.mx_quantize(x, f), (q.codes, q.scales))
+            v = torch.empty(M, H, device="cuda")
+            flce.mx_dequantize(q, out=v)
+            assert torch.equal(nat.mx_dequantize(q.codes, q.scales, f, H, torch.float32), v)
+    for M, H, V in ((1, 64, 100), (9, 264, 1300), (300, 72, 1001)):
+        X = torch.randn(M, H, generator=gen, device="cuda").bfloat16()
+        W = flce.mx_quantize(torch.randn(V, H, generator=gen, device="cuda"), "mxfp4")
+        t = torch.randint(0, V, (M,), generator=gen, device="cuda")
+        t[0] = -7
+        z = torch.empty(M, V, dtype=torch.float32, device="cuda")
+        flce.mxfp4_logits(X, W, 0.5, out=z)
+        assert torch.equal(nat.mxfp4_logits(X, W.codes, W.scales, 0.5, torch.float32), z)
+        out = (f32(M), f32(M), f32(M))
+        flce.mxfp4_forward(X, W, t, -7, 0.5, out=out)
+        assert same(nat.mxfp4_forward(X, W.codes, W.scales, t, -7, 0.5, True), out)
+        got = nat.mxfp4_forward(X, W.codes, W.scales, t, -7, 0.5, False)
+        assert same(got[:2], out[:2]) and got[2] is None
+
+
+def test_compiled_binding_declines():
+    """None, and nothing else, for what is not a plain valid call."""
+    import torch
+    from log_prob_amd import flce
+    nat = flce._fast()
+    x, w, b = norm_case(4, 64, 32)
+    y, mean, rstd = flce.layer_norm_forward(x, w, b)
+    q = flce.mx_quantize(x, "mxfp8")
+    W = flce.mx_quantize(x, "mxfp4")
+    X = x.bfloat16()
+    t = torch.zeros(4, dtype=torch.int64, device="cuda")
+    fwd = lambda *a: nat.layer_norm_forward(*a)
+    ok = [x, w, b, EPS, None, -1]
+    assert fwd(*ok) is not None
+    for i, bad in ((0, x.half()), (0, x[0]), (0, x.t()), (0, x.cpu()), (0, x[0].expand(4, 64)), (0, None), (0, 3),
+                   (1, w[:63]), (1, w.cpu()), (1, w.bfloat16()), (1, "w"), (2, b.half()), (2, b[::2]),
+                   (3, "eps"), (3, -1.0), (3, float("nan")), (4, torch.float16), (4, 5), (5, 0), (5, "mxfp8")):
+        a = list(ok)
+        a[i] = bad
+        assert fwd(*a) is None, (i, bad)
+    assert fwd(*ok[:-1]) is None and fwd() is None
+    assert fwd(X, None, None, EPS, torch.float32, -1) is None
+    ok = [y, x, None, None, -1, mean, rstd, w, None, True, None]
+    bwd = nat.layer_norm_backward
+    assert bwd(*ok) is not None
+    for i, bad in ((0, y[:3]), (0, y.cpu()), (1, x[:, :32]), (1, X), (1, None), (4, 1), (5, mean[:3]), (5, None),
+                   (6, rstd.double()), (7, w[:5]), (8, torch.bfloat16), (8, torch.float16), (9, None),
+                   (10, torch.bfloat16)):
+        a = list(ok)
+        a[i] = bad
+        assert bwd(*a) is None, (i, bad)
+    assert bwd(y, None, q.codes[:3], q.scales, 1, mean, rstd, w, None, True, None) is None
+    assert bwd(y, None, q.codes, q.scales[:, :1], 1, mean, rstd, w, None, True, None) is None
+    assert bwd(y, None, q.codes, q.scales, 0, mean, rstd, w, None, True, None) is None
+    assert nat.mx_quantize(x.half(), 1) is None and nat.mx_quantize(x, 9) is None
+    assert nat.mx_dequantize(q.codes, q.scales, 1, 65, None) is None
+    assert nat.mx_dequantize(q.codes, q.scales, 1, 0, None) is None
+    assert nat.mx_dequantize(q.codes, q.scales, 1, 1 << 70, None) is None
+    assert nat.mxfp4_logits(x, W.codes, W.scales, 1.0, None) is None
+    assert nat.mxfp4_logits(X[:, :32], W.codes, W.scales, 1.0, None) is None
+    assert nat.mxfp4_logits(X, W.codes.cpu(), W.scales, 1.0, None) is None
+    assert nat.mxfp4_logits(X, W.codes, W.scales, float("inf"), None) is None
+    assert nat.mxfp4_forward(X, W.codes, W.scales, t.int(), -100, 1.0, True) is None
+    assert nat.mxfp4_forward(X, W.codes, W.scales, t[:3], -100, 1.0, True) is None
+    assert nat.mxfp4_forward(X, W.codes, W.scales, t, 1 << 70, 1.0, True) is None
+
+
 def test_refusals():
     import torch
     from log_prob_amd import flce
