@@ -259,6 +259,48 @@ def test_two_streams_side_by_side():
                 assert torch.equal(a, e)
 
 
+def test_two_host_threads():
+    """Two threads, each on a stream of its own, in calls that let go of the interpreter."""
+    import threading
+    import torch
+    from log_prob_amd import flce
+    jobs = []
+    for seed, M, H, V in ((40, 3, 264, 5000), (41, 200, 520, 3000)):
+        x, w, b = norm_case(M, H, seed, "bfloat16")
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        W = flce.mx_quantize(torch.randn(V, H, generator=gen, device="cuda"), "mxfp4")
+        jobs.append((x, w.bfloat16(), b.bfloat16(), W, torch.randint(0, V, (M,), generator=gen, device="cuda")))
+
+    def work(x, w, b, W, t):
+        y, mean, rstd = flce.layer_norm_forward(x, w, b, EPS)
+        return (y, flce.mxfp4_logits(y, W), *flce.mxfp4_forward(y, W, t),
+                *flce.layer_norm_backward(y, x, mean, rstd, w))
+
+    want = [work(*j) for j in jobs]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def worker(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                runs = [work(*jobs[i]) for _ in range(30)]
+            s.synchronize()
+            got[i] = runs
+        except Exception as err:   # reported by the test's thread
+            errors.append(err)
+
+    threads = [threading.Thread(target=worker, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors
+    for runs, ref_ in zip(got, want):
+        for run in runs:
+            assert all(torch.equal(a, r) for a, r in zip(run, ref_))
+
+
 def test_plain_calls_and_given_buffers_agree():
     """The compiled binding of plain calls against the way that takes the results' buffers."""
     import torch
