@@ -445,7 +445,9 @@ flce_status_t flce_layer_norm_backward(const void* dy, int dy_dtype, int64_t ldd
  * with exact products and fp32 accumulation, in an order that depends on the shape of the
  * call (never on the workspace).  Shapes as in flce_workspace_query; X and both parts of W
  * 16-byte aligned; a vocabulary shard is a slice of W's rows.  A row of X that holds an
- * infinity or a NaN gives NaNs in its own outputs.
+ * infinity or a NaN gives NaNs in its own outputs, a block of W that stands for NaNs gives
+ * them in its column of the logits and in every row's logprob, lse and entropy (logprob and
+ * entropy of an ignored row stay 0).
  *
  * flce_mx_logits writes z to out [M, V] (bf16 or fp32, any row stride >= V, naturally
  * aligned).  flce_mx_forward writes logprob, lse and entropy of targets, which never leave

@@ -384,7 +384,8 @@ void with_tokens(int M, int V, bool own, int rows, F f) {
 // Merge: per token, the target logit as a dot product of codes, then m* = max m_j,
 // S = sum s_j e^(m_j - m*), U = sum e^(m_j - m*) (u_j + (m_j - m*) s_j) over the vocabulary
 // tiles j; lse = m* + log S, logprob = min(z_t - lse, 0), entropy = max(log S - U / S, 0) (the
-// bounds hold exactly: fp32 rounding can put a value next to one a few ulps past it).
+// bounds hold exactly: fp32 rounding can put a value next to one a few ulps past it; a NaN in
+// the row's sums or its target logit passes them).
 // ROWS tokens a workgroup: 16 where the tokens of a vocabulary tile are contiguous (64-byte
 // pieces, and a token's tiles over 32 threads), or 4 where that would leave most of the chip
 // idle; one where a token's tiles are contiguous.
@@ -492,8 +493,8 @@ __global__ __launch_bounds__(MERGE_THREADS) void mx_merge_kernel(MxFwdArgs p) {
     for (int k = 1; k < WAVES; ++k) z += zt[k];
   }
   p.lse[row] = top + logS;
-  p.logprob[row] = valid ? fminf(z - (top + logS), 0.f) : 0.f;
-  if constexpr (ENT) p.entropy[row] = valid ? fmaxf(logS - sm[1][0][lr] / sm[0][0][lr], 0.f) : 0.f;
+  p.logprob[row] = valid ? at_most_zero(z - (top + logS)) : 0.f;
+  if constexpr (ENT) p.entropy[row] = valid ? at_least_zero(logS - sm[1][0][lr] / sm[0][0][lr]) : 0.f;
 }
 
 }  // namespace

@@ -435,6 +435,11 @@ __device__ __forceinline__ float halves_reduce(float x, float y, Op op) {
   return op(x, y);
 }
 
+// A value bounded by 0 from above or from below.  By comparison, so that a NaN stays one:
+// fminf and fmaxf hand back the operand that is a number.
+__device__ __forceinline__ float at_most_zero(float v) { return v > 0.f ? 0.f : v; }
+__device__ __forceinline__ float at_least_zero(float v) { return v < 0.f ? 0.f : v; }
+
 // max(m, sgn a, sgn b) with sgn = -1 under NEG, as one v_max3_f32 issued directly:
 // fmaxf on values the compiler cannot prove to be quiet NaNs (here, MFMA results)
 // costs one quieting v_max per input.  m is already a running maximum of sgn-scaled
