@@ -595,9 +595,9 @@ __global__ __launch_bounds__(MERGE_ROWS * MERGE_SLICES) void fwd_merge_kernel(Fw
   // rounding can put them a few ulps past it: the target logit (its own dot product)
   // and lse (from the MFMA accumulators) round differently, and the shifted sum of the
   // row's maximum element can come out a hair above 0.  The bounds are applied
-  // exactly, which only moves a value towards the true one.
-  p.logprob[row] = valid ? fminf(zt - (ms + logS), 0.f) : 0.f;
-  if constexpr (ENT) p.entropy[row] = valid ? fmaxf(logS - U / S, 0.f) : 0.f;
+  // exactly, which only moves a value towards the true one; a NaN passes them.
+  p.logprob[row] = valid ? at_most_zero(zt - (ms + logS)) : 0.f;
+  if constexpr (ENT) p.entropy[row] = valid ? at_least_zero(logS - U / S) : 0.f;
 }
 
 // ---------------------------------------------------------------------------

@@ -87,3 +87,58 @@ def test_fp4_weights(M, H, V, scale):
         want = z.clone()
         want[:, word] = float("nan")
         assert same(flce.mxfp4_logits(X, W2, scale), want)
+
+
+def bf16_case(M, H, V):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(11 * M + V)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    X, W = n(M, H).bfloat16(), (n(V, H) / H ** 0.5).bfloat16()
+    t = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    t[torch.rand(M, generator=gen, device="cuda") < 0.2] = IGNORE
+    t[M // 2] = V - 1
+    return X, W, t
+
+
+def shards(X, W, t, ent):
+    """The forward in two vocabulary shards, merged."""
+    import torch
+    from log_prob_amd import flce
+    (M, H), V = X.shape, W.shape[0]
+    cut = max(1, V // 3)
+    parts = [flce.forward_partials_shard(X, W[a:b], t, a, IGNORE, compute_entropy=ent)
+             for a, b in ((0, cut), (cut, V))]
+    stride = max(p.numel() for p in parts)
+    stride = -(-stride // 256) * 256
+    gathered = torch.zeros(2 * stride, dtype=torch.uint8, device="cuda")
+    for r, p in enumerate(parts):
+        gathered[r * stride:r * stride + p.numel()] = p
+    return flce.forward_merge_shards(t, [0, cut, V], gathered, stride, IGNORE, ent)
+
+
+@pytest.mark.parametrize("ent", [True, False])
+@pytest.mark.parametrize("M,H,V", [(1, 136, 700), (300, 264, 1300), (600, 72, 5001)])
+def test_bf16_head(M, H, V, ent):
+    """The bf16 head likewise, through one call, the static scratch and vocabulary shards; what
+    hangs on the log-probs sees the NaN."""
+    import torch
+    from log_prob_amd import flce
+    X, W, t = bf16_case(M, H, V)
+    rows = torch.arange(M, device="cuda")
+    bad = (rows == M // 2) | (rows % 97 == 5) | ((t == IGNORE) & (rows % 3 == 0))
+    every = torch.ones_like(bad)
+    for f in (lambda x, w: flce.forward(x, w, t, IGNORE, compute_entropy=ent),
+              lambda x, w: flce.forward_noalloc(x, w, t, IGNORE, compute_entropy=ent),
+              lambda x, w: shards(x, w, t, ent)):
+        clean = f(X, W)
+        assert not any(torch.isnan(v).any() for v in clean if v is not None)
+        for value in (float("nan"), float("inf"), -float("inf")):
+            X2 = X.clone()
+            X2[bad, H // 3] = value
+            got = f(X2, W)
+            check_rows(clean, got, bad, t)
+        assert torch.isnan(flce.nll_reduce(got[0], t, V, IGNORE)[[0, 2]]).all()
+        for word in (0, V - 1):
+            W2 = W.clone()
+            W2[word, 5] = float("nan")
+            check_rows(clean, f(X, W2), every, t)
