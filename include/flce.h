@@ -330,6 +330,7 @@ flce_status_t flce_nll_mean_grad(const int64_t* targets, int64_t M, int64_t V,
  *   c = min(max(r, 1 - eps_low), 1 + eps_high)
  *   per_token_loss[m] = -min(r A[m], c A[m])      (0 on invalid rows, as fp32)
  *   is_clipped[m]     = c A[m] < r A[m]           (optional output, NULL to skip)
+ * where a NaN among a valid row's inputs makes its loss (and its gradient below) NaN,
  * and four fp64 values to the device array out: the sum of the per-token loss over
  * valid rows, the number of valid rows, the number of clipped rows, and the loss
  * sum / N with N = denominator if > 0 (the caller's normaliser, e.g. the number of

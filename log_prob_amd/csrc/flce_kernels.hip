@@ -1062,7 +1062,9 @@ __device__ __forceinline__ PolicyTerm policy_term(const PolicyLossArgs& p, long 
   const double old = p.old_logprob ? (double)p.old_logprob[i] : lp;
   const double a = (double)p.advantages[i];
   const double r = exp(lp - old);
-  const double c = fmin(fmax(r, 1.0 - p.eps_low), 1.0 + p.eps_high);
+  // by comparisons, here and for the minimum: fmin and fmax would drop a NaN
+  const double lo = 1.0 - p.eps_low, hi = 1.0 + p.eps_high;
+  const double c = r < lo ? lo : r > hi ? hi : r;
   o.u = r * a;
   o.cl = c * a;
   return o;
@@ -1084,7 +1086,7 @@ __global__ __launch_bounds__(PL_THREADS) void policy_loss_reduce_kernel(
   for (long i = t; i < p.M; i += PL_THREADS) {
     const PolicyTerm o = policy_term(p, i);
     const bool clipped = o.valid && o.cl < o.u;
-    const double loss = o.valid ? -fmin(o.u, o.cl) : 0.0;
+    const double loss = o.valid ? -(o.cl < o.u ? o.cl : o.u) : 0.0;
     per_token_loss[i] = (float)loss;
     if (is_clipped) is_clipped[i] = clipped ? 1 : 0;
     s += loss;

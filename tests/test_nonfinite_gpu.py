@@ -142,3 +142,33 @@ def test_bf16_head(M, H, V, ent):
             W2 = W.clone()
             W2[word, 5] = float("nan")
             check_rows(clean, f(X, W2), every, t)
+
+
+@pytest.mark.parametrize("on_policy", [False, True])
+def test_policy_loss(on_policy):
+    """A log-prob, old log-prob or advantage without a number reaches the token's loss, the sum
+    and the token's gradient, clipped or not; ignored tokens and the other ones are as before."""
+    import torch
+    from log_prob_amd import flce
+    M, V = 40, 100
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    lp = -3 * torch.rand(M, generator=gen, device="cuda")
+    old = None if on_policy else lp + torch.randn(M, generator=gen, device="cuda")
+    adv = torch.randn(M, generator=gen, device="cuda")
+    t = torch.randint(0, V, (M,), generator=gen, device="cuda")
+    t[7] = IGNORE
+    ignored = t == IGNORE
+    clean, clips, sums = flce.policy_loss_reduce(lp, old, adv, t, V, IGNORE)
+    grad = flce.policy_loss_grad(lp, old, adv, t, V, sums, IGNORE)
+    assert torch.isfinite(clean).all() and torch.isfinite(sums).all()
+    for k in range(2 if on_policy else 3):
+        args = [lp.clone(), adv.clone(), None if on_policy else old.clone()]
+        bad = torch.arange(M, device="cuda") % 9 == 7   # the ignored token among them
+        args[k][bad] = float("nan")
+        loss, clip, out = flce.policy_loss_reduce(args[0], args[2], args[1], t, V, IGNORE)
+        got = flce.policy_loss_grad(args[0], args[2], args[1], t, V, out, IGNORE)
+        want, want_grad, want_clip = clean.clone(), grad.clone(), clips.clone()
+        want[bad & ~ignored] = want_grad[bad & ~ignored] = float("nan")
+        want_clip[bad] = 0
+        assert same(loss, want) and same(got, want_grad) and torch.equal(clip, want_clip)
+        assert torch.isnan(out[[0, 3]]).all() and out[1] == sums[1] and out[2] == want_clip.sum()
