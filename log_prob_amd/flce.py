@@ -565,6 +565,17 @@ def _vector(t, name, dev, dtype, n):
     raise ValueError(f"{name}: expected {n} contiguous elements, got shape {tuple(t.shape)}")
 
 
+def _workspace(workspace, nbytes, dev):
+    if workspace is None:
+        return alloc_workspace(nbytes, dev)
+    if workspace.device != dev:
+        raise ValueError(f"workspace: expected a tensor on {dev}, got {workspace.device}")
+    # its size is counted in elements: a view that repeats or skips some has other bytes
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return workspace
+
+
 def _launch(dev, fn, *args):
     """Call fn(*args, stream) with dev's current stream, on dev."""
     import torch
@@ -790,10 +801,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx_dtype=None, need_para
     pd = _DTYPE_IDS.get(param_dtype)
     if pd is None:
         raise TypeError(f"param_dtype: expected bfloat16 or float32, got {param_dtype}")
-    if workspace is None:
-        workspace = alloc_workspace(layer_norm_backward_workspace(m, h), dev)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace: expected a tensor on {dev}, got {workspace.device}")
+    workspace = _workspace(
+        workspace, layer_norm_backward_workspace(m, h) if workspace is None else 0, dev)
     _launch(dev, load().flce_layer_norm_backward, dy.data_ptr(), dyd, lddy, xp, xd, ldx, f, codes,
             scales, _ptr(weight), pd, mean.data_ptr(), rstd.data_ptr(), m, h, dx.data_ptr(), dxd,
             lddx, _ptr(dw), _ptr(db), workspace.data_ptr(), workspace.numel() * workspace.element_size())
@@ -828,14 +837,6 @@ def _mx_head(X, W):
     v = W.codes.shape[0]
     _mx_check(W, "W", dev, 0, v, h)
     return dev, m, h, v
-
-
-def _workspace(workspace, nbytes, dev):
-    if workspace is None:
-        return alloc_workspace(nbytes, dev)
-    if workspace.device != dev:
-        raise ValueError(f"workspace: expected a tensor on {dev}, got {workspace.device}")
-    return workspace
 
 
 def mxfp4_logits(X, W: MXTensor, scale: float = 1.0, out_dtype=None, workspace=None, out=None):
