@@ -496,22 +496,34 @@ class MXTensor(NamedTuple):
     cols: int
 
 
+class _Unbound:
+    """Stands in for the compiled binding where it was not built: every call goes the long way."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 _native = None
 
 
 def _fast():
     """The compiled binding of the calls below (csrc/binding.cpp).  Its functions return None
-    where a call is not plain and valid; what follows here then decides, or raises."""
+    where a call is not plain and valid; what follows here then decides, or raises.  Without it
+    every call takes that way, through ctypes into the same library, a few microseconds longer."""
     global _native
     if _native is None:
         import torch  # noqa: F401  (the binding's libraries)
         load()
         try:
             from . import _binding
+            _native = _binding
         except ImportError as err:
-            raise ImportError("log_prob_amd/_binding.so is missing or does not fit this torch; "
-                              "run `python -m log_prob_amd.build`") from err
-        _native = _binding
+            if os.path.exists(os.path.join(HERE, "_binding.so")):
+                import warnings
+                warnings.warn(f"log_prob_amd/_binding.so does not load ({err}): calls go through "
+                              "ctypes; `python -m log_prob_amd.build` makes one for this torch",
+                              RuntimeWarning, stacklevel=3)
+            _native = _Unbound()
     return _native
 
 
