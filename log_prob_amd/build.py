@@ -41,12 +41,19 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found")
 
 
+def binding_needs() -> str:
+    """What the Python binding's build lacks here; empty if it can be built."""
+    torch = importlib.util.find_spec("torch")
+    have = {"torch for ROCm": torch is not None and os.path.exists(os.path.join(
+                torch.submodule_search_locations[0], "include", "c10", "hip", "HIPStream.h")),
+            "g++": shutil.which("g++"),
+            "Python.h": os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))}
+    return " and ".join(name for name, there in have.items() if not there)
+
+
 def compile_binding(obj: str, verbose: bool) -> str:
     """The binding's object file; returns torch's library folder."""
-    spec = importlib.util.find_spec("torch")
-    if spec is None or shutil.which("g++") is None:
-        raise RuntimeError("the Python binding needs torch and g++")
-    torch = spec.submodule_search_locations[0]
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     include = [os.path.join(torch, "include"),
                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"],
@@ -60,18 +67,25 @@ def compile_binding(obj: str, verbose: bool) -> str:
     return os.path.join(torch, "lib")
 
 
-def link_binding(obj: str, torch_lib: str, verbose: bool) -> None:
-    out_tmp = BINDING + ".tmp"
-    cmd = ["g++", "-shared", obj, "-o", out_tmp, "-L", HERE, "-l:libflce.so", "-Wl,-rpath,$ORIGIN",
+def link_binding(obj: str, torch_lib: str, lib_dir: str, out: str, verbose: bool) -> None:
+    """Link against the libflce.so in lib_dir; at run time the one beside the binding is found."""
+    cmd = ["g++", "-shared", obj, "-o", out, "-L", lib_dir, "-l:libflce.so", "-Wl,-rpath,$ORIGIN",
            "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10_hip", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(out_tmp, BINDING)
 
 
 def build(verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
+    """Build the library at `out`.  For the package's own one the compiled binding is built with
+    it, or left out where torch or g++ is missing: its calls then go through ctypes.  Nothing is
+    replaced before everything has been built."""
     cc = hipcc()
+    bind = out == LIB
+    if bind and binding_needs():
+        print(f"without {binding_needs()} the Python binding is left out (calls go through ctypes)",
+              flush=True)
+    with_binding = bind and not binding_needs()
     with tempfile.TemporaryDirectory() as tmp:
         binding = os.path.join(tmp, "binding.o")
         def compile_one(src):
@@ -85,16 +99,21 @@ def build(verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
 
         # one compiler process a source, side by side
         with ThreadPoolExecutor(max_workers=min(len(SOURCES), 4)) as pool:
-            torch_lib = pool.submit(compile_binding, binding, verbose) if out == LIB else None
+            torch_lib = pool.submit(compile_binding, binding, verbose) if with_binding else None
             objs = list(pool.map(compile_one, SOURCES))
-        out_tmp = out + ".tmp"
-        cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", out_tmp]
+        lib = os.path.join(tmp, "libflce.so")
+        cmd = [cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", lib]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-        os.replace(out_tmp, out)
-        if torch_lib is not None:
-            link_binding(binding, torch_lib.result(), verbose)
+        if with_binding:
+            link_binding(binding, torch_lib.result(), tmp, BINDING + ".tmp", verbose)
+        shutil.copy(lib, out + ".tmp")
+    os.replace(out + ".tmp", out)
+    if with_binding:
+        os.replace(BINDING + ".tmp", BINDING)
+    elif bind and os.path.exists(BINDING):
+        os.remove(BINDING)   # it was built with another library
     return out
 
 
