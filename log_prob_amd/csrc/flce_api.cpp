@@ -42,9 +42,7 @@ using flce::fail;
 using flce::ok;
 
 constexpr int64_t kTile = flce::kTile;
-constexpr int64_t kMaxM = int64_t(1) << 30;
-constexpr int64_t kMaxV = int64_t(1) << 30;
-constexpr int64_t kMaxH = int64_t(1) << 20;
+constexpr int64_t kMaxM = flce::kMaxRows, kMaxV = flce::kMaxVocab, kMaxH = flce::kMaxHidden;
 // A dispatch covers at most 2^32 - 1 work-items per dimension: the tile kernels run
 // 256 threads per workgroup, the target-logit kernel 64 per row, the merge 16 per row.
 constexpr int64_t kMaxWorkgroups = flce::kMaxWorkgroups;
@@ -757,8 +755,9 @@ size_t mx_scales_bytes(int64_t rows, int64_t H, bool tiled) {
 // smaller tiles that a unit runs two at a time, or 64-token ones where all are resident at once
 // (us, against large tiles: logits of 400 tokens, H=4096, V=4000 16 against 30; of 257, H=1600,
 // V=50257 35 against 44; of 400, H=2048, V=151936 146 against 104).  Over 724 timings (129 to
-// 16384 tokens, H 512 to 8192, V 300 to 128256) the choice costs 0.4% of the better kernel's
-// time on average, large tiles throughout 22%; past the sizes timed it takes the large tiles.
+// 16384 tokens, H 512 to 8192, V 300 to 128256; profiles/mx_head_choice.md) the choice costs 0.3%
+// of the better kernel's time on average and 21% at worst, large tiles throughout 22% and small
+// ones 6%; past the sizes timed it takes the large tiles.
 bool mx_streams(int64_t M, int64_t H, int64_t V) {
   if (M <= flce::kMxStreamTokens) return true;
   const int64_t steps = cdiv(H, 256), large = cdiv(M, 256) * cdiv(V, 256);

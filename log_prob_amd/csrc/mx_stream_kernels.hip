@@ -6,9 +6,13 @@
 // They come through a ring of LDS stages by direct-to-LDS loads, 128 contiguous bytes of a row
 // for 8 lanes, ahead of the products (loaded straight into the matrix instruction's registers,
 // 16 bytes a lane from 32 rows at once, one token over 151936 x 2048 took 60 us).  Two
-// workgroups of four waves share a compute unit, so a stage has 32 KiB at most (one workgroup
-// and three stages for 128 tokens: 65 us over 151936 x 2048 instead of 48).  More tokens run in
-// tiles of up to 128, bound by the loads to LDS and the reads from it.
+// workgroups of four waves share a compute unit where each takes 128 vocabulary rows, so a stage
+// has 32 KiB at most (one workgroup and three stages for 128 tokens: 65 us over 151936 x 2048
+// instead of 48); with fewer rows and more than 8 tokens the stages fill half of the LDS and
+// more, and one runs (StreamCfg<2, 2, 32>, <1, 4, 32> and <2, 2, 64>: 84, 104 and 100 KiB).
+// More tokens run in tiles of up to 128.  A round of 510 such tiles (288 x 21760, 128 x 96, two
+// a unit) takes 6.3 us and 0.9 to 1.05 us for each 256 K, in which a unit loads 57 KB to LDS, 24
+// bytes a clock, and its matrix pipe works for a third of the cycles: neither is at its limit.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -46,7 +50,7 @@ struct StreamCfg {
   static constexpr int LDS = OWN_AT + (OWN ? kMxOwnBytes + kMxOwnBytes / 8 : 0);
   static constexpr int MB = 1, NB = TB;  // as lane_col_max and lane_col_sums name them
   static_assert(RW * KW == 4 && W_BYTES == 16384, "four waves");
-  static_assert(LDS <= 160 * 1024, "LDS");
+  static_assert(LDS <= (KW == 1 ? 80 : 160) * 1024, "LDS; two a compute unit with 128 rows each");
 };
 
 // Order of a step's products: one product a time, each but the last block's with a read of the
@@ -357,7 +361,8 @@ __global__ __launch_bounds__(256) void mx_stream_fwd_kernel(MxFwdArgs p) {
 
 // The configuration for M tokens of a call that takes `rows` vocabulary rows a workgroup
 // (mx_stream_rows); own: X has not been quantised.  Tiles of 64 tokens, three stages deep, where
-// all are resident at once; else of 96 or 128, of two stages, which load less for each product
+// all are resident at once or the workgroup takes 64 vocabulary rows; else of 96 or 128, of two
+// stages, which load less for each product
 // (300 x 4096 x 4000 logits: 15 against 19 us; 600 x 1600 x 50257: 72 against 59 us).
 template <int XR, class F>
 void with_cfg(int rows, F f) {
@@ -501,7 +506,11 @@ __global__ __launch_bounds__(MERGE_THREADS) void mx_merge_kernel(MxFwdArgs p) {
 
 // Fewer vocabulary rows a workgroup, with the waves sharing K instead, where 128 (and 64
 // tokens) would leave less than one and a half workgroups a compute unit, as far as the staged
-// tokens fit.  Of the whole call, for the order of summation.
+// tokens fit.  Of the whole call, for the order of summation.  Logits in us by this rule and with
+// 128 rows throughout: 1 x 4096 x 8000 6.2 and 8.9, 32 x 4096 x 8000 10.2 and 12.1, 128 x 4096 x
+// 8000 11.0 and 13.5; past a vocabulary of about 16000, where one workgroup a unit runs at a
+// time, 128 rows are the faster ones: 32 x 4096 x 24000 18.3 and 13.3, 64 x 4096 x 40000 28.7 and
+// 26.3, 32 x 2048 x 24000 15.0 and 10.4.
 int mx_stream_rows(long M, int V) {
   const int64_t n_mt = (M + 63) / 64;
   if ((V + 127) / 128 * n_mt >= 384) return 128;

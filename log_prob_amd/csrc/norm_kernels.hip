@@ -9,8 +9,11 @@
 // registers that also sums the centred values themselves: their mean is what the first pass
 // got wrong, and correcting both statistics by it makes an offset much larger than the
 // spread cost no digits (a constant row is centred to exact zeros).  Both directions are
-// bound by memory: every element is read once and written once.  A row lives in the
-// registers of one wave (H <= 2048) or one workgroup, 8 consecutive elements a chunk.
+// bound by memory: every element is read once and written once.  A row lives in registers, 8
+// consecutive elements a chunk: those of one wave or less up to H = 512 in the forward and 1024
+// in the backward, of one workgroup up to 16384 and 8192.  Longer rows are read again from
+// memory for every pass (three in the forward; in the backward one for the column sums and two
+// for dx).
 // The forward can write a microscaled 8-bit copy of x on the way (the quad of lanes that
 // holds a block of 32 finds its scale), and the backward can read that copy in place of x.
 //

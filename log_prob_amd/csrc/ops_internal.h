@@ -111,7 +111,7 @@ hipError_t launch_mx_dequantize(const MxQuantArgs& a, int dtype, int fmt, bool v
 
 // The head with 4-bit weights: X and W as MXFP4 codes and scales.  Calls of at most
 // kMxStreamTokens tokens always run the kernels that stream W past the tokens, of which
-// kMxStreamResident workgroups run at once.
+// kMxStreamResident workgroups run at once (those of 128 vocabulary rows).
 constexpr int64_t kMxStreamTokens = 128, kMxStreamResident = 512;
 struct MxOperand {
   const uint8_t* codes;
