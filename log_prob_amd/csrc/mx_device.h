@@ -194,6 +194,12 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
   return __uint_as_float(byte == 0u ? 0x00400000u : byte == 255u ? 0x7fc00000u : byte << 23);
 }
 
+// d 2^(a - 127) 2^(b - 127), rounded once: neither scale on its own takes d past fp32's range.
+__device__ __forceinline__ float mx_scale_product(float d, uint32_t a, uint32_t b) {
+  const float v = __builtin_amdgcn_ldexpf(d, (int)(a + b) - 254);
+  return a == 255u || b == 255u ? __uint_as_float(0x7fc00000u) : v;
+}
+
 // Codes of 8 elements over a scale: 4 bytes (fp4, even element in a byte's low half) or 8.
 template <int FMT>
 __device__ __forceinline__ u32x2_t mx_encode(const float (&v)[8], uint32_t byte) {

@@ -403,11 +403,12 @@ __global__ __launch_bounds__(MERGE_THREADS) void mx_merge_kernel(MxFwdArgs p) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const long row0 = (long)blockIdx.x * ROWS;
   const long code_ld = mx_code_bytes(p.H, kMxFp4);
-  auto scale = [](const MxOperand& o, long r, int b) {
-    return mx_scale(o.scales[mx_scale_row(o.layout, r) + (b >> 4) * o.layout.quad_stride + (b & 15)]);
+  auto scale = [](const MxOperand& o, long r, int b) -> uint32_t {
+    return o.scales[mx_scale_row(o.layout, r) + (b >> 4) * o.layout.quad_stride + (b & 15)];
   };
   // target logits: a wave a token (one token: its blocks over all waves); a block's sum of
-  // code products is exact, its two scales multiply it once
+  // code products is exact, its two scales multiply it as one (with X's largest blocks against
+  // W's smallest, one after the other passed fp32's range on the way)
   for (int i = ROWS == 1 ? 0 : wave; i < ROWS; i += WAVES) {
     const long row = row0 + i;
     const int64_t t = row < p.M ? p.targets[row] : -1;
@@ -425,7 +426,7 @@ __global__ __launch_bounds__(MERGE_THREADS) void mx_merge_kernel(MxFwdArgs p) {
         float d = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) d = fmaf(xv[j], wv[j], d);
-        s = fmaf(d * mx_scale(byte), scale(p.w, t, c >> 2), s);
+        s += mx_scale_product(d, byte, scale(p.w, t, c >> 2));
       }
     } else if (valid) {
       for (int b = ROWS == 1 ? (int)threadIdx.x : lane; b < (int)mx_blocks(p.H);
@@ -441,7 +442,7 @@ __global__ __launch_bounds__(MERGE_THREADS) void mx_merge_kernel(MxFwdArgs p) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) d = fmaf(xv[j], wv[j], d);
         }
-        s = fmaf(d * scale(p.x, row, b), scale(p.w, t, b), s);
+        s += mx_scale_product(d, scale(p.x, row, b), scale(p.w, t, b));
       }
     }
 #pragma unroll
