@@ -448,7 +448,8 @@ flce_status_t flce_layer_norm_backward(const void* dy, int dy_dtype, int64_t ldd
  * 16-byte aligned; a vocabulary shard is a slice of W's rows.  A row of X that holds an
  * infinity or a NaN gives NaNs in its own outputs, a block of W that stands for NaNs gives
  * them in its column of the logits and in every row's logprob, lse and entropy (logprob and
- * entropy of an ignored row stay 0).
+ * entropy of an ignored row stay 0).  Errors of logprob, lse and entropy are relative to the
+ * row's largest |z|; past |z| = 2^30 a row may come out as NaN, here and in flce_forward.
  *
  * flce_mx_logits writes z to out [M, V] (bf16 or fp32, any row stride >= V, naturally
  * aligned).  flce_mx_forward writes logprob, lse and entropy of targets, which never leave

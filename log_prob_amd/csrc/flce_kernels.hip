@@ -580,7 +580,7 @@ __global__ __launch_bounds__(MERGE_ROWS * MERGE_SLICES) void fwd_merge_kernel(Fw
     S += sm[1][k][lr];
     if constexpr (ENT) U += sm[2][k][lr];
   }
-  const float logS = logf(S);
+  const float logS = log_sum(S);
   const int64_t t = p.targets[row];
   const bool valid = t != p.ignore_index && t >= 0 && t < p.sh.v_lo[p.sh.n];
   float zt = 0.f;

@@ -490,7 +490,7 @@ __global__ __launch_bounds__(MERGE_THREADS) void mx_merge_kernel(MxFwdArgs p) {
     __syncthreads();
   }
   if (sl != 0 || !live) return;
-  const float logS = logf(sm[0][0][lr]);
+  const float logS = log_sum(sm[0][0][lr]);
   const int64_t t = p.targets[row];
   const bool valid = t != p.ignore_index && t >= 0 && t < p.V;
   float z = zt[lr];

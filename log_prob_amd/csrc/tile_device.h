@@ -440,6 +440,14 @@ __device__ __forceinline__ float halves_reduce(float x, float y, Op op) {
 __device__ __forceinline__ float at_most_zero(float v) { return v > 0.f ? 0.f : v; }
 __device__ __forceinline__ float at_least_zero(float v) { return v < 0.f ? 0.f : v; }
 
+// log of a row's sum of shifted exponentials.  The largest term is 2^r, r being what rounding
+// took from the shift (half a step of the largest logit in log2 units): 64 at logits of 2^30.  Of
+// logits twice as large and more the sum can come out 0 or infinite, which says nothing about
+// the row: NaN.
+__device__ __forceinline__ float log_sum(float s) {
+  return s > 0.f && s < INFINITY ? logf(s) : __uint_as_float(0x7fc00000u);
+}
+
 // max(m, sgn a, sgn b) with sgn = -1 under NEG, as one v_max3_f32 issued directly:
 // fmaxf on values the compiler cannot prove to be quiet NaNs (here, MFMA results)
 // costs one quieting v_max per input.  m is already a running maximum of sgn-scaled
