@@ -89,7 +89,7 @@ def blas_reference(case, steps):
 
 PROFILE = os.path.join(ROOT, "profiles", "fwd_bwd_M8192_H8192_V131072.md")
 KERNEL_SOURCES = ("log_prob_amd/csrc/flce_kernels.hip", "log_prob_amd/csrc/tile_device.h",
-                  "log_prob_amd/csrc/flce_internal.h")
+                  "log_prob_amd/csrc/mainloop_device.h", "log_prob_amd/csrc/flce_internal.h")
 
 
 def kernel_source_hash():
