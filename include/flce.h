@@ -471,6 +471,119 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
                               float* logprob, float* lse, float* entropy, void* workspace,
                               size_t workspace_bytes, struct ihipStream_t* stream);
 
+/*
+ * Matrix product with bias, activation and residual in its epilogue: the dense block in front of
+ * a head, or a head's logits.
+ *   pre = X W^T + bias,  out = act(pre) + residual       (NULL bias, residual: none)
+ * X [M, K] and W [N, K] bf16, products exact, sums in fp32; bias [N], residual and out [M, N]
+ * bf16 or fp32, pre bf16 (NULL: not written).  Activations: none, relu, gelu (x Phi(x)),
+ * gelu_tanh (x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2), silu (x / (1 + e^-x)).
+ * 0 <= M <= 2^30 (0: nothing is touched), 1 <= N <= 2^20, K a multiple of 8 up to 2^20.  Rows of
+ * X and W are 16-byte aligned, with row strides (elements) up to 2^21; the other matrices are
+ * naturally aligned with any row strides >= N (rows of multiples of 8 elements at 16-byte aligned
+ * addresses move fastest).  out may be residual where their types and strides agree.  workspace:
+ * 256-byte aligned, at least the forward bytes of flce_linear_workspace (0: may be NULL).  Results
+ * are bitwise repeatable; the order of summation depends on the shape.
+ */
+typedef enum {
+  FLCE_ACT_NONE = 0,
+  FLCE_ACT_RELU = 1,
+  FLCE_ACT_GELU = 2,
+  FLCE_ACT_GELU_TANH = 3,
+  FLCE_ACT_SILU = 4
+} flce_activation_t;
+
+/* Workspace bytes of flce_linear_forward and flce_linear_backward (either output may be NULL). */
+flce_status_t flce_linear_workspace(int64_t M, int64_t N, int64_t K, size_t* fwd_bytes,
+                                    size_t* bwd_bytes);
+flce_status_t flce_linear_forward(const void* X, int64_t ldx, const void* W, int64_t ldw,
+                                  const void* bias, int bias_dtype, int activation,
+                                  const void* residual, int residual_dtype, int64_t ldr, int64_t M,
+                                  int64_t N, int64_t K, void* out, int out_dtype, int64_t ldo,
+                                  void* pre, int64_t ldp, void* workspace, size_t workspace_bytes,
+                                  struct ihipStream_t* stream);
+
+/*
+ * Backward of it, from the forward's pre (unused without an activation; relu's slope at 0 is 0):
+ *   dpre = dy act'(pre),  dX = dpre W,  dW = dpre^T X,  dbias = sum_m dpre
+ * (the residual's gradient is dy itself).  dy bf16 or fp32; dX [M, K] and dW [N, K] bf16 with any
+ * row strides; dbias [N] bf16 or fp32; each may be NULL.  dpre is rounded to bf16 for the two
+ * products (the operands of the matrix instruction), not for dbias.  X is needed for dW, W for
+ * dX.  M = 0 writes zeros to dW and dbias.  No atomics: bitwise repeatable.  workspace as above,
+ * with the backward bytes.
+ */
+flce_status_t flce_linear_backward(const void* dy, int dy_dtype, int64_t lddy, const void* pre,
+                                   int64_t ldp, int activation, const void* X, int64_t ldx,
+                                   const void* W, int64_t ldw, int64_t M, int64_t N, int64_t K,
+                                   void* dX, int64_t lddx, void* dW, int64_t lddw, void* dbias,
+                                   int bias_dtype, void* workspace, size_t workspace_bytes,
+                                   struct ihipStream_t* stream);
+
+/*
+ * Dropout over x [M, H] and the residual it is added to (NULL: none):
+ *   y = residual + x keep / (1 - q),  keep[m, h] = bits[m, h] >= threshold
+ * with threshold = 65536 p rounded to nearest, q = threshold / 65536, and 16 random bits an
+ * element from Philox4x32-10 (Salmon, Moraes, Dror, Shaw, SC11): counter (h / 8, m, offset low,
+ * offset high), key (seed low, seed high); column h takes word (h % 8) / 2, the low half where h
+ * is even.  The mask is not stored: the gradient of x is the same call on dy without a residual
+ * (the residual's gradient is dy itself).  seed_at (NULL: seed counts) is a place in device memory
+ * that the kernel reads the seed from, so that a captured call draws anew where its caller writes
+ * there.  A call needs a (seed, offset) of its own for masks of its own.  x, residual and y are
+ * bf16 or fp32 each, with any row strides, naturally aligned; 0 <= p <= 1 (1: everything is
+ * dropped); sums in fp32; a dropped infinity or NaN is gone.  0 <= M <= 2^30 (0: nothing is
+ * touched), 1 <= H <= 2^20.  y may be x or residual where their types and strides agree.
+ */
+flce_status_t flce_dropout(const void* x, int x_dtype, int64_t ldx, const void* residual,
+                           int residual_dtype, int64_t ldr, int64_t M, int64_t H, double p,
+                           uint64_t seed, const uint64_t* seed_at, uint64_t offset, void* y,
+                           int y_dtype, int64_t ldy, struct ihipStream_t* stream);
+
+/*
+ * Log-probs of given tokens, entropy and the largest alternatives from logits x [M, V] (bf16 or
+ * fp32, any row stride, naturally aligned), under softmax(scale x), 0 < scale <= 2^64:
+ *   logprob[m, j] = log p[m, tokens[m, j]]     (0 where the token is ignore_index or outside
+ *                                               [0, V); tokens int64 [M, n_tokens])
+ *   lse[m] = log sum_v exp(scale x),  entropy[m] = -sum_v p log p          (NULL: not wanted)
+ *   top_ids[m, i], top_logprob[m, i]: the n_top largest logits of the row, in falling order,
+ *                                     equal ones by their index
+ * and stats[m] = (largest logit, log sum_v exp(scale (x - largest))) for the backward.  All of
+ * them fp32, ids int64; sums in fp32.  A logit of -inf is masked: it has probability 0 and adds
+ * nothing.  In a row that is masked throughout lse and every log-prob are -inf and entropy is 0.
+ * In a row with a NaN or +inf they are NaN, the alternatives in their order all the same, NaNs
+ * with the masked ones.  0 <= M <= 2^30 (0: nothing is touched), 1 <= V <= 2^30, n_tokens <=
+ * FLCE_MAX_TOKENS, n_top <= FLCE_MAX_TOP and V; either may be 0.  workspace: 256-byte aligned, at
+ * least flce_token_logprobs_workspace bytes (0: may be NULL).
+ */
+#define FLCE_MAX_TOP 128
+#define FLCE_MAX_TOKENS 1024
+flce_status_t flce_token_logprobs_workspace(int64_t M, int64_t V, int64_t n_top, size_t* bytes);
+flce_status_t flce_token_logprobs(const void* logits, int dtype, int64_t ldl, int64_t M, int64_t V,
+                                  const int64_t* tokens, int64_t n_tokens, int64_t ignore_index,
+                                  float scale, int64_t n_top, float* logprob, float* lse,
+                                  float* entropy, float* stats, int64_t* top_ids,
+                                  float* top_logprob, void* workspace, size_t workspace_bytes,
+                                  struct ihipStream_t* stream);
+
+/*
+ * Gradient of those with respect to the logits:
+ *   dx[m, v] = scale (sum_j g[m, j] (1[v = t[m, j]] - p[m, v])
+ *                     - b[m] p[m, v] (log p[m, v] + entropy[m]) + c[m] p[m, v])
+ * over the given tokens with grad_logprob [M, n_tokens] and the alternatives with grad_top [M,
+ * n_top] (NULL: none of them), b = grad_entropy [M] (NULL: 0; needs the forward's entropy), c =
+ * grad_lse [M] (NULL: 0).  Ignored
+ * and invalid tokens add nothing; a token given several times adds each of its gradients.  dlogits
+ * has the logits' type, any row stride, and may be their own memory.  Rows that nothing valid is
+ * asked of, and rows masked throughout, get zeros.
+ */
+flce_status_t flce_token_logprobs_backward(const void* logits, int dtype, int64_t ldl, int64_t M,
+                                           int64_t V, const int64_t* tokens, int64_t n_tokens,
+                                           int64_t ignore_index, float scale, const float* stats,
+                                           const float* entropy, const int64_t* top_ids,
+                                           int64_t n_top, const float* grad_logprob,
+                                           const float* grad_top, const float* grad_entropy,
+                                           const float* grad_lse, void* dlogits, int64_t ldd,
+                                           struct ihipStream_t* stream);
+
 /* Static description of a status code. */
 const char* flce_status_string(flce_status_t status);
 

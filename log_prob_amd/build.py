@@ -17,7 +17,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["flce_kernels.hip", "norm_kernels.hip", "mx_quant_kernels.hip",
-           "mx_stream_kernels.hip", "mx_tile_kernels.hip", "flce_api.cpp", "ops_api.cpp"]
+           "mx_stream_kernels.hip", "mx_tile_kernels.hip", "linear_kernels.hip",
+           "logprob_kernels.hip", "dropout_kernels.hip", "flce_api.cpp", "ops_api.cpp",
+           "block_api.cpp"]
 LIB = os.path.join(HERE, "libflce.so")
 BINDING = os.path.join(HERE, "_binding.so")
 ARCH = "gfx950"

@@ -1,0 +1,634 @@
+// Log-probs of given tokens, entropy and the largest alternatives from a matrix of logits, and
+// their gradient (gfx950).
+//
+//   m = max_v x_v,  S = sum_v exp(scale (x_v - m)),  logp_v = scale (x_v - m) - log S
+//   lse = scale m + log S,  entropy = log S - sum_v exp(scale (x_v - m)) scale (x_v - m) / S
+//   dx_v = scale (sum_j g_j (1[v = t_j] - p_v) - b p_v (logp_v + entropy) + c p_v)
+//          g, b, c: gradients of the log-probs, the entropy and lse
+//
+// Both are bound by memory: the logits are read once, with the running maximum, the sums and
+// the alternatives of a row kept on the way, and the gradient reads them once more and writes
+// as much.  A workgroup takes a row, or a piece of it where there are few rows; the pieces
+// meet in a second kernel.
+//
+// Alternatives: candidates above a running threshold go to LDS with their index.  The first
+// 8192 logits set it: the k-th largest of the 256 threads' own maxima is at most the k-th largest
+// of all (k different elements reach it), and about k elements lie above it.  When candidates
+// pile up, the k-th largest of them (found bit by bit, the counts by ballots) becomes the
+// threshold and the others go.  So of a row of independent logits a few hundred ever reach LDS;
+// rows in ascending order reach it whole, in steps that fit.  Order is that of the logits, equal
+// ones by their index; the order in which candidates arrive changes nothing.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "block_internal.h"
+#include "mx_device.h"
+#include "tile_device.h"
+
+namespace flce {
+
+namespace {
+
+constexpr int T = 256;              // threads of a workgroup
+constexpr int NV = 4;               // vectors of 8 logits a thread holds at once
+constexpr int VEC_STEP = 8 * T;     // logits of one vector of every thread
+constexpr int STEP = NV * VEC_STEP;
+constexpr int CAP = 2048;           // candidates in LDS
+constexpr int CROWDED = 512;        // more than these are thinned out
+constexpr int SPARE = 64;           // equal logits kept beyond k without a look at their index
+constexpr float LOWEST = -3.402823466e38f;
+static_assert(CAP >= kMaxTop + SPARE + VEC_STEP / 2, "half a vector of every thread fits after thinning");
+
+// Floats ordered as whole numbers.  -0 is 0, and a NaN ranks with -inf.
+constexpr uint32_t KEY_NONE = 0x007fffffu;  // -inf
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  const uint32_t k = u & 0x80000000u ? ~u : u | 0x80000000u;
+  return x > -INFINITY ? k : KEY_NONE;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+// A float that everything of at least this key exceeds, and nothing else does (-inf: all numbers
+// exceed it; below 0 comes the first negative number, not -0).
+__device__ __forceinline__ float below(uint32_t k) {
+  return k <= KEY_NONE + 1 ? -INFINITY : value_of(k == 0x80000000u ? k - 2 : k - 1);
+}
+
+// Candidates of a row, and what the waves tell each other.
+struct Shared {
+  uint32_t key[CAP];
+  uint32_t idx[CAP];
+  uint32_t lane_key[T];
+  int count;
+  float threshold;
+  float red[3][T / 64];
+};
+
+__device__ __forceinline__ int count_of(bool b) { return __popcll(__ballot(b)); }
+
+// The largest t with count(t) >= k, for a count that falls with t, where the answer shares the
+// bits above `bits` with `prefix`; found early where the count is k exactly.
+template <class Count>
+__device__ __forceinline__ uint32_t kth(uint32_t prefix, int bits, int k, Count count) {
+  uint32_t t = prefix;
+  for (int b = bits - 1; b >= 0; --b) {
+    const uint32_t c = t | (1u << b);
+    const int n = count(c);
+    if (n >= k) t = c;
+    if (n == k) break;
+  }
+  return t;
+}
+// Bits in which values between lo and hi may differ, and the rest of them.
+__device__ __forceinline__ int open_bits(uint32_t lo, uint32_t hi) {
+  return lo == hi ? 0 : 32 - __clz((int)(lo ^ hi));
+}
+__device__ __forceinline__ uint32_t closed(uint32_t lo, int bits) { return bits >= 32 ? 0u : lo >> bits << bits; }
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const uint32_t w = (uint32_t)__shfl_xor((int)v, o);
+    v = v > w ? v : w;
+  }
+  return v;
+}
+__device__ __forceinline__ uint32_t wave_min(uint32_t v) { return ~wave_max(~v); }
+
+// Wave 0: keep the k largest of sh.count > k candidates, and up to SPARE more that equal the
+// last of them; the threshold becomes that one's logit.  Candidates that come later have larger
+// indexes, so only larger logits can displace what is kept.
+__device__ __forceinline__ void thin_out(Shared& sh, int k) {
+  const int lane = threadIdx.x & 63, n = min(sh.count, CAP);
+  uint32_t lo = ~0u, hi = 0u;
+  for (int i = lane; i < n; i += 64) {
+    lo = min(lo, sh.key[i]);
+    hi = max(hi, sh.key[i]);
+  }
+  lo = wave_min(lo);
+  hi = wave_max(hi);
+  const int bits = open_bits(lo, hi);
+  const uint32_t t = kth(closed(lo, bits), bits, k, [&](uint32_t c) {
+    int s = 0;
+    for (int i = lane; i < n + lane; i += 64) s += count_of(i < n && sh.key[i] >= c);
+    return s;
+  });
+  // (t may lie between two candidates: the threshold is the least one at or above it)
+  int above = 0, equal = 0;
+  uint32_t least = ~0u;
+  for (int i = lane; i < n; i += 64)
+    if (sh.key[i] >= t) least = min(least, sh.key[i]);
+  least = wave_min(least);
+  for (int i = lane; i < n + lane; i += 64) {
+    above += count_of(i < n && sh.key[i] > least);
+    equal += count_of(i < n && sh.key[i] == least);
+  }
+  uint32_t last = ~0u;  // the largest index kept among equal ones
+  if (above + equal > k + SPARE) {
+    // the (k - above)-th smallest index among them: the kth largest of the complements
+    last = ~kth(0u, 32, k - above, [&](uint32_t c) {
+      int s = 0;
+      for (int i = lane; i < n + lane; i += 64) s += count_of(i < n && sh.key[i] == least && ~sh.idx[i] >= c);
+      return s;
+    });
+  }
+  // compact in place: what a step reads lies at or behind what it writes
+  int kept = 0;
+  for (int i = lane; i < n + lane; i += 64) {
+    const bool in = i < n;
+    const uint32_t key = in ? sh.key[i] : 0u, idx = in ? sh.idx[i] : 0u;
+    const bool keep = in && (key > least || (key == least && idx <= last));
+    const unsigned long long mask = __ballot(keep);
+    const int at = kept + __popcll(mask & ((1ull << lane) - 1ull));
+    if (keep) {
+      sh.key[at] = key;
+      sh.idx[at] = idx;
+    }
+    kept += __popcll(mask);
+  }
+  if (lane == 0) {
+    sh.count = kept;
+    sh.threshold = value_of(least);
+  }
+}
+
+// Every thread: thin out where there are more candidates than `most`.  The count is read between
+// two barriers, so that all threads decide alike.
+__device__ __forceinline__ void settle(Shared& sh, int k, int most) {
+  __syncthreads();
+  const int n = sh.count;
+  __syncthreads();
+  if (n > most && n > k) {
+    if (threadIdx.x < 64) thin_out(sh, k);
+    __syncthreads();
+  }
+}
+
+// Running maximum and sums of one thread: s = sum 2^d, u = sum 2^d d, d = c (x - m).
+template <bool ENT>
+struct Sums {
+  float m = LOWEST, s = 0.f, u = 0.f;
+  __device__ __forceinline__ void raise(float to, float c) {
+    // (bounded, so that nothing of a sum that is still 0 becomes 0 times infinity)
+    const float d = fmaxf((m - to) * c, -1e30f), r = __builtin_amdgcn_exp2f(d);
+    if constexpr (ENT) u = r * fmaf(d, s, u);
+    s *= r;
+    m = to;
+  }
+  __device__ __forceinline__ void add(const float (&x)[8], float top, float c) {
+    if (top > m) raise(top, c);
+    float e[8], w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = (x[i] - m) * c;
+      e[i] = __builtin_amdgcn_exp2f(d);
+      // (a masked logit: 0 times its bound)
+      if constexpr (ENT) w[i] = e[i] * fmaxf(d, -1e30f);
+    }
+    s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    if constexpr (ENT) u += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+  }
+};
+
+// Their largest, or a NaN where one of them is a signaling one (v_max3_f32 issued directly: fmaxf
+// quiets each input first).
+__device__ __forceinline__ float max8(const float (&x)[8]) {
+  return max3_run<false>(max3_run<false>(max3_run<false>(max_raw(x[0], x[1]), x[2], x[3]), x[4], x[5]), x[6], x[7]);
+}
+
+// (m, s, u) of the workgroup from those of its threads, in every thread.
+template <bool ENT>
+__device__ __forceinline__ void join(Sums<ENT>& a, Shared& sh, float c) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float m = a.m;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if (lane == 0) sh.red[0][wave] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < T / 64; ++w) m = fmaxf(m, sh.red[0][w]);
+  a.raise(m, c);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    a.s += __shfl_xor(a.s, o);
+    if constexpr (ENT) a.u += __shfl_xor(a.u, o);
+  }
+  if (lane == 0) {
+    sh.red[1][wave] = a.s;
+    if constexpr (ENT) sh.red[2][wave] = a.u;
+  }
+  __syncthreads();
+  a.s = sh.red[1][0];
+  a.u = ENT ? sh.red[2][0] : 0.f;
+#pragma unroll
+  for (int w = 1; w < T / 64; ++w) {
+    a.s += sh.red[1][w];
+    if constexpr (ENT) a.u += sh.red[2][w];
+  }
+}
+
+// The place of candidate i among the n (n is small: the last thinning left at most k + SPARE).
+__device__ __forceinline__ int rank_of(const Shared& sh, int i, int n) {
+  const uint32_t key = sh.key[i], idx = sh.idx[i];
+  int r = 0;
+  for (int j = 0; j < n; ++j) r += sh.key[j] > key || (sh.key[j] == key && sh.idx[j] < idx);
+  return r;
+}
+
+// A row's results from its sums and, in LDS, its candidates.
+template <class TX, bool TOP>
+__device__ __forceinline__ void finish_row(const TokenLogprobArgs& p, long row, float m, float s, float u,
+                                           Shared& sh) {
+  const typename TX::mem* x = static_cast<const typename TX::mem*>(p.logits) + row * p.ldl;
+  const float nan = __uint_as_float(0x7fc00000u);
+  // s: 0 where every logit is masked, a NaN where one is an infinity or a NaN
+  const bool none = s == 0.f, bad = !(s >= 0.f) || m == INFINITY;
+  const float logs = bad ? nan : none ? 0.f : logf(s);
+  const float top = bad ? nan : none ? -INFINITY : m;
+  auto logp = [&](float v) { return bad ? nan : none ? -INFINITY : at_most_zero(p.scale * (v - top) - logs); };
+  if (threadIdx.x == 0) {
+    p.stats[2 * row] = top;
+    p.stats[2 * row + 1] = logs;
+    p.lse[row] = fmaf(p.scale, top, logs);
+    if (p.entropy) p.entropy[row] = bad ? nan : none ? 0.f : at_least_zero(logs - u * LN2 / s);
+  }
+  for (int j = threadIdx.x; j < p.n_tokens; j += T) {
+    const int64_t t = p.tokens[row * p.n_tokens + j];
+    const bool valid = t != p.ignore_index && t >= 0 && t < p.V;
+    p.logprob[row * p.n_tokens + j] = valid ? logp(TX::to_f32(x[t])) : 0.f;
+  }
+  if constexpr (TOP) {
+    const int n = sh.count, k = p.n_top;
+    for (int i = threadIdx.x; i < n; i += T) {
+      const int r = rank_of(sh, i, n);
+      if (r < k) {
+        p.top_ids[row * k + r] = (int64_t)sh.idx[i];
+        p.top_logprob[row * k + r] = logp(value_of(sh.key[i]));
+      }
+    }
+    // fewer than k logits above -inf: the first of the others follow.  Fewer than k of the first
+    // 2 k logits are above it, so those hold enough (k <= V)
+    if (n < k && threadIdx.x < 64) {
+      int at = n;
+      for (int v0 = 0; v0 < min(2 * k, p.V); v0 += 64) {
+        const int v = v0 + (int)threadIdx.x;
+        const bool masked = v < p.V && !(TX::to_f32(x[v < p.V ? v : 0]) > -INFINITY);
+        const unsigned long long mask = __ballot(masked);
+        const int r = at + __popcll(mask & ((1ull << threadIdx.x) - 1ull));
+        if (masked && r < k) {
+          p.top_ids[row * k + r] = v;
+          p.top_logprob[row * k + r] = bad ? nan : -INFINITY;
+        }
+        at += __popcll(mask);
+      }
+    }
+  }
+}
+
+template <class TX, bool VEC, bool ENT, bool TOP>
+__global__ __launch_bounds__(T) void token_logprob_kernel(TokenLogprobArgs p) {
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, k = p.n_top;
+  const float c = p.scale * LOG2E;
+  const long items = p.M * p.parts;
+  for (long item = blockIdx.x; item < items; item += gridDim.x) {
+    const long row = item / p.parts;
+    const int part = (int)(item - row * p.parts);
+    const int v0 = part * p.part_len, v1 = min(p.V, v0 + p.part_len);
+    const typename TX::mem* x = static_cast<const typename TX::mem*>(p.logits) + row * p.ldl;
+    Sums<ENT> sums;
+    float threshold = -INFINITY;
+    int held = 0;  // candidates in LDS
+    if constexpr (TOP) {
+      if (tid == 0) sh.count = 0;
+    }
+    for (int base = v0; base < v1; base += STEP) {
+      Chunk8<TX, VEC> raw[NV];
+      float top[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int col = base + j * VEC_STEP + 8 * tid;
+        raw[j].load(x, col, col < v1 ? (long)p.V : 0l);
+      }
+      auto values = [&](int j, float (&v)[8]) {
+        const int col = base + j * VEC_STEP + 8 * tid;
+        raw[j].value(col, p.V, v);
+        if (base + STEP > v1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = col + i < v1 ? v[i] : -INFINITY;
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        float v[8];
+        values(j, v);
+        top[j] = max8(v);
+        sums.add(v, top[j], c);
+      }
+      if constexpr (TOP) {
+        if (base == v0) {
+          float most = top[0];
+#pragma unroll
+          for (int j = 1; j < NV; ++j) most = fmaxf(most, top[j]);
+          sh.lane_key[tid] = key_of(most);
+          __syncthreads();
+          uint32_t mine[T / 64], hi = 0u, lo = ~0u;
+#pragma unroll
+          for (int w = 0; w < T / 64; ++w) {
+            mine[w] = sh.lane_key[64 * w + (tid & 63)];
+            hi = max(hi, mine[w]);
+            lo = min(lo, mine[w]);
+          }
+          hi = wave_max(hi);
+          lo = wave_min(lo);
+          // (every wave for itself: the same answer)
+          const int bits = open_bits(lo, hi);
+          threshold = below(kth(closed(lo, bits), bits, k, [&](uint32_t cand) {
+            int n = 0;
+#pragma unroll
+            for (int w = 0; w < T / 64; ++w) n += count_of(mine[w] >= cand);
+            return n;
+          }));
+        }
+        auto offer = [&](float value, int col) {
+          if (value > threshold) {
+            const int at = atomicAdd(&sh.count, 1);
+            if (at < CAP) {
+              sh.key[at] = key_of(value);
+              sh.idx[at] = (uint32_t)col;
+            }
+          }
+        };
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if (!(top[j] <= threshold)) {
+            float v[8];
+            values(j, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) offer(v[i], base + j * VEC_STEP + 8 * tid + i);
+          }
+        __syncthreads();
+        const int now = sh.count;  // (between barriers: the same for every thread)
+        __syncthreads();
+        if (now > CAP) {
+          // they do not fit: again in halves of a vector, thinned out after each
+          if (tid == 0) sh.count = held;
+          __syncthreads();
+          settle(sh, k, k + SPARE);
+          // (indexes do not ascend from one half to the next, so the halves keep the threshold
+          // of the steps before them and offer what equals a later one too)
+          if (held > k + SPARE) threshold = sh.threshold;
+#pragma unroll 1
+          for (int h = 0; h < 2 * NV; ++h) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+              if (j == h / 2) {
+                float v[8];
+                values(j, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float a = h & 1 ? v[4 + i] : v[i];
+                  offer(a, base + j * VEC_STEP + 8 * tid + 4 * (h & 1) + i);
+                }
+              }
+            settle(sh, k, k + SPARE);
+          }
+          threshold = sh.threshold;
+          held = sh.count;
+          __syncthreads();
+        } else if (now > CROWDED) {
+          if (tid < 64) thin_out(sh, k);
+          __syncthreads();
+          threshold = sh.threshold;
+          held = sh.count;
+          __syncthreads();
+        } else {
+          held = now;
+        }
+      }
+    }
+    join<ENT>(sums, sh, c);
+    if constexpr (TOP) settle(sh, k, k + SPARE);
+    if (p.parts == 1) {
+      finish_row<TX, TOP>(p, row, sums.m, sums.s, sums.u, sh);
+    } else {
+      if (tid == 0) {
+        float* to = p.part_sums + 3 * item;
+        to[0] = sums.m;
+        to[1] = sums.s;
+        to[2] = sums.u;
+      }
+      if constexpr (TOP) {
+        const int n = sh.count;
+        unsigned long long* to = p.part_top + item * k;
+        for (int i = tid; i < n; i += T) {
+          const int r = rank_of(sh, i, n);
+          if (r < k) to[r] = (unsigned long long)sh.key[i] << 32 | (uint32_t)~sh.idx[i];
+        }
+        for (int r = n + tid; r < k; r += T) to[r] = 0ull;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// The pieces of a row: their sums rescaled to the largest maximum, their candidates together.
+template <class TX, bool TOP>
+__global__ __launch_bounds__(T) void token_logprob_join_kernel(TokenLogprobArgs p) {
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, k = p.n_top;
+  const float c = p.scale * LOG2E;
+  for (long row = blockIdx.x; row < p.M; row += gridDim.x) {
+    const float* part = p.part_sums + 3 * row * p.parts;
+    float m = LOWEST;
+    for (int i = 0; i < p.parts; ++i) m = fmaxf(m, part[3 * i]);
+    float s = 0.f, u = 0.f;
+    for (int i = 0; i < p.parts; ++i) {
+      const float d = fmaxf((part[3 * i] - m) * c, -1e30f), r = __builtin_amdgcn_exp2f(d);
+      s += r * part[3 * i + 1];
+      u += r * fmaf(d, part[3 * i + 1], part[3 * i + 2]);
+    }
+    if constexpr (TOP) {
+      if (tid == 0) sh.count = 0;
+      __syncthreads();
+      const int n = p.parts * k;  // at most CAP
+      const unsigned long long* from = p.part_top + row * n;
+      for (int i = tid; i < n; i += T) {
+        const unsigned long long e = from[i];
+        if (e) {
+          const int at = atomicAdd(&sh.count, 1);
+          sh.key[at] = (uint32_t)(e >> 32);
+          sh.idx[at] = ~(uint32_t)e;
+        }
+      }
+      settle(sh, k, k + SPARE);
+    }
+    finish_row<TX, TOP>(p, row, m, s, u, sh);
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The gradient: a workgroup takes a piece of a row.  What the given tokens add is computed first
+// (from the logits, so dlogits may be the logits' own memory) and written over the rest after a
+// barrier; several entries of one token are added in their order.
+constexpr int LIST = kMaxTokens + kMaxTop;
+
+struct GradShared {
+  int id[LIST];     // the entry's token, -1 outside this piece
+  float g[LIST];
+  int at[LIST];     // where the entry's thread writes `value`, -1: nowhere
+  float value[LIST];
+  float red[T / 64];
+  int any[T / 64];
+};
+
+template <class TX, bool VEC>
+__global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradArgs p, int pieces) {
+  __shared__ GradShared sh;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int L = p.n_tokens + p.n_top;
+  const long items = p.M * pieces;
+  for (long item = blockIdx.x; item < items; item += gridDim.x) {
+    const long row = item / pieces;
+    const int v0 = (int)(item - row * pieces) * STEP, v1 = min(p.V, v0 + STEP);
+    const typename TX::mem* x = static_cast<const typename TX::mem*>(p.logits) + row * p.ldl;
+    typename TX::mem* dx = static_cast<typename TX::mem*>(p.dlogits) + row * p.ldd;
+    Chunk8<TX, VEC> raw[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int col = v0 + j * VEC_STEP + 8 * tid;
+      raw[j].load(x, col, col < v1 ? (long)p.V : 0l);
+    }
+    const float top = p.stats[2 * row], logs = p.stats[2 * row + 1];
+    const float b = p.grad_entropy ? p.grad_entropy[row] : 0.f, ent = p.grad_entropy ? p.entropy[row] : 0.f;
+    const float of_lse = p.grad_lse ? p.grad_lse[row] : 0.f;
+
+    // the list of (token, gradient): their sum, and those of this piece
+    float sum = 0.f;
+    bool any = false;
+    for (int j = tid; j < L; j += T) {
+      const bool given = j < p.n_tokens;
+      const long at = given ? row * p.n_tokens + j : row * p.n_top + (j - p.n_tokens);
+      const int64_t t = given ? p.tokens[at] : p.top_ids[at];
+      const bool valid = !(given && t == p.ignore_index) && t >= 0 && t < p.V;
+      const float g = valid ? (given ? p.grad_logprob : p.grad_top)[at] : 0.f;
+      sum += g;
+      any |= valid;
+      sh.id[j] = valid && t >= v0 && t < v1 ? (int)t : -1;
+      sh.g[j] = g;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+    const bool any_wave = __any(any);
+    if (lane == 0) {
+      sh.red[wave] = sum;
+      sh.any[wave] = any_wave;
+    }
+    __syncthreads();
+    sum = sh.red[0];
+    any = sh.any[0];
+#pragma unroll
+    for (int w = 1; w < T / 64; ++w) {
+      sum += sh.red[w];
+      any |= sh.any[w] != 0;
+    }
+    // a row that nothing is asked of, or in which everything is masked, has no gradient
+    const bool zero = (!any && b == 0.f && of_lse == 0.f) || top == -INFINITY;
+    const float c0 = zero ? 0.f : p.scale * (of_lse - fmaf(b, ent, sum)), c1 = zero ? 0.f : -p.scale * b;
+    auto slope = [&](float v) {
+      const float lp = fmaxf(fmaf(p.scale, v - top, -logs), -1e30f);
+      return __builtin_amdgcn_exp2f(lp * LOG2E) * fmaf(c1, lp, c0);
+    };
+    // (a NaN in the row's statistics has to reach every element: fmaxf alone would drop it)
+    const float add_nan = zero ? 0.f : 0.f * (top + logs);
+
+    for (int j = tid; j < L; j += T) {
+      const int id = zero ? -1 : sh.id[j];
+      int first = -1;  // the first entry of this token
+      float g = 0.f;
+      if (id >= 0)
+        for (int i = L - 1; i >= 0; --i)
+          if (sh.id[i] == id) first = i;
+      if (first == j)
+        for (int i = j; i < L; ++i) g += sh.id[i] == id ? sh.g[i] : 0.f;
+      sh.at[j] = first == j ? id : -1;
+      if (first == j) sh.value[j] = fmaf(p.scale, g, slope(TX::to_f32(x[id]))) + add_nan;
+    }
+    // (every read of these logits by hand is done before any is overwritten)
+    wait_vmcnt<0>();
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int col = v0 + j * VEC_STEP + 8 * tid;
+      float v[8];
+      raw[j].value(col, p.V, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = zero ? 0.f : slope(v[i]) + add_nan;
+      if (col < v1) store8<TX, VEC>(dx, col, p.V, v);
+    }
+    wait_vmcnt<0>();
+    __syncthreads();
+    for (int j = tid; j < L; j += T)
+      if (sh.at[j] >= 0) dx[sh.at[j]] = TX::from_f32(sh.value[j]);
+  }
+}
+
+template <class TX, bool VEC, bool ENT>
+void run_parts(const TokenLogprobArgs& a, unsigned grid, hipStream_t s) {
+  if (a.n_top) token_logprob_kernel<TX, VEC, ENT, true><<<grid, T, 0, s>>>(a);
+  else token_logprob_kernel<TX, VEC, ENT, false><<<grid, T, 0, s>>>(a);
+}
+template <class TX>
+void run(const TokenLogprobArgs& a, bool vec, hipStream_t s) {
+  const long items = a.M * a.parts, most = 1 << 22;
+  const unsigned grid = (unsigned)(items < most ? items : most);
+  if (vec) {
+    if (a.entropy) run_parts<TX, true, true>(a, grid, s);
+    else run_parts<TX, true, false>(a, grid, s);
+  } else {
+    if (a.entropy) run_parts<TX, false, true>(a, grid, s);
+    else run_parts<TX, false, false>(a, grid, s);
+  }
+  if (a.parts > 1) {
+    const unsigned rows = (unsigned)(a.M < most ? a.M : most);
+    if (a.n_top) token_logprob_join_kernel<TX, true><<<rows, T, 0, s>>>(a);
+    else token_logprob_join_kernel<TX, false><<<rows, T, 0, s>>>(a);
+  }
+}
+
+}  // namespace
+
+void token_logprob_split(int64_t M, int64_t V, int n_top, int* parts, int* part_len) {
+  const int64_t pieces = (V + VEC_STEP - 1) / VEC_STEP;
+  int64_t want = M >= 2048 || M < 1 ? 1 : 2048 / M;
+  if (want > 128) want = 128;
+  if (n_top && want > CAP / n_top) want = CAP / n_top;
+  if (want > pieces) want = pieces;
+  const int64_t each = (pieces + want - 1) / want;
+  *part_len = int(each * VEC_STEP);
+  *parts = int((pieces + each - 1) / each);
+}
+
+hipError_t launch_token_logprobs(const TokenLogprobArgs& a, int dtype, bool vec, hipStream_t s) {
+  if (dtype == kF32) run<F32>(a, vec, s);
+  else run<Bf16>(a, vec, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_token_logprobs_grad(const TokenLogprobGradArgs& a, int dtype, bool vec, hipStream_t s) {
+  const int pieces = (a.V + STEP - 1) / STEP;
+  const long items = a.M * pieces, most = 1 << 22;
+  const unsigned grid = (unsigned)(items < most ? items : most);
+  if (dtype == kF32) {
+    if (vec) token_logprob_grad_kernel<F32, true><<<grid, T, 0, s>>>(a, pieces);
+    else token_logprob_grad_kernel<F32, false><<<grid, T, 0, s>>>(a, pieces);
+  } else {
+    if (vec) token_logprob_grad_kernel<Bf16, true><<<grid, T, 0, s>>>(a, pieces);
+    else token_logprob_grad_kernel<Bf16, false><<<grid, T, 0, s>>>(a, pieces);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace flce

@@ -31,6 +31,8 @@ EXPORTS = ("flce_workspace_query", "flce_forward_workspace_min", "flce_forward_w
            "flce_mx_sizes", "flce_mx_quantize", "flce_mx_dequantize", "flce_layer_norm_forward",
            "flce_layer_norm_backward_workspace", "flce_layer_norm_backward",
            "flce_mx_workspace_query", "flce_mx_logits", "flce_mx_forward",
+           "flce_linear_workspace", "flce_linear_forward", "flce_linear_backward", "flce_dropout",
+           "flce_token_logprobs_workspace", "flce_token_logprobs", "flce_token_logprobs_backward",
            "flce_status_string",
            "flce_last_error_message", "flce_version")
 
@@ -94,7 +96,21 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.flce_mx_workspace_query.argtypes = [I64, I64, I64, I, c.POINTER(SZ), c.POINTER(SZ)]
     lib.flce_mx_logits.argtypes = [P, P, P, I64, I64, I64, c.c_float, P, I, I64, P, SZ, P]
     lib.flce_mx_forward.argtypes = [P, P, P, P, I64, I64, I64, I64, c.c_float, I, P, P, P, P, SZ, P]
-    for name in ("flce_mx_workspace_query", "flce_mx_logits", "flce_mx_forward",
+    U64, F = c.c_uint64, c.c_float
+    lib.flce_linear_workspace.argtypes = [I64, I64, I64, c.POINTER(SZ), c.POINTER(SZ)]
+    lib.flce_linear_forward.argtypes = [P, I64, P, I64, P, I, I, P, I, I64, I64, I64, I64, P, I,
+                                        I64, P, I64, P, SZ, P]
+    lib.flce_linear_backward.argtypes = [P, I, I64, P, I64, I, P, I64, P, I64, I64, I64, I64, P,
+                                         I64, P, I64, P, I, P, SZ, P]
+    lib.flce_dropout.argtypes = [P, I, I64, P, I, I64, I64, I64, D, U64, P, U64, P, I, I64, P]
+    lib.flce_token_logprobs_workspace.argtypes = [I64, I64, I64, c.POINTER(SZ)]
+    lib.flce_token_logprobs.argtypes = [P, I, I64, I64, I64, P, I64, I64, F, I64, P, P, P, P, P, P,
+                                        P, SZ, P]
+    lib.flce_token_logprobs_backward.argtypes = [P, I, I64, I64, I64, P, I64, I64, F, P, P, P, I64,
+                                                 P, P, P, P, P, I64, P]
+    for name in ("flce_linear_workspace", "flce_linear_forward", "flce_linear_backward",
+                 "flce_dropout", "flce_token_logprobs_workspace", "flce_token_logprobs",
+                 "flce_token_logprobs_backward", "flce_mx_workspace_query", "flce_mx_logits", "flce_mx_forward",
                  "flce_mx_sizes", "flce_mx_quantize", "flce_mx_dequantize",
                  "flce_layer_norm_forward", "flce_layer_norm_backward_workspace",
                  "flce_layer_norm_backward", "flce_nll_reduce", "flce_nll_mean_grad",
@@ -902,3 +918,286 @@ def mxfp4_forward(X, W: MXTensor, targets, ignore_index: int = -100, scale: floa
             targets.data_ptr(), m, h, v, ignore_index, scale, ent, logprob.data_ptr(), lse.data_ptr(),
             _ptr(entropy), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return logprob, lse, entropy
+
+
+# ----------------------------------------------------------------------------
+# the residual block in front of the head: matrix product with an epilogue, dropout
+ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _activation(name) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation: expected one of {tuple(ACTIVATIONS)}, got {name!r}")
+    return ACTIVATIONS[name]
+
+
+def _operand(t, name, dev, shape=None):
+    """Check a bf16 matrix with contiguous rows; returns its row stride."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    return _rows(t, name, dev, shape)
+
+
+def _result(out, name, dtype, dev, shape, what):
+    """A result's buffer: a new one, or the caller's, checked; with its type's id and row stride."""
+    import torch
+    if out is None:
+        out = torch.empty(*shape, dtype=dtype, device=dev)
+    elif out.dtype != dtype:
+        raise TypeError(f"{name}: expected {what} {dtype}, got {out.dtype}")
+    return out, _dtype_id(out, name), _rows(out, name, dev, shape)
+
+
+@functools.lru_cache(maxsize=256)
+def linear_workspace(M: int, N: int, K: int) -> Tuple[int, int]:
+    """Workspace bytes of (linear_forward, linear_backward)."""
+    fw, bw = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load().flce_linear_workspace(int(M), int(N), int(K), ctypes.byref(fw), ctypes.byref(bw)))
+    return fw.value, bw.value
+
+
+def linear_forward(X, W, bias=None, activation: Optional[str] = None, residual=None, out_dtype=None,
+                   keep_pre: bool = False, workspace=None, out=None):
+    """act(X W^T + bias) + residual [M, N], bf16 (the default) or fp32; with keep_pre the pair of it
+    and X W^T + bias in bf16, for linear_backward.
+
+    X [M, K] and W [N, K] are bf16 with 16-byte aligned rows, bias [N] and residual [M, N] bf16 or
+    fp32; activation is None, "relu", "gelu", "gelu_tanh" or "silu".  `out` may supply the result's
+    buffer (with keep_pre the pair), and may be residual."""
+    act = _activation(activation)
+    import torch
+    dev = _on_gpu(X, "X")
+    ldx = _operand(X, "X", dev)
+    m, k = X.shape
+    ldw = _operand(W, "W", dev)
+    n = W.shape[0]
+    if W.shape[1] != k:
+        raise ValueError(f"W: expected {k} columns, got {W.shape[1]}")
+    bd = rd = 0
+    ldr = n
+    if bias is not None:
+        bd = _dtype_id(bias, "bias")
+        _vector(bias, "bias", dev, bias.dtype, n)
+    if residual is not None:
+        rd, ldr = _dtype_id(residual, "residual"), _rows(residual, "residual", dev, (m, n))
+    out, pre = out if keep_pre and out is not None else (out, None)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    out, od, ldo = _result(out, "out", out_dtype, dev, (m, n), "out_dtype")
+    ldp = n
+    if keep_pre:
+        pre, _, ldp = _result(pre, "pre", torch.bfloat16, dev, (m, n), "")
+    workspace = _workspace(workspace, linear_workspace(m, n, k)[0] if workspace is None else 0, dev)
+    _launch(dev, load().flce_linear_forward, X.data_ptr(), ldx, W.data_ptr(), ldw, _ptr(bias), bd, act,
+            _ptr(residual), rd, ldr, m, n, k, out.data_ptr(), od, ldo, _ptr(pre), ldp,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return (out, pre) if keep_pre else out
+
+
+def linear_backward(dy, X, W, pre=None, activation: Optional[str] = None, need_dx: bool = True,
+                    need_dw: bool = True, bias_dtype=None, workspace=None, out=None):
+    """(dX, dW, dbias) of linear_forward, from dy [M, N] (bf16 or fp32) and, with an activation,
+    the forward's pre.  dX and dW are bf16, or None where they are not needed; dbias has bias_dtype
+    (None: no dbias).  The gradient of the residual is dy.  `out` may supply the three buffers."""
+    act = _activation(activation)
+    import torch
+    dev = _on_gpu(dy, "dy")
+    dyd, lddy = _dtype_id(dy, "dy"), _rows(dy, "dy", dev)
+    m, n = dy.shape
+    ldx, ldw = _operand(X, "X", dev), _operand(W, "W", dev)
+    k = X.shape[1]
+    if X.shape[0] != m:
+        raise ValueError(f"X: expected {m} rows, got {X.shape[0]}")
+    if W.shape != (n, k):
+        raise ValueError(f"W: expected shape {(n, k)}, got {tuple(W.shape)}")
+    ldp = n
+    if act:
+        if pre is None:
+            raise ValueError("pre: needed with an activation (see keep_pre of linear_forward)")
+        ldp = _operand(pre, "pre", dev, (m, n))
+    dx, dw, db = (None, None, None) if out is None else out
+    lddx = lddw = k
+    if need_dx:
+        dx, _, lddx = _result(dx, "dX", torch.bfloat16, dev, (m, k), "")
+    if need_dw:
+        dw, _, lddw = _result(dw, "dW", torch.bfloat16, dev, (n, k), "")
+    bd = 0
+    if bias_dtype is not None:
+        if db is None:
+            db = torch.empty(n, dtype=bias_dtype, device=dev)
+        bd = _dtype_id(db, "dbias")
+        _vector(db, "dbias", dev, bias_dtype, n)
+    else:
+        db = None
+    workspace = _workspace(workspace, linear_workspace(m, n, k)[1] if workspace is None else 0, dev)
+    _launch(dev, load().flce_linear_backward, dy.data_ptr(), dyd, lddy, _ptr(pre) if act else None, ldp,
+            act, X.data_ptr(), ldx, W.data_ptr(), ldw, m, n, k, _ptr(dx) if need_dx else None, lddx,
+            _ptr(dw) if need_dw else None, lddw, _ptr(db), bd, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return dx if need_dx else None, dw if need_dw else None, db
+
+
+def _uint64(v, name) -> int:
+    v = int(v)
+    if not 0 <= v < 1 << 64:
+        raise ValueError(f"{name}: expected 0 <= {name} < 2^64, got {v}")
+    return v
+
+
+def dropout(x, p: float, seed, offset: int = 0, residual=None, out_dtype=None, out=None):
+    """residual + dropout(x) over a matrix [M, H]: an element is dropped with probability p (in steps
+    of 1 / 65536), and what is kept divided by the probability of that.
+
+    The mask follows from seed, offset and the element's place (include/flce.h), so it is not
+    kept: dropout_backward forms it again.  seed is an int, or an int64 GPU tensor of one element
+    that the kernel reads (so that a captured call draws anew where its caller writes there);
+    offset tells calls with one seed apart.  x and residual are bf16 or fp32; the result has
+    out_dtype, by default residual's dtype or x's.  `out` may supply its buffer, and may be x or
+    residual."""
+    import torch
+    dev = _on_gpu(x, "x")
+    xd, ldx = _dtype_id(x, "x"), _rows(x, "x", dev)
+    m, h = x.shape
+    rd, ldr = 0, h
+    if residual is not None:
+        rd, ldr = _dtype_id(residual, "residual"), _rows(residual, "residual", dev, (m, h))
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else x.dtype if residual is None else residual.dtype
+    out, yd, ldy = _result(out, "out", out_dtype, dev, (m, h), "out_dtype")
+    at = None
+    if isinstance(seed, torch.Tensor):
+        _vector(seed.reshape(-1), "seed", dev, torch.int64, 1)
+        seed, at = 0, seed.data_ptr()
+    _launch(dev, load().flce_dropout, x.data_ptr(), xd, ldx, _ptr(residual), rd, ldr, m, h, float(p),
+            _uint64(seed, "seed"), at, _uint64(offset, "offset"), out.data_ptr(), yd, ldy)
+    return out
+
+
+def dropout_backward(dy, p: float, seed, offset: int = 0, dx_dtype=None, out=None):
+    """Gradient of dropout's x (dx_dtype: dy's by default) with the forward's p, seed and offset.
+    The gradient of residual is dy."""
+    return dropout(dy, p, seed, offset, None, dx_dtype, out)
+
+
+# ----------------------------------------------------------------------------
+# log-probs, entropy and alternatives from logits
+class TokenLogprobs(NamedTuple):
+    """Results of token_logprobs: per given token, per row, and per alternative."""
+    logprob: Any
+    lse: Any
+    entropy: Any
+    top_ids: Any
+    top_logprob: Any
+    stats: Any
+
+
+@functools.lru_cache(maxsize=256)
+def token_logprobs_workspace(M: int, V: int, n_top: int = 0) -> int:
+    """Workspace bytes of token_logprobs."""
+    b = ctypes.c_size_t()
+    _check(load().flce_token_logprobs_workspace(int(M), int(V), int(n_top), ctypes.byref(b)))
+    return b.value
+
+
+def _tokens(tokens, dev, m):
+    """Check given tokens [M] or [M, n]; returns their shape and n."""
+    import torch
+    if tokens is None:
+        return (m, 0), 0
+    if tokens.dtype != torch.int64:
+        raise TypeError(f"tokens: expected torch.int64, got {tokens.dtype}")
+    if tokens.device != dev:
+        raise ValueError(f"tokens: expected a tensor on {dev}, got {tokens.device}")
+    shape = tuple(tokens.shape)
+    if len(shape) not in (1, 2) or shape[0] != m or not tokens.is_contiguous():
+        raise ValueError(f"tokens: expected {m} contiguous rows, got shape {shape}")
+    return shape, 1 if len(shape) == 1 else shape[1]
+
+
+def _contiguous(t, name, dev, dtype, shape):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def token_logprobs(logits, tokens=None, ignore_index: int = -100, scale: float = 1.0, n_top: int = 0,
+                   compute_entropy: bool = True, workspace=None, out: Optional[TokenLogprobs] = None):
+    """Log-probs of given tokens, log-sum-exp, entropy and the n_top largest alternatives of each row
+    of logits [M, V] (bf16 or fp32) under softmax(scale * logits), as a TokenLogprobs.
+
+    tokens are int64 [M] or [M, n]; logprob has their shape (0 where a token is ignore_index or
+    outside [0, V); [M, 0] without tokens).  top_ids int64 and top_logprob [M, n_top] are ordered by
+    the logits, equal ones by index; a logit of -inf is masked.  entropy is None without
+    compute_entropy, the alternatives without n_top.  stats [M, 2] is what
+    token_logprobs_backward needs of the rows.  `out` may supply the buffers."""
+    import torch
+    dev = _on_gpu(logits, "logits")
+    d, ldl = _dtype_id(logits, "logits"), _rows(logits, "logits", dev)
+    m, v = logits.shape
+    shape, n = _tokens(tokens, dev, m)
+    n_top = int(n_top)
+    f32, f = torch.float32, functools.partial(torch.empty, device=dev)
+    if out is None:
+        out = TokenLogprobs(f(shape, dtype=f32), f(m, dtype=f32), f(m, dtype=f32) if compute_entropy else None,
+                            f(m, n_top, dtype=torch.int64) if n_top > 0 else None,
+                            f(m, n_top, dtype=f32) if n_top > 0 else None, f(m, 2, dtype=f32))
+    else:
+        _contiguous(out.logprob, "logprob", dev, f32, shape)
+        _contiguous(out.lse, "lse", dev, f32, (m,))
+        _contiguous(out.stats, "stats", dev, f32, (m, 2))
+        if compute_entropy:
+            _contiguous(out.entropy, "entropy", dev, f32, (m,))
+        if n_top > 0:
+            _contiguous(out.top_ids, "top_ids", dev, torch.int64, (m, n_top))
+            _contiguous(out.top_logprob, "top_logprob", dev, f32, (m, n_top))
+    workspace = _workspace(
+        workspace, token_logprobs_workspace(m, v, n_top) if workspace is None and v else 0, dev)
+    _launch(dev, load().flce_token_logprobs, logits.data_ptr(), d, ldl, m, v, _ptr(tokens), n, ignore_index,
+            scale, n_top, out.logprob.data_ptr(), out.lse.data_ptr(),
+            _ptr(out.entropy) if compute_entropy else None, out.stats.data_ptr(), _ptr(out.top_ids),
+            _ptr(out.top_logprob), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out
+
+
+def token_logprobs_backward(logits, tokens, stats, entropy=None, top_ids=None, grad_logprob=None,
+                            grad_top=None, grad_entropy=None, grad_lse=None,
+                            ignore_index: int = -100, scale: float = 1.0, out=None):
+    """dlogits (logits' dtype) of token_logprobs, from the gradients of logprob, of top_logprob (with
+    the forward's top_ids), of entropy (with the forward's entropy) and of lse; None counts as 0.  `out` may
+    supply its buffer, and may be logits."""
+    import torch
+    dev = _on_gpu(logits, "logits")
+    d, ldl = _dtype_id(logits, "logits"), _rows(logits, "logits", dev)
+    m, v = logits.shape
+    shape, n = _tokens(tokens, dev, m)
+    f32 = torch.float32
+    _contiguous(stats, "stats", dev, f32, (m, 2))
+    if grad_logprob is not None:
+        _contiguous(grad_logprob, "grad_logprob", dev, f32, shape)
+    n_top = 0
+    if grad_top is not None:
+        if top_ids is None:
+            raise ValueError("top_ids: needed with grad_top")
+        if top_ids.dim() != 2:
+            raise ValueError(f"top_ids: expected a matrix, got {top_ids.dim()} dimensions")
+        n_top = top_ids.shape[1]
+        _contiguous(top_ids, "top_ids", dev, torch.int64, (m, n_top))
+        _contiguous(grad_top, "grad_top", dev, f32, (m, n_top))
+    if grad_entropy is not None:
+        if entropy is None:
+            raise ValueError("entropy: needed with grad_entropy")
+        _vector(entropy, "entropy", dev, f32, m)
+        _vector(grad_entropy, "grad_entropy", dev, f32, m)
+    if grad_lse is not None:
+        _vector(grad_lse, "grad_lse", dev, f32, m)
+    out, _, ldd = _result(out, "out", logits.dtype, dev, (m, v), "logits'")
+    _launch(dev, load().flce_token_logprobs_backward, logits.data_ptr(), d, ldl, m, v, _ptr(tokens), n,
+            ignore_index, scale, stats.data_ptr(), _ptr(entropy) if grad_entropy is not None else None,
+            _ptr(top_ids) if n_top else None, n_top, _ptr(grad_logprob), _ptr(grad_top) if n_top else None,
+            _ptr(grad_entropy), _ptr(grad_lse), out.data_ptr(), ldd)
+    return out
