@@ -87,8 +87,8 @@ flce_status_t check_linear(int64_t M, int64_t N, int64_t K) {
 bool is_activation(int a) { return a >= FLCE_ACT_NONE && a <= FLCE_ACT_SILU; }
 
 flce_status_t check_grid(const flce::LinearPlan& p, int64_t M, int64_t N) {
-  const int64_t tiles = (M + p.tile_m - 1) / p.tile_m * ((N + p.tile_n - 1) / p.tile_n);
-  if (tiles * p.splits > flce::kMaxWorkgroups)
+  // (half of what a launch can hold: the gradient's has two products)
+  if (flce::linear_workgroups(p, M, N) > flce::kMaxWorkgroups / 2 - (1 << 16))
     return fail(FLCE_ERR_UNSUPPORTED, "too many tiles for one launch (%lld x %lld)", (long long)M, (long long)N);
   return FLCE_OK;
 }
@@ -98,18 +98,17 @@ struct LinearBackwardLayout {
   flce::LinearPlan dx, dw;
   int64_t ldd;
   int groups;
-  size_t off_sum, off_part, total;
+  size_t off_sum, off_dx, off_dw, total;
 };
 LinearBackwardLayout linear_backward_layout(int64_t M, int64_t N, int64_t K) {
   LinearBackwardLayout L;
-  L.dx = flce::linear_plan(M, K, N, true, false);
-  L.dw = flce::linear_plan(N, K, M, false, false);
+  flce::linear_backward_plans(M, N, K, &L.dx, &L.dw);
   L.ldd = (N + 7) / 8 * 8;
   L.groups = flce::linear_slope_groups(M, N);
   L.off_sum = align_up(size_t(M) * size_t(L.ldd) * 2);
-  L.off_part = L.off_sum + align_up(size_t(L.groups) * size_t(N) * 4);
-  const size_t px = flce::linear_part_bytes(L.dx, M, K), pw = flce::linear_part_bytes(L.dw, N, K);
-  L.total = L.off_part + align_up(px > pw ? px : pw);
+  L.off_dx = L.off_sum + align_up(size_t(L.groups) * size_t(N) * 4);
+  L.off_dw = L.off_dx + align_up(flce::linear_part_bytes(L.dx, M, K));
+  L.total = L.off_dw + align_up(flce::linear_part_bytes(L.dw, N, K));
   return L;
 }
 
@@ -160,7 +159,7 @@ flce_status_t flce_linear_workspace(int64_t M, int64_t N, int64_t K, size_t* fwd
   flce_status_t st = check_linear(M, N, K);
   if (st != FLCE_OK) return st;
   if (fwd_bytes) {
-    const flce::LinearPlan p = flce::linear_plan(M, N, K, true, true);
+    const flce::LinearPlan p = flce::linear_forward_plan(M, N, K);
     *fwd_bytes = M <= flce::kLinearFewRows ? 0 : align_up(flce::linear_part_bytes(p, M, N));
   }
   if (bwd_bytes) *bwd_bytes = linear_backward_layout(M, N, K).total;
@@ -186,7 +185,7 @@ flce_status_t flce_linear_forward(const void* X, int64_t ldx, const void* W, int
   if (!is_aligned(bias, bias ? bytes_of(bias_dtype) : 1))
     return fail(FLCE_ERR_UNSUPPORTED, "bias must be naturally aligned");
   const flce::LinearProduct a{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(W), long(ldx), long(ldw),
-                              int(M), int(N), int(K), int(K), int(K), true, true};
+                              int(M), int(N), int(K), int(K), int(K)};
   flce::LinearEpilogue e{};
   e.bias = bias;
   e.bias_dtype = bias_dtype;
@@ -199,13 +198,11 @@ flce_status_t flce_linear_forward(const void* X, int64_t ldx, const void* W, int
   e.ldo = long(ldo);
   e.pre = static_cast<uint16_t*>(pre);
   e.ldp = long(ldp);
-  e.vec = N % 8 == 0 && vectors(out, out_dtype, ldo) && vectors(residual, residual_dtype, ldr) &&
-          vectors(pre, FLCE_BF16, ldp) && vectors(bias, bias_dtype, N);
   hipError_t err;
   if (M <= flce::kLinearFewRows) {
     err = flce::launch_linear_few(a, e, stream);
   } else {
-    const flce::LinearPlan plan = flce::linear_plan(M, N, K, true, true);
+    const flce::LinearPlan plan = flce::linear_forward_plan(M, N, K);
     if ((st = check_grid(plan, M, N)) != FLCE_OK) return st;
     const size_t need = flce::linear_part_bytes(plan, M, N);
     if ((st = check_workspace(workspace, workspace_bytes, need, "linear forward")) != FLCE_OK) return st;
@@ -240,7 +237,6 @@ flce_status_t flce_linear_backward(const void* dy, int dy_dtype, int64_t lddy, c
   if (dW && (st = check_grid(L.dw, N, K)) != FLCE_OK) return st;
   if ((st = check_workspace(workspace, workspace_bytes, L.total, "linear backward")) != FLCE_OK) return st;
   char* ws = static_cast<char*>(workspace);
-  float* part = reinterpret_cast<float*>(ws + L.off_part);
 
   // dy itself where it already is what the products read
   const bool as_is = !act && dy_dtype == FLCE_BF16 && N % 8 == 0 && lddy % 8 == 0 && is_aligned(dy, 16) &&
@@ -266,32 +262,29 @@ flce_status_t flce_linear_backward(const void* dy, int dy_dtype, int64_t lddy, c
     const hipError_t e = flce::launch_linear_slope(a, stream);
     if (e != hipSuccess) return hip_fail(e, "activation gradient kernel launch");
   }
-  if (dbias) {
-    const hipError_t e = flce::launch_linear_bias_sum(reinterpret_cast<const float*>(ws + L.off_sum),
-                                                      M > 0 ? L.groups : 0, int(N), dbias, bias_dtype, stream);
-    if (e != hipSuccess) return hip_fail(e, "bias gradient kernel launch");
-  }
-  flce::LinearEpilogue e{};
-  e.act = FLCE_ACT_NONE;
-  e.out_dtype = FLCE_BF16;
+  flce::LinearGradArgs g{};
+  const int64_t N8 = (N + 7) / 8 * 8;
   if (dX && M > 0) {
-    const flce::LinearProduct a{dpre, static_cast<const uint16_t*>(W), long(ldd), long(ldw), int(M), int(K),
-                                int((N + 7) / 8 * 8), int((N + 7) / 8 * 8), int(N), true, false};
-    e.out = dX;
-    e.ldo = long(lddx);
-    e.vec = vectors(dX, FLCE_BF16, lddx);
-    const hipError_t err = flce::launch_linear_product(a, L.dx, e, part, stream);
-    if (err != hipSuccess) return hip_fail(err, "input gradient kernel launch");
+    g.dx = {dpre, static_cast<const uint16_t*>(W), long(ldd), long(ldw), int(M), int(K), int(N8), int(N8), int(N)};
+    g.out_dx.out = dX;
+    g.out_dx.out_dtype = FLCE_BF16;
+    g.out_dx.ldo = long(lddx);
+    g.n_dx = int(flce::linear_workgroups(L.dx, M, K));
   }
   if (dW) {
-    const flce::LinearProduct a{dpre, static_cast<const uint16_t*>(X), long(ldd), long(ldx), int(N), int(K), int(M),
-                                int(M), int(M), false, false};
-    e.out = dW;
-    e.ldo = long(lddw);
-    e.vec = vectors(dW, FLCE_BF16, lddw);
-    const hipError_t err = flce::launch_linear_product(a, L.dw, e, part, stream);
-    if (err != hipSuccess) return hip_fail(err, "weight gradient kernel launch");
+    g.dw = {dpre, static_cast<const uint16_t*>(X), long(ldd), long(ldx), int(N), int(K), int(M), int(M), int(M)};
+    g.out_dw.out = dW;
+    g.out_dw.out_dtype = FLCE_BF16;
+    g.out_dw.ldo = long(lddw);
+    g.n_dw = int(flce::linear_workgroups(L.dw, N, K));
   }
+  g.plan_dx = L.dx;
+  g.plan_dw = L.dw;
+  g.part_dx = reinterpret_cast<float*>(ws + L.off_dx);
+  g.part_dw = reinterpret_cast<float*>(ws + L.off_dw);
+  g.bias = {reinterpret_cast<const float*>(ws + L.off_sum), M > 0 ? L.groups : 0, int(N), dbias, bias_dtype};
+  const hipError_t e = flce::launch_linear_grad(g, stream);
+  if (e != hipSuccess) return hip_fail(e, "linear gradient kernel launch");
   return ok();
 }
 
@@ -379,8 +372,7 @@ flce_status_t flce_token_logprobs(const void* logits, int dtype, int64_t ldl, in
   a.part_len = L.part_len;
   a.part_sums = static_cast<float*>(workspace);
   a.part_top = reinterpret_cast<unsigned long long*>(static_cast<char*>(workspace) + L.off_top);
-  const bool vec = V % 8 == 0 && vectors(logits, dtype, ldl);
-  const hipError_t e = flce::launch_token_logprobs(a, dtype, vec, stream);
+  const hipError_t e = flce::launch_token_logprobs(a, dtype, stream);
   if (e != hipSuccess) return hip_fail(e, "token log-prob kernel launch");
   return ok();
 }

@@ -57,7 +57,7 @@ struct TokenLogprobArgs {
 };
 // Pieces a row is split into, and the elements of each.
 void token_logprob_split(int64_t M, int64_t V, int n_top, int* parts, int* part_len);
-hipError_t launch_token_logprobs(const TokenLogprobArgs& a, int dtype, bool vec, hipStream_t s);
+hipError_t launch_token_logprobs(const TokenLogprobArgs& a, int dtype, hipStream_t s);
 
 struct TokenLogprobGradArgs {
   const void* logits;
@@ -98,19 +98,18 @@ struct LinearEpilogue {
   long ldo;
   uint16_t* pre;           // [M, N] bf16: product + bias, or nullptr
   long ldp;
-  bool vec;                // rows of whole, aligned groups of 8 in all of them
 };
 
-// D[m, n] = sum_k A(m, k) B(n, k).  An operand either has its K contiguous (rows of K), or its
-// rows (K rows of `rows` elements); either way `ld` elements lie between the rows of its memory,
-// which are 16-byte aligned.  kvalid_* is the K extent in memory.
+// D[m, n] = sum_k A(m, k) B(n, k).  An operand either has its K contiguous in memory (rows of K)
+// or its rows (K rows of M or N elements): X and W in the forward, dpre and W^T in dX, dpre^T and
+// X^T in dW.  Either way ld elements lie between the rows of its memory, which are 16-byte aligned,
+// and kvalid_* of K exist.
 struct LinearProduct {
   const uint16_t* a;
   const uint16_t* b;
   long lda, ldb;
   int M, N, K;
   int kvalid_a, kvalid_b;
-  bool a_kc, b_kc;
 };
 // Tile and K split of a product: splits > 1 leave fp32 partial products [splits][M][ldpart] in
 // the workspace, which a second kernel adds in order.
@@ -118,13 +117,34 @@ struct LinearPlan {
   int tile_m, tile_n;
   int splits, k_each;
 };
-LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, bool a_kc, bool b_kc);
+LinearPlan linear_forward_plan(int64_t M, int64_t N, int64_t K);
+void linear_backward_plans(int64_t M, int64_t N, int64_t K, LinearPlan* dx, LinearPlan* dw);
+int64_t linear_workgroups(const LinearPlan& p, int64_t M, int64_t N);
 inline int64_t linear_part_ld(int64_t N) { return (N + 7) / 8 * 8; }
 inline size_t linear_part_bytes(const LinearPlan& p, int64_t M, int64_t N) {
   return p.splits > 1 ? size_t(p.splits) * size_t(M) * size_t(linear_part_ld(N)) * 4 : 0;
 }
+// The forward's product (both operands with their K contiguous).
 hipError_t launch_linear_product(const LinearProduct& a, const LinearPlan& plan, const LinearEpilogue& e,
                                  float* part, hipStream_t s);
+
+// The gradient's products from dpre and the bias gradient from its column sums.
+struct LinearBiasSum {
+  const float* part;       // [groups][N]
+  int groups, N;
+  void* dbias;             // nullptr: not wanted
+  int dtype;
+};
+struct LinearGradArgs {
+  LinearProduct dx, dw;
+  LinearEpilogue out_dx, out_dw;
+  LinearPlan plan_dx, plan_dw;
+  float* part_dx;
+  float* part_dw;
+  int n_dx, n_dw;          // workgroups of each (0: not wanted)
+  LinearBiasSum bias;
+};
+hipError_t launch_linear_grad(LinearGradArgs a, hipStream_t s);
 
 // A few rows of X: the weights streamed past them.
 constexpr int kLinearFewRows = 8;
@@ -148,6 +168,5 @@ struct LinearSlopeArgs {
 };
 int linear_slope_groups(int64_t M, int64_t N);
 hipError_t launch_linear_slope(const LinearSlopeArgs& a, hipStream_t s);
-hipError_t launch_linear_bias_sum(const float* part, int groups, int N, void* dbias, int dtype, hipStream_t s);
 
 }  // namespace flce

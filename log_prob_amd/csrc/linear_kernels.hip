@@ -54,17 +54,25 @@ __device__ __forceinline__ float logistic(float x) {
 constexpr float TANH_SCALE = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float TANH_CUBE = 0.044715f;
 
-__device__ __forceinline__ float activate(float x, int act) {
+template <int ACT>
+__device__ __forceinline__ float activate(float x) {
+  if constexpr (ACT == kActRelu) return x < 0.f ? 0.f : x;
+  float ex;
+  if constexpr (ACT == kActGelu) return x * normal_cdf(x, ex);
+  // (1 + tanh u) / 2 is the logistic function of 2 u
+  if constexpr (ACT == kActGeluTanh) return x * logistic(TANH_SCALE * x * fmaf(TANH_CUBE * x, x, 1.f));
+  if constexpr (ACT == kActSilu) return x * logistic(x);
+  return x;
+}
+// f(integral_constant of act): the branch is the same for every lane.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f) {
   switch (act) {
-    case kActRelu: return x < 0.f ? 0.f : x;
-    case kActGelu: {
-      float ex;
-      return x * normal_cdf(x, ex);
-    }
-    // (1 + tanh u) / 2 is the logistic function of 2 u
-    case kActGeluTanh: return x * logistic(TANH_SCALE * x * fmaf(TANH_CUBE * x, x, 1.f));
-    case kActSilu: return x * logistic(x);
-    default: return x;
+    case kActRelu: f(std::integral_constant<int, kActRelu>()); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>()); break;
+    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>()); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>()); break;
+    default: f(std::integral_constant<int, kActNone>()); break;
   }
 }
 __device__ __forceinline__ float slope(float x, int act) {
@@ -88,114 +96,212 @@ __device__ __forceinline__ float slope(float x, int act) {
     default: return 1.f;
   }
 }
-// (the branch is the same for every lane)
 __device__ __forceinline__ void activate8(float (&v)[8], int act) {
-  if (act == kActNone) return;
+  with_act(act, [&](auto a) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = activate(v[i], act);
+    for (int i = 0; i < 8; ++i) v[i] = activate<decltype(a)::value>(v[i]);
+  });
 }
 
 // ---------------------------------------------------------------------------
 // The epilogue of 8 consecutive columns of a row.
-template <bool VEC>
-__device__ __forceinline__ void load_any(const void* p, int dtype, long at, int col, int N, float (&v)[8]) {
-  if (dtype == kF32) load8<F32, VEC>(static_cast<const float*>(p) + at, col, N, v);
-  else load8<Bf16, VEC>(static_cast<const uint16_t*>(p) + at, col, N, v);
+
+// 8 elements of either type, as they come from memory.
+struct AnyChunk {
+  u32x4_t u[2];
+  __device__ __forceinline__ void load(const void* p, int dtype, long at, int col, int cols) {
+    if (dtype == kF32) {
+      Chunk8<F32, false> c;
+      c.load(static_cast<const float*>(p) + at, col, cols);
+      u[0] = c.u[0];
+      u[1] = c.u[1];
+    } else {
+      Chunk8<Bf16, false> c;
+      c.load(static_cast<const uint16_t*>(p) + at, col, cols);
+      u[0] = c.u[0];
+    }
+  }
+  __device__ __forceinline__ void value(int dtype, int col, int cols, float (&v)[8]) const {
+    if (dtype == kF32) {
+      const Chunk8<F32, false> c{{u[0], u[1]}};
+      c.value(col, cols, v);
+    } else {
+      const Chunk8<Bf16, false> c{{u[0]}};
+      c.value(col, cols, v);
+    }
+  }
+};
+__device__ __forceinline__ void add8(float (&v)[8], const void* p, int dtype, long at, int col, int cols) {
+  AnyChunk c;
+  c.load(p, dtype, at, col, cols);
+  float b[8];
+  c.value(dtype, col, cols, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] += b[i];
 }
-template <bool VEC>
+__device__ __forceinline__ void store_any(void* p, int dtype, long at, int col, int cols, const float (&v)[8]) {
+  if (dtype == kF32) store8<F32, false>(static_cast<float*>(p) + at, col, cols, v);
+  else store8<Bf16, false>(static_cast<uint16_t*>(p) + at, col, cols, v);
+}
 __device__ __forceinline__ void finish8(const LinearEpilogue& e, long m, int col, int N, float (&v)[8]) {
-  if (e.bias) {
-    float b[8];
-    load_any<VEC>(e.bias, e.bias_dtype, 0, col, N, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
-  if (e.pre) store8<Bf16, VEC>(e.pre + m * e.ldp, col, N, v);
+  if (e.bias) add8(v, e.bias, e.bias_dtype, 0, col, N);
+  if (e.pre) store8<Bf16, false>(e.pre + m * e.ldp, col, N, v);
   activate8(v, e.act);
-  if (e.residual) {
-    float r[8];
-    load_any<VEC>(e.residual, e.residual_dtype, m * e.ldr, col, N, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += r[i];
-  }
-  if (e.out_dtype == kF32) store8<F32, VEC>(static_cast<float*>(e.out) + m * e.ldo, col, N, v);
-  else store8<Bf16, VEC>(static_cast<uint16_t*>(e.out) + m * e.ldo, col, N, v);
+  if (e.residual) add8(v, e.residual, e.residual_dtype, m * e.ldr, col, N);
+  store_any(e.out, e.out_dtype, m * e.ldo, col, N, v);
 }
 
 // A wave's accumulators (WM x WN of the tile at (m0, n0)) to the epilogue, 64 rows at a time
 // through its own slice of LDS: row r, column c at float r WN + (c ^ 32 ((r >> 2) & 1)), so that
 // the two half-waves of a write (rows r and r + 4) meet different banks where rows are 64 columns
-// or more.  With `part` the fp32 values go there as they are.
-template <class S, bool VEC>
+// or more.  A lane then has the same 8 columns of every row, and goes over the slice twice: bias,
+// pre and activation in place, then the residual and the store.  The residual's loads go out half a
+// slice at once, the first half ahead of everything else.
+template <class S>
+struct Slice {
+  static constexpr int WN = S::WN, ROWS = 64, BLOCKS = ROWS / 32, COLS8 = WN / 8, PER = 64 / COLS8;
+  static constexpr int STEPS = ROWS / PER, HALF = STEPS / 2;
+  static_assert(S::MB % BLOCKS == 0 && S::NWAVES * ROWS * WN * 4 <= S::PIPE_BYTES, "slices");
+  float* sl;
+  int lane, row0;  // the slice's first row in D
+  __device__ __forceinline__ int row(int it) const { return PER * it + lane / COLS8; }
+  __device__ __forceinline__ float* at(int it) const {
+    const int r = row(it);
+    return sl + r * WN + ((8 * (lane % COLS8)) ^ (WN >= 64 ? ((r >> 2) & 1) << 5 : 0));
+  }
+  __device__ __forceinline__ void get(int it, float (&v)[8]) const {
+    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(at(it)), up = *reinterpret_cast<const f32x4_t*>(at(it) + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = lo[i];
+      v[4 + i] = up[i];
+    }
+  }
+  __device__ __forceinline__ void put(int it, const float (&v)[8]) const {
+    *reinterpret_cast<f32x4_t*>(at(it)) = f32x4_t{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4_t*>(at(it) + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+  }
+};
+
+// FULL: with bias, pre, activation and residual, if any; otherwise (the gradients' products) the
+// values go out as they are.  With `part` (a share of a split K) they go there in fp32.
+template <class S, bool FULL>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::MB][S::NB], char* smem, const LinearEpilogue& e,
                                            float* part, long ldpart, int M, int N, int m0, int n0) {
-  constexpr int WN = S::WN, ROWS = 64, BLOCKS = ROWS / 32, COLS8 = WN / 8, PER = 64 / COLS8;
-  static_assert(S::MB % BLOCKS == 0 && S::NWAVES * ROWS * WN * 4 <= S::PIPE_BYTES, "slices");
+  using L = Slice<S>;
+  constexpr int WN = S::WN, HALF = L::HALF;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  float* sl = reinterpret_cast<float*>(smem) + wave * ROWS * WN;
+  L sl;
+  sl.sl = reinterpret_cast<float*>(smem) + wave * L::ROWS * WN;
+  sl.lane = lane;
   const int lc = lane & 31, hi = lane >> 5, sw = WN >= 64 ? hi << 5 : 0;
-  const int row0 = m0 + (wave / S::WAVES_N) * S::WM, col0 = n0 + (wave % S::WAVES_N) * WN;
-  const int col = col0 + 8 * (lane % COLS8);
+  const int col = n0 + (wave % S::WAVES_N) * WN + 8 * (lane % L::COLS8);
+  const bool first_pass = FULL && !part && (e.bias || e.pre || e.act != kActNone);
+  const bool residual = FULL && !part && e.residual;
+  void* const to = part ? static_cast<void*>(part) : e.out;
+  const int dtype = part ? kF32 : e.out_dtype;
+  const long ld = part ? ldpart : e.ldo;
+  float b[8];
 #pragma unroll
-  for (int s = 0; s < S::MB / BLOCKS; ++s) {
+  for (int i = 0; i < 8; ++i) b[i] = 0.f;
+  if (first_pass && e.bias) add8(b, e.bias, e.bias_dtype, 0, col, N);
+  auto slice = [&](auto number) {
+    constexpr int s = decltype(number)::value;
+    sl.row0 = m0 + (wave / S::WAVES_N) * S::WM + L::ROWS * s;
+    AnyChunk res[HALF];
+    auto load_residual = [&](int it) {
+      const int m = sl.row0 + sl.row(it);
+      res[it % HALF].load(e.residual, e.residual_dtype, (long)m * e.ldr, col, m < M ? N : 0);
+    };
+    if (residual) {
 #pragma unroll
-    for (int mi = 0; mi < BLOCKS; ++mi)
+      for (int i = 0; i < HALF; ++i) load_residual(i);
+    }
+#pragma unroll
+    for (int mi = 0; mi < L::BLOCKS; ++mi)
 #pragma unroll
       for (int nb = 0; nb < S::NB; ++nb)
 #pragma unroll
         for (int q = 0; q < 16; ++q)
-          sl[(32 * mi + acc_row(lane, q)) * WN + ((32 * nb + lc) ^ sw)] = acc_read(acc[BLOCKS * s + mi][nb][q]);
+          sl.sl[(32 * mi + acc_row(lane, q)) * WN + ((32 * nb + lc) ^ sw)] = acc_read(acc[L::BLOCKS * s + mi][nb][q]);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    // (not unrolled further: the unrolled block would be too long for the loop over s to be)
-#pragma unroll 2
-    for (int it = 0; it < ROWS / PER; ++it) {
-      const int r = PER * it + lane / COLS8, m = row0 + ROWS * s + r;
-      const int c = (8 * (lane % COLS8)) ^ (WN >= 64 ? ((r >> 2) & 1) << 5 : 0);
-      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(sl + r * WN + c);
-      const f32x4_t up = *reinterpret_cast<const f32x4_t*>(sl + r * WN + c + 4);
-      if (m < M && col < N) {
-        if (part) {
-          float* to = part + (long)m * ldpart + col;
-          *reinterpret_cast<f32x4_t*>(to) = lo;
-          *reinterpret_cast<f32x4_t*>(to + 4) = up;
-        } else {
-          float v[8] = {lo[0], lo[1], lo[2], lo[3], up[0], up[1], up[2], up[3]};
-          finish8<VEC>(e, m, col, N, v);
+    if (first_pass)
+      with_act(e.act, [&](auto a) {
+#pragma unroll 4
+        for (int it = 0; it < L::STEPS; ++it) {
+          const int m = sl.row0 + sl.row(it);
+          float v[8];
+          sl.get(it, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += b[i];
+          if (e.pre && m < M) store8<Bf16, false>(e.pre + (long)m * e.ldp, col, N, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = activate<decltype(a)::value>(v[i]);
+          sl.put(it, v);
         }
+      });
+    if (residual) {
+#pragma unroll
+      for (int it = 0; it < L::STEPS; ++it) {
+        const int m = sl.row0 + sl.row(it);
+        float v[8], r[8];
+        sl.get(it, v);
+        res[it % HALF].value(e.residual_dtype, col, N, r);
+        if (it < HALF) load_residual(it + HALF);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += r[j];
+        if (m < M) store_any(to, dtype, (long)m * ld, col, N, v);
+      }
+    } else {
+#pragma unroll 4
+      for (int it = 0; it < L::STEPS; ++it) {
+        const int m = sl.row0 + sl.row(it);
+        float v[8];
+        sl.get(it, v);
+        if (m < M) store_any(to, dtype, (long)m * ld, col, N, v);
       }
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  }
+  };
+  // (one after the other by name: a loop this long is not unrolled, and accumulators indexed at
+  // run time would go to memory)
+  slice(std::integral_constant<int, 0>());
+  if constexpr (S::MB / L::BLOCKS == 2) slice(std::integral_constant<int, 1>());
+  static_assert(S::MB / L::BLOCKS <= 2, "slices");
 }
 
-// A tile of TM x TN over a share of K.  Workgroups of one XCD take neighbouring tiles of the same
-// share (groups of 8 tile rows).
-template <class S, bool A_KC, bool B_KC, bool VEC>
-__global__ __launch_bounds__(S::NTHREADS, S::WAVES_PER_EU) void linear_tile_kernel(LinearProduct p,
-                                                                                  LinearEpilogue e, float* part,
-                                                                                  long ldpart, int n_mt, int n_nt,
-                                                                                  int splits, int k_each) {
-  __shared__ __attribute__((aligned(1024))) char smem[S::PIPE_BYTES];
-  const int tiles = n_mt * n_nt, per = (int)gridDim.x >> 3;
-  int L = blockIdx.x;
-  if (L < (per << 3)) L = (L & 7) * per + (L >> 3);
+// Workgroup `id` of n_mt x n_nt tiles times `splits` shares of K.  Workgroups of one XCD take
+// neighbouring tiles of the same share (groups of 8 tile rows).
+template <class S, bool A_KC, bool B_KC>
+__device__ __forceinline__ void run_tile(char* smem, int id, const LinearProduct& p, const LinearEpilogue& e,
+                                         float* part, const LinearPlan& plan) {
+  const int n_mt = (p.M + S::TM - 1) / S::TM, n_nt = (p.N + S::TN - 1) / S::TN;
+  const int tiles = n_mt * n_nt, per = tiles * plan.splits >> 3;
+  const int L = id < (per << 3) ? (id & 7) * per + (id >> 3) : id;
   const int split = L / tiles;
   int mt, nt;
   group_coords(L - split * tiles, n_mt, n_nt, 8, mt, nt);
   const int m0 = mt * S::TM, n0 = nt * S::TN;
-  const int k0 = split * k_each, k1 = min(p.K, k0 + k_each);
+  const int k0 = split * plan.k_each, k1 = min(p.K, k0 + plan.k_each);
   const TileSrc A{A_KC ? p.a + (long)m0 * p.lda + k0 : p.a + (long)k0 * p.lda + m0, p.lda, p.M - m0,
                   min(p.kvalid_a, k1) - k0, 0};
   const TileSrc B{B_KC ? p.b + (long)n0 * p.ldb + k0 : p.b + (long)k0 * p.ldb + n0, p.ldb, p.N - n0,
                   min(p.kvalid_b, k1) - k0, 0};
   f32x16 acc[S::MB][S::NB];
   mainloop<S, A_KC, B_KC>(acc, smem, A, B, k1 - k0);
-  float* mine = splits > 1 ? part + (long)split * p.M * ldpart : nullptr;
-  store_tile<S, VEC>(acc, smem, e, mine, ldpart, p.M, p.N, m0, n0);
+  const long ldpart = (p.N + 7) / 8 * 8;
+  float* mine = plan.splits > 1 ? part + (long)split * p.M * ldpart : nullptr;
+  store_tile<S, A_KC && B_KC>(acc, smem, e, mine, ldpart, p.M, p.N, m0, n0);
+}
+
+template <class S>
+__global__ __launch_bounds__(S::NTHREADS, S::WAVES_PER_EU) void linear_tile_kernel(LinearProduct p, LinearEpilogue e,
+                                                                                  float* part, LinearPlan plan) {
+  __shared__ __attribute__((aligned(1024))) char smem[S::PIPE_BYTES];
+  run_tile<S, true, true>(smem, blockIdx.x, p, e, part, plan);
 }
 
 // The partial products of a split K, added in order, and the epilogue: 8 columns a thread.
-template <bool VEC>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinearEpilogue e, const float* part, long ldpart,
                                                           int splits, long M, int N) {
   const int chunks = (N + 7) / 8;
@@ -217,23 +323,25 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearEpilogue e, cons
         v[4 + j] += up[j];
       }
     }
-    finish8<VEC>(e, m, col, N, v);
+    finish8(e, m, col, N, v);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Up to MT <= 8 rows of X: W is read once, and bounds the call.  A wave takes R rows of W, its
-// lanes 8 consecutive K each (1 KiB of a row at once), two steps of loads ahead; X lies in LDS,
-// at most 64 KiB of it at a time, and is read from there once for the R rows.  Products of a
-// pair of bf16 go through v_dot2: two multiplications and no unpacking (with unpacking and
-// fp32 fused multiply-adds 8 rows of X would take more time than the loads of W).
-constexpr int FEW_R = 4, FEW_LDS = 64 * 1024;
+// lanes 8 consecutive K each (1 KiB of a row at once), in batches of U loads a row; the next
+// batch is in flight under the work on this one.  X lies in LDS, at most 64 KiB of it at a time,
+// staged under the first batch, and is read from there once for the R rows.  Products of a pair of
+// bf16 go through v_dot2: two multiplications and no unpacking (with unpacking and fp32 fused
+// multiply-adds 8 rows of X would take more time than the loads of W).
+constexpr int FEW_LDS = 64 * 1024;
+constexpr int few_rows(int mt) { return mt <= 2 ? 2 : 4; }
 typedef __bf16 bf16x2_v __attribute__((ext_vector_type(2)));
 
 template <int MT>
 __global__ __launch_bounds__(256) void linear_few_kernel(LinearProduct p, LinearEpilogue e, int k_stage) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  constexpr int R = FEW_R, NVAL = R * MT;
+  constexpr int R = few_rows(MT), U = 4 / R, NVAL = R * MT, BATCH = 512 * U;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const u32x4_t zero = {0u, 0u, 0u, 0u};
   u32x4_t* xs = reinterpret_cast<u32x4_t*>(smem);  // [MT][k_stage / 8]
@@ -246,48 +354,53 @@ __global__ __launch_bounds__(256) void linear_few_kernel(LinearProduct p, Linear
     for (int i = 0; i < NVAL; ++i) acc[i] = 0.f;
     for (int ks = 0; ks < p.K; ks += k_stage) {
       const int len = min(k_stage, p.K - ks);
+      const uint16_t* w[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) w[r] = p.b + (long)min(n0 + r, p.N - 1) * p.ldb + ks + 8 * lane;
+      u32x4_t wv[2][U][R];
+      auto load = [&](int b, int k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            wv[b][u][r] = k0 + 512 * u + 8 * lane < len
+                              ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(w[r] + k0 + 512 * u))
+                              : zero;
+      };
+      auto use = [&](int b, int k0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int k = k0 + 512 * u + 8 * lane;
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const u32x4_t x = k < len ? xs[m * ld8 + k / 8] : zero;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                // (values of their own: a cast of a vector's element takes the vector's first)
+                const uint32_t wi = wv[b][u][r][i], xi = x[i];
+                acc[r * MT + m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_v, wi),
+                                                                  __builtin_bit_cast(bf16x2_v, xi),
+                                                                  acc[r * MT + m], false);
+              }
+          }
+        }
+      };
+      load(0, 0);
       if (!staged) {
         __syncthreads();
-        for (int i = threadIdx.x; i < MT * (len / 8); i += 256) {
-          const int m = i / (len / 8), c = i - m * (len / 8);
-          xs[m * ld8 + c] = m < p.M ? *reinterpret_cast<const u32x4_t*>(p.a + m * p.lda + ks + 8 * c) : zero;
-        }
+        for (int m = 0; m < MT; ++m)
+          for (int c = threadIdx.x; c < len / 8; c += 256)
+            xs[m * ld8 + c] = m < p.M ? *reinterpret_cast<const u32x4_t*>(p.a + m * p.lda + ks + 8 * c) : zero;
         __syncthreads();
         staged = k_stage >= p.K;
       }
-      const uint16_t* w[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) w[r] = p.b + (long)min(n0 + r, p.N - 1) * p.ldb + ks;
-      u32x4_t wv[2][R];
-      auto load = [&](int b, int k) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          wv[b][r] = k < len ? __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(w[r] + k)) : zero;
-      };
-      auto use = [&](int b, int k) {
-        const int c = min(k, len - 8) / 8;  // (past the end W is zero, and X a number or not as it was)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const u32x4_t x = k < len ? xs[m * ld8 + c] : zero;
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // (values of their own: a cast of a vector's element takes the vector's first)
-              const uint32_t wi = wv[b][r][i], xi = x[i];
-              acc[r * MT + m] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_v, wi),
-                                                                __builtin_bit_cast(bf16x2_v, xi),
-                                                                acc[r * MT + m], false);
-            }
-        }
-      };
-      load(0, 8 * lane);
-      load(1, 8 * lane + 512);
-      for (int k = 0; k < len; k += 1024) {
-        use(0, k + 8 * lane);
-        load(0, k + 1024 + 8 * lane);
-        use(1, k + 512 + 8 * lane);
-        load(1, k + 1536 + 8 * lane);
+      for (int k = 0; k < len; k += 2 * BATCH) {
+        load(1, k + BATCH);
+        use(0, k);
+        load(0, k + 2 * BATCH);
+        use(1, k + BATCH);
       }
     }
     // the sums over the lanes: each exchange halves the values a lane holds, so that in the end
@@ -312,7 +425,7 @@ __global__ __launch_bounds__(256) void linear_few_kernel(LinearProduct p, Linear
         v += e.bias_dtype == kF32 ? static_cast<const float*>(e.bias)[n]
                                   : Bf16::to_f32(static_cast<const uint16_t*>(e.bias)[n]);
       if (e.pre) e.pre[m * e.ldp + n] = Bf16::from_f32(v);
-      v = activate(v, e.act);
+      with_act(e.act, [&](auto a) { v = activate<decltype(a)::value>(v); });
       if (e.residual)
         v += e.residual_dtype == kF32 ? static_cast<const float*>(e.residual)[m * e.ldr + n]
                                       : Bf16::to_f32(static_cast<const uint16_t*>(e.residual)[m * e.ldr + n]);
@@ -382,92 +495,165 @@ __global__ __launch_bounds__(256) void linear_slope_kernel(LinearSlopeArgs p) {
 }
 
 // The groups' column sums added in order: 32 columns a workgroup, 8 shares of the groups.
-__global__ __launch_bounds__(256) void linear_bias_sum_kernel(const float* part, int groups, int N, void* dbias,
-                                                              int dtype) {
-  __shared__ float red[8][32];
-  const int c = threadIdx.x & 31, sl = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
+__device__ __forceinline__ void bias_sum(char* smem, int id, const LinearBiasSum& b) {
+  float(*red)[32] = reinterpret_cast<float(*)[32]>(smem);
+  const int c = threadIdx.x & 31, sl = threadIdx.x >> 5, col = id * 32 + c;
   float s = 0.f;
-  if (col < N)
-    for (int g = sl; g < groups; g += 8) s += part[(long)g * N + col];
+  if (col < b.N) {
+#pragma unroll 4
+    for (int g = sl; g < b.groups; g += 8) s += b.part[(long)g * b.N + col];
+  }
   red[sl][c] = s;
   __syncthreads();
-  if (sl == 0 && col < N) {
+  if (sl == 0 && col < b.N) {
 #pragma unroll
     for (int k = 1; k < 8; ++k) s += red[k][c];
-    if (dtype == kF32) static_cast<float*>(dbias)[col] = s;
-    else static_cast<uint16_t*>(dbias)[col] = Bf16::from_f32(s);
+    if (b.dtype == kF32) static_cast<float*>(b.dbias)[col] = s;
+    else static_cast<uint16_t*>(b.dbias)[col] = Bf16::from_f32(s);
   }
+}
+
+// The whole gradient after dpre in one launch: the tiles of dX, those of dW and the bias sums,
+// none of which depends on another (at 513 x 1000 x 2048, where neither product fills the chip,
+// one after the other they took 31 us).
+template <class SX, class SW>
+__global__ __launch_bounds__(256, SX::WAVES_PER_EU) void linear_grad_kernel(LinearGradArgs p) {
+  constexpr int LDS = SX::PIPE_BYTES > SW::PIPE_BYTES ? SX::PIPE_BYTES : SW::PIPE_BYTES;
+  static_assert(SX::NTHREADS == 256 && SW::NTHREADS == 256 && SX::WAVES_PER_EU == SW::WAVES_PER_EU, "one launch");
+  __shared__ __attribute__((aligned(1024))) char smem[LDS];
+  int id = blockIdx.x;
+  if (id < p.n_dw) {
+    run_tile<SW, false, false>(smem, id, p.dw, p.out_dw, p.part_dw, p.plan_dw);
+    return;
+  }
+  id -= p.n_dw;
+  if (id < p.n_dx) {
+    run_tile<SX, true, false>(smem, id, p.dx, p.out_dx, p.part_dx, p.plan_dx);
+    return;
+  }
+  bias_sum(smem, id - p.n_dx, p.bias);
 }
 
 // ---------------------------------------------------------------------------
 using Tile128 = Shape<128, 128, 64, 2, 2>;
 using Tile64 = Shape<64, 128, 64, 2, 2, 1, 4>;
 
-template <class S, bool A_KC, bool B_KC>
-void run_tiles(const LinearProduct& p, const LinearPlan& plan, const LinearEpilogue& e, float* part, hipStream_t s) {
-  const int n_mt = (p.M + S::TM - 1) / S::TM, n_nt = (p.N + S::TN - 1) / S::TN;
-  const unsigned grid = (unsigned)n_mt * (unsigned)n_nt * (unsigned)plan.splits;
-  const long ldpart = linear_part_ld(p.N);
-  if (e.vec)
-    linear_tile_kernel<S, A_KC, B_KC, true><<<grid, S::NTHREADS, 0, s>>>(p, e, part, ldpart, n_mt, n_nt, plan.splits,
-                                                                         plan.k_each);
-  else
-    linear_tile_kernel<S, A_KC, B_KC, false><<<grid, S::NTHREADS, 0, s>>>(p, e, part, ldpart, n_mt, n_nt,
-                                                                          plan.splits, plan.k_each);
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int tiles_of(const LinearPlan& p, int64_t M, int64_t N) { return int(cdiv(M, p.tile_m) * cdiv(N, p.tile_n)); }
+
+// A plan's time in us.  Workgroups go to the 256 compute units in turn, `resident` at once.  A step
+// of 64 K takes (measured at K = 4096, the tiles of one, two and three a unit): 64 x 128 0.52,
+// 0.64, 0.80 us; 128 x 128 0.60, 0.95; 256 x 256 1.05 with few units busy and 1.65 with all of them
+// (the clock).  A launch adds 3, a split a second launch and its partial products there and back
+// at the copy rate, which also bounds the operands.  E.g. (us; tile/splits):
+//   64 x 4096 x 4096     64/8 14.7, 128/8 15.4, 256/8 22, 64/1 35
+//   512 x 4096 x 4096    64/2 31, 128/2 32, 64/1 36, 256/4 40, 128/1 40
+//   1024 x 4096 x 4096   64/1 42, 128/1 43, 256/4 54, 256/1 69
+//   2048 x 4096 x 4096   128/1 62, 256/1 74, 64/1 87
+//   4096 x 4096 x 4096   256/1 106, 128/1 121, 64/1 153
+double plan_time(const LinearPlan& p, int64_t M, int64_t N, int64_t K) {
+  const int64_t n = int64_t(tiles_of(p, M, N)) * p.splits;
+  const double steps = double(cdiv(p.k_each, 64));
+  const int resident = p.tile_m == 256 ? 1 : p.tile_m == 128 ? 2 : 3;
+  const double full = double(n) / 256 < 1 ? double(n) / 256 : 1;
+  auto step = [&](int r) {
+    if (r == 0) return 0.0;
+    if (p.tile_m == 256) return 1.05 + 0.6 * full * full;
+    if (p.tile_m == 128) return r == 1 ? 0.60 : 0.95;
+    return r == 1 ? 0.54 : r == 2 ? 0.64 : 0.80;
+  };
+  const int64_t load = cdiv(n, 256);
+  double t = steps * (double(load / resident) * step(resident) + step(int(load % resident))) + 3;
+  const double bytes = 2.0 * (double(M) * K + double(N) * K) / 5.0e6;
+  if (t < bytes) t = bytes;
+  if (p.splits > 1) t += 4.5 + 8.0 * p.splits * double(M) * double(N) / 5.0e6;
+  return t;
 }
-template <bool A_KC, bool B_KC>
-void run_plan(const LinearProduct& p, const LinearPlan& plan, const LinearEpilogue& e, float* part, hipStream_t s) {
-  if (plan.tile_m == 256) {
-    run_tiles<BigShape, A_KC, B_KC>(p, plan, e, part, s);
-  } else if (plan.tile_m == 128) {
-    run_tiles<Tile128, A_KC, B_KC>(p, plan, e, part, s);
-  } else if constexpr (A_KC) {
-    run_tiles<Tile64, A_KC, B_KC>(p, plan, e, part, s);
-  }
+
+LinearPlan plan_of(int tile, int64_t splits, int64_t K) {
+  LinearPlan p{};
+  p.tile_m = tile;
+  p.tile_n = tile == 64 ? 128 : tile;
+  const int64_t k = K > 0 ? K : 1;
+  p.k_each = int(cdiv(cdiv(k, splits), 64) * 64);
+  p.splits = int(cdiv(k, p.k_each));
+  return p;
+}
+// The quickest plan among the tiles from `least` to `most`.
+LinearPlan best_plan(int64_t M, int64_t N, int64_t K, int least, int most, double* time) {
+  LinearPlan best{};
+  *time = 1e30;
+  for (int tile = least; tile <= most; tile *= 2)
+    for (int64_t splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+      if (splits > 1 && K / splits < 128) break;
+      const LinearPlan p = plan_of(tile, splits, K);
+      const double t = plan_time(p, M, N, K);
+      if (t < *time) {
+        *time = t;
+        best = p;
+      }
+    }
+  return best;
+}
+
+hipError_t join(const LinearProduct& p, const LinearPlan& plan, const LinearEpilogue& e, const float* part,
+                hipStream_t s) {
+  const long total = (long)p.M * ((p.N + 7) / 8), need = (total + 255) / 256;
+  const unsigned grid = (unsigned)(need < 4096 ? need : 4096);
+  linear_join_kernel<<<grid, 256, 0, s>>>(e, part, linear_part_ld(p.N), plan.splits, p.M, p.N);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, bool a_kc, bool b_kc) {
-  (void)b_kc;
-  auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  LinearPlan p{};
-  const int64_t big = cdiv(M, 256) * cdiv(N, 256);
-  if (big >= 192) p.tile_m = p.tile_n = 256;
-  else if (M <= 64 && a_kc) p.tile_m = 64, p.tile_n = 128;
-  else p.tile_m = p.tile_n = 128;
-  const int64_t tiles = cdiv(M, p.tile_m) * cdiv(N, p.tile_n);
-  int64_t splits = 1;
-  if (p.tile_m < 256 && tiles > 0) {
-    splits = 512 / tiles;
-    if (splits > K / 512) splits = K / 512;
-    if (splits < 1) splits = 1;
-  }
-  p.k_each = int(cdiv(cdiv(K > 0 ? K : 1, splits), 64) * 64);
-  p.splits = int(cdiv(K > 0 ? K : 1, p.k_each));
-  return p;
+LinearPlan linear_forward_plan(int64_t M, int64_t N, int64_t K) {
+  double t;
+  return best_plan(M, N, K, 64, 256, &t);
+}
+
+void linear_backward_plans(int64_t M, int64_t N, int64_t K, LinearPlan* dx, LinearPlan* dw) {
+  // both run in one launch: large tiles for both, or small ones (dW's operands are read by
+  // columns, which takes tiles of 128 at least)
+  double big_x, big_w, small_x, small_w;
+  const LinearPlan bx = best_plan(M, K, N, 256, 256, &big_x), bw = best_plan(N, K, M, 256, 256, &big_w);
+  const LinearPlan sx = best_plan(M, K, N, 64, 128, &small_x), sw = best_plan(N, K, M, 128, 128, &small_w);
+  const bool big = big_x + big_w < small_x + small_w;
+  *dx = big ? bx : sx;
+  *dw = big ? bw : sw;
+}
+
+int64_t linear_workgroups(const LinearPlan& p, int64_t M, int64_t N) {
+  return cdiv(M, p.tile_m) * cdiv(N, p.tile_n) * p.splits;
 }
 
 hipError_t launch_linear_product(const LinearProduct& p, const LinearPlan& plan, const LinearEpilogue& e, float* part,
                                  hipStream_t s) {
-  if (p.a_kc && p.b_kc) run_plan<true, true>(p, plan, e, part, s);
-  else if (p.a_kc) run_plan<true, false>(p, plan, e, part, s);
-  else run_plan<false, false>(p, plan, e, part, s);
+  const unsigned grid = (unsigned)linear_workgroups(plan, p.M, p.N);
+  if (plan.tile_m == 256) linear_tile_kernel<BigShape><<<grid, BigShape::NTHREADS, 0, s>>>(p, e, part, plan);
+  else if (plan.tile_m == 128) linear_tile_kernel<Tile128><<<grid, Tile128::NTHREADS, 0, s>>>(p, e, part, plan);
+  else linear_tile_kernel<Tile64><<<grid, Tile64::NTHREADS, 0, s>>>(p, e, part, plan);
+  const hipError_t err = hipGetLastError();
+  return err != hipSuccess || plan.splits == 1 ? err : join(p, plan, e, part, s);
+}
+
+hipError_t launch_linear_grad(LinearGradArgs a, hipStream_t s) {
+  const unsigned bias = a.bias.dbias ? (unsigned)((a.bias.N + 31) / 32) : 0u;
+  const unsigned grid = (unsigned)a.n_dx + (unsigned)a.n_dw + bias;
+  if (grid == 0) return hipSuccess;
+  if (a.plan_dw.tile_m == 256) linear_grad_kernel<BigShape, BigShape><<<grid, 256, 0, s>>>(a);
+  else if (a.plan_dx.tile_m == 128) linear_grad_kernel<Tile128, Tile128><<<grid, 256, 0, s>>>(a);
+  else linear_grad_kernel<Tile64, Tile128><<<grid, 256, 0, s>>>(a);
   hipError_t err = hipGetLastError();
-  if (err != hipSuccess || plan.splits == 1) return err;
-  const long total = (long)p.M * ((p.N + 7) / 8), need = (total + 255) / 256;
-  const unsigned grid = (unsigned)(need < 4096 ? need : 4096);
-  const long ldpart = linear_part_ld(p.N);
-  if (e.vec) linear_join_kernel<true><<<grid, 256, 0, s>>>(e, part, ldpart, plan.splits, p.M, p.N);
-  else linear_join_kernel<false><<<grid, 256, 0, s>>>(e, part, ldpart, plan.splits, p.M, p.N);
-  return hipGetLastError();
+  if (err == hipSuccess && a.n_dx && a.plan_dx.splits > 1) err = join(a.dx, a.plan_dx, a.out_dx, a.part_dx, s);
+  if (err == hipSuccess && a.n_dw && a.plan_dw.splits > 1) err = join(a.dw, a.plan_dw, a.out_dw, a.part_dw, s);
+  return err;
 }
 
 hipError_t launch_linear_few(const LinearProduct& p, const LinearEpilogue& e, hipStream_t s) {
   const int MT = p.M <= 1 ? 1 : p.M <= 2 ? 2 : p.M <= 4 ? 4 : 8;
   const int most = FEW_LDS / (2 * MT), k_stage = p.K < most ? p.K : most;
   const size_t lds = size_t(MT) * size_t(k_stage) * 2;
-  const int groups = (p.N + 4 * FEW_R - 1) / (4 * FEW_R);
+  const int per = 4 * few_rows(MT), groups = (p.N + per - 1) / per;
   const unsigned grid = (unsigned)(groups < 1024 ? groups : 1024);
   if (MT == 1) linear_few_kernel<1><<<grid, 256, lds, s>>>(p, e, k_stage);
   else if (MT == 2) linear_few_kernel<2><<<grid, 256, lds, s>>>(p, e, k_stage);
@@ -493,11 +679,6 @@ hipError_t launch_linear_slope(const LinearSlopeArgs& a, hipStream_t s) {
     if (a.vec) linear_slope_kernel<Bf16, true><<<grid, 256, 0, s>>>(a);
     else linear_slope_kernel<Bf16, false><<<grid, 256, 0, s>>>(a);
   }
-  return hipGetLastError();
-}
-
-hipError_t launch_linear_bias_sum(const float* part, int groups, int N, void* dbias, int dtype, hipStream_t s) {
-  linear_bias_sum_kernel<<<(unsigned)((N + 31) / 32), 256, 0, s>>>(part, groups, N, dbias, dtype);
   return hipGetLastError();
 }
 

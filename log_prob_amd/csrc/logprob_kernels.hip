@@ -286,7 +286,91 @@ __device__ __forceinline__ void finish_row(const TokenLogprobArgs& p, long row, 
   }
 }
 
-template <class TX, bool VEC, bool ENT, bool TOP>
+// 8 consecutive logits as they lie in memory, at any alignment of an element.
+template <class TX>
+struct Raw8 {
+  static constexpr bool HALF = sizeof(typename TX::mem) == 2;
+  static constexpr int N = HALF ? 1 : 2;
+  u32x4_t u[N];
+  __device__ __forceinline__ void load(const typename TX::mem* x) {
+    if constexpr (HALF) {
+      u[0] = *reinterpret_cast<const u32x4_a2*>(x);
+    } else {
+      u[0] = *reinterpret_cast<const u32x4_a4*>(x);
+      u[1] = *reinterpret_cast<const u32x4_a4*>(x + 4);
+    }
+  }
+  // The first n of them, then -inf.
+  __device__ __forceinline__ void load_part(const typename TX::mem* x, int n) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const uint32_t none = HALF ? 0xff80ff80u : 0xff800000u;
+      u[k] = u32x4_t{none, none, none, none};
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        if constexpr (HALF) u[0][i / 2] = i & 1 ? (u[0][i / 2] & 0xffffu) | (uint32_t)x[i] << 16 : (u[0][i / 2] & 0xffff0000u) | x[i];
+        else u[i / 4][i & 3] = __float_as_uint(x[i]);
+      }
+  }
+  __device__ __forceinline__ void value(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (HALF) v[i] = i & 1 ? bf16_hi(u[0][i / 2]) : bf16_lo(u[0][i / 2]);
+      else v[i] = __uint_as_float(u[i / 4][i & 3]);
+    }
+  }
+};
+
+template <class TX>
+__device__ __forceinline__ void load_step(Raw8<TX> (&raw)[NV], const typename TX::mem* x, int base, int v1) {
+  const int col = base + 8 * (int)threadIdx.x;
+  if (base + STEP <= v1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) raw[j].load(x + col + j * VEC_STEP);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = col + j * VEC_STEP;
+      if (c + 8 <= v1) raw[j].load(x + c);
+      else raw[j].load_part(x + c, v1 - c);
+    }
+  }
+}
+
+__device__ __forceinline__ void offer(Shared& sh, float value, float threshold, int col) {
+  if (value > threshold) {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < CAP) {
+      sh.key[at] = key_of(value);
+      sh.idx[at] = (uint32_t)col;
+    }
+  }
+}
+
+// The candidates of one step do not fit: they are offered again in halves of a vector, thinned
+// out after each.  Indexes do not ascend from one half to the next, so the halves keep the
+// threshold of the steps before them, and offer what equals a later one too.
+template <class TX>
+__device__ __forceinline__ void offer_in_parts(Shared& sh, const typename TX::mem* x, int base, int v1, int held,
+                                               float threshold, int k) {
+  if (threadIdx.x == 0) sh.count = held;
+  __syncthreads();
+  settle(sh, k, k + SPARE);
+  if (held > k + SPARE) threshold = sh.threshold;
+#pragma unroll 1
+  for (int h = 0; h < 2 * NV; ++h) {
+    const int col = base + (h >> 1) * VEC_STEP + 8 * (int)threadIdx.x + 4 * (h & 1);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i)
+      if (col + i < v1) offer(sh, TX::to_f32(x[col + i]), threshold, col + i);
+    settle(sh, k, k + SPARE);
+  }
+}
+
+// The next step's loads are in flight under the work on this one.
+template <class TX, bool ENT, bool TOP>
 __global__ __launch_bounds__(T) void token_logprob_kernel(TokenLogprobArgs p) {
   __shared__ Shared sh;
   const int tid = threadIdx.x, k = p.n_top;
@@ -303,26 +387,17 @@ __global__ __launch_bounds__(T) void token_logprob_kernel(TokenLogprobArgs p) {
     if constexpr (TOP) {
       if (tid == 0) sh.count = 0;
     }
+    Raw8<TX> raw[NV], next[NV];
+    load_step<TX>(next, x, v0, v1);
     for (int base = v0; base < v1; base += STEP) {
-      Chunk8<TX, VEC> raw[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) raw[j] = next[j];
+      if (base + STEP < v1) load_step<TX>(next, x, base + STEP, v1);
       float top[NV];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int col = base + j * VEC_STEP + 8 * tid;
-        raw[j].load(x, col, col < v1 ? (long)p.V : 0l);
-      }
-      auto values = [&](int j, float (&v)[8]) {
-        const int col = base + j * VEC_STEP + 8 * tid;
-        raw[j].value(col, p.V, v);
-        if (base + STEP > v1) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = col + i < v1 ? v[i] : -INFINITY;
-        }
-      };
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
         float v[8];
-        values(j, v);
+        raw[j].value(v);
         top[j] = max8(v);
         sums.add(v, top[j], c);
       }
@@ -351,60 +426,29 @@ __global__ __launch_bounds__(T) void token_logprob_kernel(TokenLogprobArgs p) {
             return n;
           }));
         }
-        auto offer = [&](float value, int col) {
-          if (value > threshold) {
-            const int at = atomicAdd(&sh.count, 1);
-            if (at < CAP) {
-              sh.key[at] = key_of(value);
-              sh.idx[at] = (uint32_t)col;
-            }
-          }
-        };
 #pragma unroll
         for (int j = 0; j < NV; ++j)
           if (!(top[j] <= threshold)) {
             float v[8];
-            values(j, v);
+            raw[j].value(v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) offer(v[i], base + j * VEC_STEP + 8 * tid + i);
+            for (int i = 0; i < 8; ++i) offer(sh, v[i], threshold, base + j * VEC_STEP + 8 * tid + i);
           }
         __syncthreads();
         const int now = sh.count;  // (between barriers: the same for every thread)
         __syncthreads();
-        if (now > CAP) {
-          // they do not fit: again in halves of a vector, thinned out after each
-          if (tid == 0) sh.count = held;
-          __syncthreads();
-          settle(sh, k, k + SPARE);
-          // (indexes do not ascend from one half to the next, so the halves keep the threshold
-          // of the steps before them and offer what equals a later one too)
-          if (held > k + SPARE) threshold = sh.threshold;
-#pragma unroll 1
-          for (int h = 0; h < 2 * NV; ++h) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j)
-              if (j == h / 2) {
-                float v[8];
-                values(j, v);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const float a = h & 1 ? v[4 + i] : v[i];
-                  offer(a, base + j * VEC_STEP + 8 * tid + 4 * (h & 1) + i);
-                }
-              }
-            settle(sh, k, k + SPARE);
+        if (now <= CROWDED) {
+          held = now;
+        } else {
+          if (now <= CAP) {
+            if (tid < 64) thin_out(sh, k);
+            __syncthreads();
+          } else {
+            offer_in_parts<TX>(sh, x, base, v1, held, threshold, k);
           }
           threshold = sh.threshold;
           held = sh.count;
           __syncthreads();
-        } else if (now > CROWDED) {
-          if (tid < 64) thin_out(sh, k);
-          __syncthreads();
-          threshold = sh.threshold;
-          held = sh.count;
-          __syncthreads();
-        } else {
-          held = now;
         }
       }
     }
@@ -433,30 +477,38 @@ __global__ __launch_bounds__(T) void token_logprob_kernel(TokenLogprobArgs p) {
   }
 }
 
-// The pieces of a row: their sums rescaled to the largest maximum, their candidates together.
+// The pieces of a row: their sums rescaled to the largest maximum, their candidates together.  A
+// piece's list is in order, so the largest of the lists' last entries bounds what can count.
 template <class TX, bool TOP>
 __global__ __launch_bounds__(T) void token_logprob_join_kernel(TokenLogprobArgs p) {
   __shared__ Shared sh;
+  __shared__ unsigned long long bound;
   const int tid = threadIdx.x, k = p.n_top;
   const float c = p.scale * LOG2E;
   for (long row = blockIdx.x; row < p.M; row += gridDim.x) {
-    const float* part = p.part_sums + 3 * row * p.parts;
-    float m = LOWEST;
-    for (int i = 0; i < p.parts; ++i) m = fmaxf(m, part[3 * i]);
-    float s = 0.f, u = 0.f;
-    for (int i = 0; i < p.parts; ++i) {
-      const float d = fmaxf((part[3 * i] - m) * c, -1e30f), r = __builtin_amdgcn_exp2f(d);
-      s += r * part[3 * i + 1];
-      u += r * fmaf(d, part[3 * i + 1], part[3 * i + 2]);
-    }
+    // a piece a thread (there are at most 128)
+    const bool mine = tid < p.parts;
+    const float* part = p.part_sums + 3 * (row * p.parts + (mine ? tid : 0));
+    Sums<true> sums;
+    sums.m = mine ? part[0] : LOWEST;
+    sums.s = mine ? part[1] : 0.f;
+    sums.u = mine ? part[2] : 0.f;
+    const unsigned long long* from = p.part_top + row * p.parts * k;
     if constexpr (TOP) {
-      if (tid == 0) sh.count = 0;
+      if (tid == 0) {
+        sh.count = 0;
+        bound = 0ull;
+      }
       __syncthreads();
+      if (mine) atomicMax(&bound, from[tid * k + k - 1]);
+    }
+    join<true>(sums, sh, c);
+    if constexpr (TOP) {
+      const unsigned long long least = bound > 0ull ? bound : 1ull;
       const int n = p.parts * k;  // at most CAP
-      const unsigned long long* from = p.part_top + row * n;
       for (int i = tid; i < n; i += T) {
         const unsigned long long e = from[i];
-        if (e) {
+        if (e >= least) {
           const int at = atomicAdd(&sh.count, 1);
           sh.key[at] = (uint32_t)(e >> 32);
           sh.idx[at] = ~(uint32_t)e;
@@ -464,7 +516,7 @@ __global__ __launch_bounds__(T) void token_logprob_join_kernel(TokenLogprobArgs 
       }
       settle(sh, k, k + SPARE);
     }
-    finish_row<TX, TOP>(p, row, m, s, u, sh);
+    finish_row<TX, TOP>(p, row, sums.m, sums.s, sums.u, sh);
     __syncthreads();
   }
 }
@@ -575,22 +627,17 @@ __global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradA
   }
 }
 
-template <class TX, bool VEC, bool ENT>
+template <class TX, bool ENT>
 void run_parts(const TokenLogprobArgs& a, unsigned grid, hipStream_t s) {
-  if (a.n_top) token_logprob_kernel<TX, VEC, ENT, true><<<grid, T, 0, s>>>(a);
-  else token_logprob_kernel<TX, VEC, ENT, false><<<grid, T, 0, s>>>(a);
+  if (a.n_top) token_logprob_kernel<TX, ENT, true><<<grid, T, 0, s>>>(a);
+  else token_logprob_kernel<TX, ENT, false><<<grid, T, 0, s>>>(a);
 }
 template <class TX>
-void run(const TokenLogprobArgs& a, bool vec, hipStream_t s) {
+void run(const TokenLogprobArgs& a, hipStream_t s) {
   const long items = a.M * a.parts, most = 1 << 22;
   const unsigned grid = (unsigned)(items < most ? items : most);
-  if (vec) {
-    if (a.entropy) run_parts<TX, true, true>(a, grid, s);
-    else run_parts<TX, true, false>(a, grid, s);
-  } else {
-    if (a.entropy) run_parts<TX, false, true>(a, grid, s);
-    else run_parts<TX, false, false>(a, grid, s);
-  }
+  if (a.entropy) run_parts<TX, true>(a, grid, s);
+  else run_parts<TX, false>(a, grid, s);
   if (a.parts > 1) {
     const unsigned rows = (unsigned)(a.M < most ? a.M : most);
     if (a.n_top) token_logprob_join_kernel<TX, true><<<rows, T, 0, s>>>(a);
@@ -611,9 +658,9 @@ void token_logprob_split(int64_t M, int64_t V, int n_top, int* parts, int* part_
   *parts = int((pieces + each - 1) / each);
 }
 
-hipError_t launch_token_logprobs(const TokenLogprobArgs& a, int dtype, bool vec, hipStream_t s) {
-  if (dtype == kF32) run<F32>(a, vec, s);
-  else run<Bf16>(a, vec, s);
+hipError_t launch_token_logprobs(const TokenLogprobArgs& a, int dtype, hipStream_t s) {
+  if (dtype == kF32) run<F32>(a, s);
+  else run<Bf16>(a, s);
   return hipGetLastError();
 }
 
