@@ -15,8 +15,8 @@
 // 8192 logits set it: the k-th largest of the 256 threads' own maxima is at most the k-th largest
 // of all (k different elements reach it), and about k elements lie above it.  When candidates
 // pile up, the k-th largest of them (found bit by bit, the counts by ballots) becomes the
-// threshold and the others go.  So of a row of independent logits a few hundred ever reach LDS;
-// rows in ascending order reach it whole, in steps that fit.  Order is that of the logits, equal
+// threshold and the others go.  So of a row of independent logits some 5 k ever reach LDS; rows in
+// ascending order reach it whole, in steps that fit.  Order is that of the logits, equal
 // ones by their index; the order in which candidates arrive changes nothing.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -30,14 +30,17 @@ namespace flce {
 namespace {
 
 constexpr int T = 256;              // threads of a workgroup
-constexpr int NV = 4;               // vectors of 8 logits a thread holds at once
-constexpr int VEC_STEP = 8 * T;     // logits of one vector of every thread
-constexpr int STEP = NV * VEC_STEP;
+constexpr int VEC_STEP = 8 * T;     // logits of one vector (8 logits) of every thread
+// Vectors that a thread holds at once: 64 bytes.
+template <class TX>
+constexpr int NV = sizeof(typename TX::mem) == 2 ? 4 : 2;
+template <class TX>
+constexpr int STEP = NV<TX> * VEC_STEP;
 constexpr int CAP = 2048;           // candidates in LDS
-constexpr int CROWDED = 512;        // more than these are thinned out
+constexpr int CROWDED = 32;         // more than this and 3 k are thinned out
 constexpr int SPARE = 64;           // equal logits kept beyond k without a look at their index
 constexpr float LOWEST = -3.402823466e38f;
-static_assert(CAP >= kMaxTop + SPARE + VEC_STEP / 2, "half a vector of every thread fits after thinning");
+static_assert(CAP >= CROWDED + 3 * kMaxTop && CAP >= kMaxTop + SPARE + VEC_STEP / 2, "half a vector of every thread fits after thinning");
 
 // Floats ordered as whole numbers.  -0 is 0, and a NaN ranks with -inf.
 constexpr uint32_t KEY_NONE = 0x007fffffu;  // -inf
@@ -55,10 +58,18 @@ __device__ __forceinline__ float below(uint32_t k) {
   return k <= KEY_NONE + 1 ? -INFINITY : value_of(k == 0x80000000u ? k - 2 : k - 1);
 }
 
+// A candidate: its logit's key above the complement of its index, so that the larger of two comes
+// first.
+typedef unsigned long long Candidate;
+__device__ __forceinline__ Candidate candidate(float x, int index) {
+  return (Candidate)key_of(x) << 32 | ~(uint32_t)index;
+}
+__device__ __forceinline__ uint32_t key_in(Candidate c) { return (uint32_t)(c >> 32); }
+__device__ __forceinline__ uint32_t index_in(Candidate c) { return ~(uint32_t)c; }
+
 // Candidates of a row, and what the waves tell each other.
 struct Shared {
-  uint32_t key[CAP];
-  uint32_t idx[CAP];
+  Candidate cand[CAP];
   uint32_t lane_key[T];
   int count;
   float threshold;
@@ -98,53 +109,57 @@ __device__ __forceinline__ uint32_t wave_min(uint32_t v) { return ~wave_max(~v);
 
 // Wave 0: keep the k largest of sh.count > k candidates, and up to SPARE more that equal the
 // last of them; the threshold becomes that one's logit.  Candidates that come later have larger
-// indexes, so only larger logits can displace what is kept.
+// indexes, so only larger logits can displace what is kept.  Up to 256 keys (the usual case) stay
+// in registers while the bits of the k-th largest are found.
 __device__ __forceinline__ void thin_out(Shared& sh, int k) {
   const int lane = threadIdx.x & 63, n = min(sh.count, CAP);
-  uint32_t lo = ~0u, hi = 0u;
+  uint32_t held[4], lo = ~0u, hi = 0u;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) held[w] = 64 * w + lane < n ? key_in(sh.cand[64 * w + lane]) : 0u;
   for (int i = lane; i < n; i += 64) {
-    lo = min(lo, sh.key[i]);
-    hi = max(hi, sh.key[i]);
+    lo = min(lo, key_in(sh.cand[i]));
+    hi = max(hi, key_in(sh.cand[i]));
   }
   lo = wave_min(lo);
   hi = wave_max(hi);
   const int bits = open_bits(lo, hi);
+  // (keys are not 0, and neither is what they are compared with)
   const uint32_t t = kth(closed(lo, bits), bits, k, [&](uint32_t c) {
     int s = 0;
-    for (int i = lane; i < n + lane; i += 64) s += count_of(i < n && sh.key[i] >= c);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) s += count_of(held[w] >= c);
+    for (int i = 256 + lane; i < n + lane; i += 64) s += count_of(i < n && key_in(sh.cand[i]) >= c);
     return s;
   });
   // (t may lie between two candidates: the threshold is the least one at or above it)
   int above = 0, equal = 0;
   uint32_t least = ~0u;
-  for (int i = lane; i < n; i += 64)
-    if (sh.key[i] >= t) least = min(least, sh.key[i]);
+  for (int i = lane; i < n; i += 64) {
+    const uint32_t key = key_in(sh.cand[i]);
+    if (key >= t) least = min(least, key);
+  }
   least = wave_min(least);
   for (int i = lane; i < n + lane; i += 64) {
-    above += count_of(i < n && sh.key[i] > least);
-    equal += count_of(i < n && sh.key[i] == least);
+    const uint32_t key = i < n ? key_in(sh.cand[i]) : 0u;
+    above += count_of(key > least);
+    equal += count_of(key == least);
   }
-  uint32_t last = ~0u;  // the largest index kept among equal ones
+  uint32_t last = 0u;  // the smallest complement of an index kept among equal ones
   if (above + equal > k + SPARE) {
-    // the (k - above)-th smallest index among them: the kth largest of the complements
-    last = ~kth(0u, 32, k - above, [&](uint32_t c) {
+    last = kth(0u, 32, k - above, [&](uint32_t c) {
       int s = 0;
-      for (int i = lane; i < n + lane; i += 64) s += count_of(i < n && sh.key[i] == least && ~sh.idx[i] >= c);
+      for (int i = lane; i < n + lane; i += 64)
+        s += count_of(i < n && key_in(sh.cand[i]) == least && (uint32_t)sh.cand[i] >= c);
       return s;
     });
   }
+  const Candidate cut = (Candidate)least << 32 | last;
   // compact in place: what a step reads lies at or behind what it writes
   int kept = 0;
   for (int i = lane; i < n + lane; i += 64) {
-    const bool in = i < n;
-    const uint32_t key = in ? sh.key[i] : 0u, idx = in ? sh.idx[i] : 0u;
-    const bool keep = in && (key > least || (key == least && idx <= last));
-    const unsigned long long mask = __ballot(keep);
-    const int at = kept + __popcll(mask & ((1ull << lane) - 1ull));
-    if (keep) {
-      sh.key[at] = key;
-      sh.idx[at] = idx;
-    }
+    const Candidate c = i < n ? sh.cand[i] : 0ull;
+    const unsigned long long mask = __ballot(c >= cut);
+    if (c >= cut) sh.cand[kept + __popcll(mask & ((1ull << lane) - 1ull))] = c;
     kept += __popcll(mask);
   }
   if (lane == 0) {
@@ -228,11 +243,14 @@ __device__ __forceinline__ void join(Sums<ENT>& a, Shared& sh, float c) {
   }
 }
 
-// The place of candidate i among the n (n is small: the last thinning left at most k + SPARE).
-__device__ __forceinline__ int rank_of(const Shared& sh, int i, int n) {
-  const uint32_t key = sh.key[i], idx = sh.idx[i];
-  int r = 0;
-  for (int j = 0; j < n; ++j) r += sh.key[j] > key || (sh.key[j] == key && sh.idx[j] < idx);
+// The place of candidate c among the n (n is small: the last thinning left at most k + SPARE).
+__device__ __forceinline__ int rank_of(const Shared& sh, Candidate c, int n) {
+  int r = 0, j = 0;
+  for (; j + 8 <= n; j += 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r += sh.cand[j + i] > c;
+  }
+  for (; j < n; ++j) r += sh.cand[j] > c;
   return r;
 }
 
@@ -261,10 +279,11 @@ __device__ __forceinline__ void finish_row(const TokenLogprobArgs& p, long row, 
   if constexpr (TOP) {
     const int n = sh.count, k = p.n_top;
     for (int i = threadIdx.x; i < n; i += T) {
-      const int r = rank_of(sh, i, n);
+      const Candidate own = sh.cand[i];
+      const int r = rank_of(sh, own, n);
       if (r < k) {
-        p.top_ids[row * k + r] = (int64_t)sh.idx[i];
-        p.top_logprob[row * k + r] = logp(value_of(sh.key[i]));
+        p.top_ids[row * k + r] = (int64_t)index_in(own);
+        p.top_logprob[row * k + r] = logp(value_of(key_in(own)));
       }
     }
     // fewer than k logits above -inf: the first of the others follow.  Fewer than k of the first
@@ -324,14 +343,14 @@ struct Raw8 {
 };
 
 template <class TX>
-__device__ __forceinline__ void load_step(Raw8<TX> (&raw)[NV], const typename TX::mem* x, int base, int v1) {
+__device__ __forceinline__ void load_step(Raw8<TX> (&raw)[NV<TX>], const typename TX::mem* x, int base, int v1) {
   const int col = base + 8 * (int)threadIdx.x;
-  if (base + STEP <= v1) {
+  if (base + STEP<TX> <= v1) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) raw[j].load(x + col + j * VEC_STEP);
+    for (int j = 0; j < NV<TX>; ++j) raw[j].load(x + col + j * VEC_STEP);
   } else {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+    for (int j = 0; j < NV<TX>; ++j) {
       const int c = col + j * VEC_STEP;
       if (c + 8 <= v1) raw[j].load(x + c);
       else raw[j].load_part(x + c, v1 - c);
@@ -342,10 +361,7 @@ __device__ __forceinline__ void load_step(Raw8<TX> (&raw)[NV], const typename TX
 __device__ __forceinline__ void offer(Shared& sh, float value, float threshold, int col) {
   if (value > threshold) {
     const int at = atomicAdd(&sh.count, 1);
-    if (at < CAP) {
-      sh.key[at] = key_of(value);
-      sh.idx[at] = (uint32_t)col;
-    }
+    if (at < CAP) sh.cand[at] = candidate(value, col);
   }
 }
 
@@ -360,7 +376,7 @@ __device__ __forceinline__ void offer_in_parts(Shared& sh, const typename TX::me
   settle(sh, k, k + SPARE);
   if (held > k + SPARE) threshold = sh.threshold;
 #pragma unroll 1
-  for (int h = 0; h < 2 * NV; ++h) {
+  for (int h = 0; h < 2 * NV<TX>; ++h) {
     const int col = base + (h >> 1) * VEC_STEP + 8 * (int)threadIdx.x + 4 * (h & 1);
 #pragma unroll 1
     for (int i = 0; i < 4; ++i)
@@ -371,9 +387,9 @@ __device__ __forceinline__ void offer_in_parts(Shared& sh, const typename TX::me
 
 // The next step's loads are in flight under the work on this one.
 template <class TX, bool ENT, bool TOP>
-__global__ __launch_bounds__(T) void token_logprob_kernel(TokenLogprobArgs p) {
+__global__ __launch_bounds__(T, 5) void token_logprob_kernel(TokenLogprobArgs p) {
   __shared__ Shared sh;
-  const int tid = threadIdx.x, k = p.n_top;
+  const int tid = threadIdx.x, k = p.n_top, crowded = CROWDED + 3 * k;
   const float c = p.scale * LOG2E;
   const long items = p.M * p.parts;
   for (long item = blockIdx.x; item < items; item += gridDim.x) {
@@ -387,15 +403,15 @@ __global__ __launch_bounds__(T) void token_logprob_kernel(TokenLogprobArgs p) {
     if constexpr (TOP) {
       if (tid == 0) sh.count = 0;
     }
-    Raw8<TX> raw[NV], next[NV];
+    Raw8<TX> raw[NV<TX>], next[NV<TX>];
     load_step<TX>(next, x, v0, v1);
-    for (int base = v0; base < v1; base += STEP) {
+    for (int base = v0; base < v1; base += STEP<TX>) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) raw[j] = next[j];
-      if (base + STEP < v1) load_step<TX>(next, x, base + STEP, v1);
-      float top[NV];
+      for (int j = 0; j < NV<TX>; ++j) raw[j] = next[j];
+      if (base + STEP<TX> < v1) load_step<TX>(next, x, base + STEP<TX>, v1);
+      float top[NV<TX>];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
+      for (int j = 0; j < NV<TX>; ++j) {
         float v[8];
         raw[j].value(v);
         top[j] = max8(v);
@@ -405,7 +421,7 @@ __global__ __launch_bounds__(T) void token_logprob_kernel(TokenLogprobArgs p) {
         if (base == v0) {
           float most = top[0];
 #pragma unroll
-          for (int j = 1; j < NV; ++j) most = fmaxf(most, top[j]);
+          for (int j = 1; j < NV<TX>; ++j) most = fmaxf(most, top[j]);
           sh.lane_key[tid] = key_of(most);
           __syncthreads();
           uint32_t mine[T / 64], hi = 0u, lo = ~0u;
@@ -426,18 +442,35 @@ __global__ __launch_bounds__(T) void token_logprob_kernel(TokenLogprobArgs p) {
             return n;
           }));
         }
+        // (a thread's candidates of the step take their places with one atomic)
+        uint32_t hits = 0u;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV<TX>; ++j)
           if (!(top[j] <= threshold)) {
             float v[8];
             raw[j].value(v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) offer(sh, v[i], threshold, base + j * VEC_STEP + 8 * tid + i);
+            for (int i = 0; i < 8; ++i) hits |= v[i] > threshold ? 1u << (8 * j + i) : 0u;
           }
+        if (hits) {
+          int at = atomicAdd(&sh.count, __popc(hits));
+#pragma unroll
+          for (int j = 0; j < NV<TX>; ++j)
+            if (hits >> (8 * j) & 255u) {
+              float v[8];
+              raw[j].value(v);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (hits >> (8 * j + i) & 1u) {
+                  if (at < CAP) sh.cand[at] = candidate(v[i], base + j * VEC_STEP + 8 * tid + i);
+                  ++at;
+                }
+            }
+        }
         __syncthreads();
         const int now = sh.count;  // (between barriers: the same for every thread)
         __syncthreads();
-        if (now <= CROWDED) {
+        if (now <= crowded) {
           held = now;
         } else {
           if (now <= CAP) {
@@ -465,10 +498,11 @@ __global__ __launch_bounds__(T) void token_logprob_kernel(TokenLogprobArgs p) {
       }
       if constexpr (TOP) {
         const int n = sh.count;
-        unsigned long long* to = p.part_top + item * k;
+        Candidate* to = p.part_top + item * k;
         for (int i = tid; i < n; i += T) {
-          const int r = rank_of(sh, i, n);
-          if (r < k) to[r] = (unsigned long long)sh.key[i] << 32 | (uint32_t)~sh.idx[i];
+          const Candidate own = sh.cand[i];
+          const int r = rank_of(sh, own, n);
+          if (r < k) to[r] = own;
         }
         for (int r = n + tid; r < k; r += T) to[r] = 0ull;
       }
@@ -478,11 +512,13 @@ __global__ __launch_bounds__(T) void token_logprob_kernel(TokenLogprobArgs p) {
 }
 
 // The pieces of a row: their sums rescaled to the largest maximum, their candidates together.  A
-// piece's list is in order, so the largest of the lists' last entries bounds what can count.
+// piece's list is in order, so where q pieces reach x with their a-th entry, a q entries are x or
+// more: with a q >= k the q-th largest of the a-th entries bounds what can count, and leaves little
+// more than k of the lists' entries.  All loads go out at once: this kernel is a chain of waits.
 template <class TX, bool TOP>
 __global__ __launch_bounds__(T) void token_logprob_join_kernel(TokenLogprobArgs p) {
   __shared__ Shared sh;
-  __shared__ unsigned long long bound;
+  constexpr int HELD = CAP / T;  // entries of a thread
   const int tid = threadIdx.x, k = p.n_top;
   const float c = p.scale * LOG2E;
   for (long row = blockIdx.x; row < p.M; row += gridDim.x) {
@@ -493,27 +529,27 @@ __global__ __launch_bounds__(T) void token_logprob_join_kernel(TokenLogprobArgs 
     sums.m = mine ? part[0] : LOWEST;
     sums.s = mine ? part[1] : 0.f;
     sums.u = mine ? part[2] : 0.f;
-    const unsigned long long* from = p.part_top + row * p.parts * k;
+    const int n = TOP ? p.parts * k : 0;  // at most CAP
+    const Candidate* from = p.part_top + row * n;
+    Candidate entry[HELD];
     if constexpr (TOP) {
-      if (tid == 0) {
-        sh.count = 0;
-        bound = 0ull;
-      }
-      __syncthreads();
-      if (mine) atomicMax(&bound, from[tid * k + k - 1]);
+#pragma unroll
+      for (int i = 0; i < HELD; ++i) entry[i] = tid + i * T < n ? from[tid + i * T] : 0ull;
+      const int a = (k + p.parts - 1) / p.parts;
+      sh.lane_key[tid] = mine ? key_in(from[tid * k + a - 1]) : 0u;
+      if (tid == 0) sh.count = 0;
     }
     join<true>(sums, sh, c);
     if constexpr (TOP) {
-      const unsigned long long least = bound > 0ull ? bound : 1ull;
-      const int n = p.parts * k;  // at most CAP
-      for (int i = tid; i < n; i += T) {
-        const unsigned long long e = from[i];
-        if (e >= least) {
-          const int at = atomicAdd(&sh.count, 1);
-          sh.key[at] = (uint32_t)(e >> 32);
-          sh.idx[at] = ~(uint32_t)e;
-        }
-      }
+      const int a = (k + p.parts - 1) / p.parts, q = (k + a - 1) / a, lane = tid & 63;
+      const uint32_t one = sh.lane_key[lane], two = sh.lane_key[64 + lane];
+      const int bits = open_bits(0u, wave_max(max(one, two)));
+      // (an entry of no candidate is 0; where fewer than q pieces have an a-th one, all count)
+      const uint32_t least =
+          max(1u, kth(0u, bits, q, [&](uint32_t cand) { return count_of(one >= cand) + count_of(two >= cand); }));
+#pragma unroll
+      for (int i = 0; i < HELD; ++i)
+        if (key_in(entry[i]) >= least) sh.cand[atomicAdd(&sh.count, 1)] = entry[i];
       settle(sh, k, k + SPARE);
     }
     finish_row<TX, TOP>(p, row, sums.m, sums.s, sums.u, sh);
@@ -526,6 +562,7 @@ __global__ __launch_bounds__(T) void token_logprob_join_kernel(TokenLogprobArgs 
 // (from the logits, so dlogits may be the logits' own memory) and written over the rest after a
 // barrier; several entries of one token are added in their order.
 constexpr int LIST = kMaxTokens + kMaxTop;
+constexpr int GRAD_NV = 4, GRAD_STEP = GRAD_NV * VEC_STEP;
 
 struct GradShared {
   int id[LIST];     // the entry's token, -1 outside this piece
@@ -544,12 +581,12 @@ __global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradA
   const long items = p.M * pieces;
   for (long item = blockIdx.x; item < items; item += gridDim.x) {
     const long row = item / pieces;
-    const int v0 = (int)(item - row * pieces) * STEP, v1 = min(p.V, v0 + STEP);
+    const int v0 = (int)(item - row * pieces) * GRAD_STEP, v1 = min(p.V, v0 + GRAD_STEP);
     const typename TX::mem* x = static_cast<const typename TX::mem*>(p.logits) + row * p.ldl;
     typename TX::mem* dx = static_cast<typename TX::mem*>(p.dlogits) + row * p.ldd;
-    Chunk8<TX, VEC> raw[NV];
+    Chunk8<TX, VEC> raw[GRAD_NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+    for (int j = 0; j < GRAD_NV; ++j) {
       const int col = v0 + j * VEC_STEP + 8 * tid;
       raw[j].load(x, col, col < v1 ? (long)p.V : 0l);
     }
@@ -612,7 +649,7 @@ __global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradA
     wait_vmcnt<0>();
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
+    for (int j = 0; j < GRAD_NV; ++j) {
       const int col = v0 + j * VEC_STEP + 8 * tid;
       float v[8];
       raw[j].value(col, p.V, v);
@@ -649,7 +686,7 @@ void run(const TokenLogprobArgs& a, hipStream_t s) {
 
 void token_logprob_split(int64_t M, int64_t V, int n_top, int* parts, int* part_len) {
   const int64_t pieces = (V + VEC_STEP - 1) / VEC_STEP;
-  int64_t want = M >= 2048 || M < 1 ? 1 : 2048 / M;
+  int64_t want = M >= 1024 || M < 1 ? 1 : 1024 / M;
   if (want > 128) want = 128;
   if (n_top && want > CAP / n_top) want = CAP / n_top;
   if (want > pieces) want = pieces;
@@ -665,7 +702,7 @@ hipError_t launch_token_logprobs(const TokenLogprobArgs& a, int dtype, hipStream
 }
 
 hipError_t launch_token_logprobs_grad(const TokenLogprobGradArgs& a, int dtype, bool vec, hipStream_t s) {
-  const int pieces = (a.V + STEP - 1) / STEP;
+  const int pieces = (a.V + GRAD_STEP - 1) / GRAD_STEP;
   const long items = a.M * pieces, most = 1 << 22;
   const unsigned grid = (unsigned)(items < most ? items : most);
   if (dtype == kF32) {
