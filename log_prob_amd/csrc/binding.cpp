@@ -302,6 +302,193 @@ PyObject* mxfp4_forward(PyObject* const* a) {
   return tuple({wrap(lp), wrap(lse), wrap_or_none(en)});
 }
 
+bool double_arg(PyObject* o, double& v) {
+  v = PyFloat_AsDouble(o);
+  if (v != -1.0 || !PyErr_Occurred()) return true;
+  PyErr_Clear();
+  return false;
+}
+bool uint_arg(PyObject* o, uint64_t& v) {
+  if (!PyLong_Check(o)) return false;
+  v = PyLong_AsUnsignedLongLong(o);
+  if (v != uint64_t(-1) || !PyErr_Occurred()) return true;
+  PyErr_Clear();
+  return false;
+}
+// A matrix with contiguous rows and the same size as `like`, or None.
+bool rows_like(PyObject* o, int64_t m, int64_t h, Rows& r, void*& at) {
+  at = nullptr;
+  r.dtype = FLCE_BF16;
+  r.ld = h;
+  if (o == Py_None) return true;
+  if (!r.init(o) || r.m != m || r.h != h) return false;
+  at = r.data();
+  return true;
+}
+// Contiguous elements of type s and the given size (nullptr for None).
+bool block(PyObject* o, at::ScalarType s, at::IntArrayRef size, const Tensor*& t) {
+  t = nullptr;
+  if (o == Py_None) return true;
+  t = gpu_tensor(o);
+  return t && t->scalar_type() == s && t->sizes() == size && t->is_contiguous();
+}
+
+// (x, p, seed, offset, residual, out_dtype) -> y
+PyObject* dropout(PyObject* const* a) {
+  Rows x, r;
+  void* residual;
+  double p;
+  uint64_t seed = 0, offset;
+  const uint64_t* seed_at = nullptr;
+  int yd;
+  if (!x.init(a[0]) || !double_arg(a[1], p) || !uint_arg(a[3], offset) || !rows_like(a[4], x.m, x.h, r, residual) ||
+      !dtype_arg(a[5], residual ? r.dtype : x.dtype, yd))
+    return nullptr;
+  if (!uint_arg(a[2], seed)) {
+    const Tensor* t = gpu_tensor(a[2]);
+    if (!t || t->scalar_type() != at::kLong || t->numel() != 1) return nullptr;
+    seed_at = static_cast<const uint64_t*>(t->data_ptr());
+  }
+  const Tensor y = buffer({x.m, x.h}, scalar(yd));
+  if (!run([&] {
+        return flce_dropout(x.data(), x.dtype, x.ld, residual, r.dtype, r.ld, x.m, x.h, p, seed, seed_at, offset,
+                            y.data_ptr(), yd, x.h, stream());
+      }))
+    return nullptr;
+  return wrap(y);
+}
+
+// (X, W, bias, activation, residual, out_dtype, keep_pre) -> out, or (out, pre)
+PyObject* linear_forward(PyObject* const* a) {
+  Rows X, W, r;
+  const Tensor *bias, *none;
+  void* residual;
+  int64_t act, keep;
+  int bd, od;
+  size_t bytes = 0;
+  if (!X.init(a[0]) || !W.init(a[1]) || X.dtype != FLCE_BF16 || W.dtype != FLCE_BF16 || W.h != X.h ||
+      !params(Py_None, a[2], W.m, none, bias, bd) || !int_arg(a[3], act) || !rows_like(a[4], X.m, W.m, r, residual) ||
+      !dtype_arg(a[5], FLCE_BF16, od) || !int_arg(a[6], keep) ||
+      flce_linear_workspace(X.m, W.m, X.h, &bytes, nullptr) != FLCE_OK)
+    return nullptr;
+  const Tensor out = buffer({X.m, W.m}, scalar(od));
+  Tensor ws, pre;
+  if (bytes) ws = workspace(bytes);
+  if (keep) pre = buffer({X.m, W.m}, at::kBFloat16);
+  if (!run([&] {
+        return flce_linear_forward(X.data(), X.ld, W.data(), W.ld, data(bias), bd, int(act), residual, r.dtype, r.ld,
+                                   X.m, W.m, X.h, out.data_ptr(), od, W.m, keep ? pre.data_ptr() : nullptr, W.m,
+                                   bytes ? ws.data_ptr() : nullptr, bytes ? ws.nbytes() : 0, stream());
+      }))
+    return nullptr;
+  return keep ? tuple({wrap(out), wrap(pre)}) : wrap(out);
+}
+
+// (dy, X, W, pre, activation, need_dx, need_dw, bias_dtype) -> (dX, dW, dbias)
+PyObject* linear_backward(PyObject* const* a) {
+  Rows dy, X, W, pre;
+  void* kept;
+  int64_t act, need_dx, need_dw;
+  int bd = FLCE_BF16;
+  size_t bytes = 0;
+  if (!dy.init(a[0]) || !X.init(a[1]) || !W.init(a[2]) || X.dtype != FLCE_BF16 || W.dtype != FLCE_BF16 ||
+      X.m != dy.m || W.m != dy.h || X.h != W.h || !int_arg(a[4], act) || !int_arg(a[5], need_dx) ||
+      !int_arg(a[6], need_dw) || (a[7] != Py_None && !dtype_arg(a[7], FLCE_BF16, bd)))
+    return nullptr;
+  if (!rows_like(act ? a[3] : Py_None, dy.m, dy.h, pre, kept) || pre.dtype != FLCE_BF16 || (act && !kept) ||
+      flce_linear_workspace(dy.m, dy.h, X.h, nullptr, &bytes) != FLCE_OK)
+    return nullptr;
+  const Tensor ws = workspace(bytes);
+  Tensor dx, dw, db;
+  if (need_dx) dx = buffer({X.m, X.h}, at::kBFloat16);
+  if (need_dw) dw = buffer({W.m, W.h}, at::kBFloat16);
+  if (a[7] != Py_None) db = buffer({W.m}, scalar(bd));
+  auto at_of = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+  if (!run([&] {
+        return flce_linear_backward(dy.data(), dy.dtype, dy.ld, kept, pre.ld, int(act), X.data(), X.ld, W.data(), W.ld,
+                                    dy.m, dy.h, X.h, at_of(dx), X.h, at_of(dw), X.h, at_of(db), bd, ws.data_ptr(),
+                                    ws.nbytes(), stream());
+      }))
+    return nullptr;
+  return tuple({wrap_or_none(dx), wrap_or_none(dw), wrap_or_none(db)});
+}
+
+// Given tokens [m] or [m, n], or None.
+bool token_block(PyObject* o, int64_t m, const Tensor*& t, int64_t& n) {
+  t = nullptr;
+  n = 0;
+  if (o == Py_None) return true;
+  t = gpu_tensor(o);
+  if (!t || t->scalar_type() != at::kLong || t->dim() < 1 || t->dim() > 2 || t->size(0) != m || !t->is_contiguous())
+    return false;
+  n = t->dim() == 1 ? 1 : t->size(1);
+  return true;
+}
+
+// (logits, tokens, ignore_index, scale, n_top, compute_entropy)
+// -> (logprob, lse, entropy, top_ids, top_logprob, stats)
+PyObject* token_logprobs(PyObject* const* a) {
+  Rows x;
+  const Tensor* tokens;
+  int64_t n, ignore, k, ent;
+  float scale;
+  size_t bytes = 0;
+  if (!x.init(a[0]) || !token_block(a[1], x.m, tokens, n) || !int_arg(a[2], ignore) || !float_arg(a[3], scale) ||
+      !int_arg(a[4], k) || !int_arg(a[5], ent) || k < 0 ||
+      flce_token_logprobs_workspace(x.m, x.h, k, &bytes) != FLCE_OK)
+    return nullptr;
+  const Tensor lp = tokens ? buffer(tokens->sizes(), at::kFloat) : buffer({x.m, 0}, at::kFloat),
+               lse = buffer({x.m}, at::kFloat), stats = buffer({x.m, 2}, at::kFloat);
+  Tensor ws, en, ids, top;
+  if (bytes) ws = workspace(bytes);
+  if (ent) en = buffer({x.m}, at::kFloat);
+  if (k) {
+    ids = buffer({x.m, k}, at::kLong);
+    top = buffer({x.m, k}, at::kFloat);
+  }
+  if (!run([&] {
+        return flce_token_logprobs(x.data(), x.dtype, x.ld, x.m, x.h, data_of<int64_t>(tokens), n, ignore, scale, k,
+                                   lp.data_ptr<float>(), lse.data_ptr<float>(), ent ? en.data_ptr<float>() : nullptr,
+                                   stats.data_ptr<float>(), k ? ids.data_ptr<int64_t>() : nullptr,
+                                   k ? top.data_ptr<float>() : nullptr, bytes ? ws.data_ptr() : nullptr,
+                                   bytes ? ws.nbytes() : 0, stream());
+      }))
+    return nullptr;
+  return tuple({wrap(lp), wrap(lse), wrap_or_none(en), wrap_or_none(ids), wrap_or_none(top), wrap(stats)});
+}
+
+// (logits, tokens, stats, entropy, top_ids, grad_logprob, grad_top, grad_entropy, grad_lse,
+// ignore_index, scale) -> dlogits
+PyObject* token_logprobs_backward(PyObject* const* a) {
+  Rows x;
+  const Tensor *tokens, *stats, *entropy = nullptr, *ids = nullptr, *g, *gt = nullptr, *ge, *gl;
+  int64_t n, ignore, k = 0;
+  float scale;
+  if (!x.init(a[0]) || !token_block(a[1], x.m, tokens, n)) return nullptr;
+  const int64_t no_tokens[2] = {x.m, 0};
+  if (a[2] == Py_None || !block(a[2], at::kFloat, {x.m, 2}, stats) ||
+      !block(a[5], at::kFloat, tokens ? tokens->sizes() : at::IntArrayRef(no_tokens, 2), g) ||
+      !block(a[7], at::kFloat, {x.m}, ge) || !block(a[8], at::kFloat, {x.m}, gl) || !int_arg(a[9], ignore) ||
+      !float_arg(a[10], scale))
+    return nullptr;
+  if (ge && (a[3] == Py_None || !block(a[3], at::kFloat, {x.m}, entropy))) return nullptr;
+  if (a[6] != Py_None) {
+    const Tensor* t = gpu_tensor(a[4]);
+    if (!t || t->dim() != 2) return nullptr;
+    k = t->size(1);
+    if (!block(a[4], at::kLong, {x.m, k}, ids) || !block(a[6], at::kFloat, {x.m, k}, gt)) return nullptr;
+  }
+  const Tensor d = buffer({x.m, x.h}, scalar(x.dtype));
+  if (!run([&] {
+        return flce_token_logprobs_backward(
+            x.data(), x.dtype, x.ld, x.m, x.h, data_of<int64_t>(tokens), n, ignore, scale, data_of<float>(stats),
+            data_of<float>(entropy), k ? data_of<int64_t>(ids) : nullptr, k, data_of<float>(g),
+            k ? data_of<float>(gt) : nullptr, data_of<float>(ge), data_of<float>(gl), d.data_ptr(), x.h, stream());
+      }))
+    return nullptr;
+  return wrap(d);
+}
+
 // nullptr from a function means "not this way": None.  Nothing that C++ throws (memory that
 // cannot be had) leaves the entry; the long way then raises it.
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -325,6 +512,11 @@ PyMethodDef methods[] = {method<layer_norm_forward, 6>("layer_norm_forward"),
                          method<mx_dequantize, 5>("mx_dequantize"),
                          method<mxfp4_logits, 5>("mxfp4_logits"),
                          method<mxfp4_forward, 7>("mxfp4_forward"),
+                         method<dropout, 6>("dropout"),
+                         method<linear_forward, 7>("linear_forward"),
+                         method<linear_backward, 8>("linear_backward"),
+                         method<token_logprobs, 6>("token_logprobs"),
+                         method<token_logprobs_backward, 11>("token_logprobs_backward"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -966,6 +966,10 @@ def linear_forward(X, W, bias=None, activation: Optional[str] = None, residual=N
     fp32; activation is None, "relu", "gelu", "gelu_tanh" or "silu".  `out` may supply the result's
     buffer (with keep_pre the pair), and may be residual."""
     act = _activation(activation)
+    if out is None and workspace is None:
+        r = _fast().linear_forward(X, W, bias, act, residual, out_dtype, bool(keep_pre))
+        if r is not None:
+            return r
     import torch
     dev = _on_gpu(X, "X")
     ldx = _operand(X, "X", dev)
@@ -1001,6 +1005,10 @@ def linear_backward(dy, X, W, pre=None, activation: Optional[str] = None, need_d
     the forward's pre.  dX and dW are bf16, or None where they are not needed; dbias has bias_dtype
     (None: no dbias).  The gradient of the residual is dy.  `out` may supply the three buffers."""
     act = _activation(activation)
+    if out is None and workspace is None:
+        r = _fast().linear_backward(dy, X, W, pre, act, bool(need_dx), bool(need_dw), bias_dtype)
+        if r is not None:
+            return r
     import torch
     dev = _on_gpu(dy, "dy")
     dyd, lddy = _dtype_id(dy, "dy"), _rows(dy, "dy", dev)
@@ -1055,6 +1063,10 @@ def dropout(x, p: float, seed, offset: int = 0, residual=None, out_dtype=None, o
     offset tells calls with one seed apart.  x and residual are bf16 or fp32; the result has
     out_dtype, by default residual's dtype or x's.  `out` may supply its buffer, and may be x or
     residual."""
+    if out is None:
+        r = _fast().dropout(x, p, seed, offset, residual, out_dtype)
+        if r is not None:
+            return r
     import torch
     dev = _on_gpu(x, "x")
     xd, ldx = _dtype_id(x, "x"), _rows(x, "x", dev)
@@ -1135,6 +1147,10 @@ def token_logprobs(logits, tokens=None, ignore_index: int = -100, scale: float =
     the logits, equal ones by index; a logit of -inf is masked.  entropy is None without
     compute_entropy, the alternatives without n_top.  stats [M, 2] is what
     token_logprobs_backward needs of the rows.  `out` may supply the buffers."""
+    if out is None and workspace is None:
+        r = _fast().token_logprobs(logits, tokens, ignore_index, scale, n_top, bool(compute_entropy))
+        if r is not None:
+            return TokenLogprobs(*r)
     import torch
     dev = _on_gpu(logits, "logits")
     d, ldl = _dtype_id(logits, "logits"), _rows(logits, "logits", dev)
@@ -1170,6 +1186,11 @@ def token_logprobs_backward(logits, tokens, stats, entropy=None, top_ids=None, g
     """dlogits (logits' dtype) of token_logprobs, from the gradients of logprob, of top_logprob (with
     the forward's top_ids), of entropy (with the forward's entropy) and of lse; None counts as 0.  `out` may
     supply its buffer, and may be logits."""
+    if out is None:
+        r = _fast().token_logprobs_backward(logits, tokens, stats, entropy, top_ids, grad_logprob, grad_top,
+                                            grad_entropy, grad_lse, ignore_index, scale)
+        if r is not None:
+            return r
     import torch
     dev = _on_gpu(logits, "logits")
     d, ldl = _dtype_id(logits, "logits"), _rows(logits, "logits", dev)
