@@ -160,7 +160,7 @@ flce_status_t flce_linear_workspace(int64_t M, int64_t N, int64_t K, size_t* fwd
   if (st != FLCE_OK) return st;
   if (fwd_bytes) {
     const flce::LinearPlan p = flce::linear_forward_plan(M, N, K);
-    *fwd_bytes = M <= flce::kLinearFewRows ? 0 : align_up(flce::linear_part_bytes(p, M, N));
+    *fwd_bytes = flce::linear_takes_few(M, N, K) ? 0 : align_up(flce::linear_part_bytes(p, M, N));
   }
   if (bwd_bytes) *bwd_bytes = linear_backward_layout(M, N, K).total;
   return ok();
@@ -199,7 +199,7 @@ flce_status_t flce_linear_forward(const void* X, int64_t ldx, const void* W, int
   e.pre = static_cast<uint16_t*>(pre);
   e.ldp = long(ldp);
   hipError_t err;
-  if (M <= flce::kLinearFewRows) {
+  if (flce::linear_takes_few(M, N, K)) {
     err = flce::launch_linear_few(a, e, stream);
   } else {
     const flce::LinearPlan plan = flce::linear_forward_plan(M, N, K);
@@ -417,8 +417,7 @@ flce_status_t flce_token_logprobs_backward(const void* logits, int dtype, int64_
   a.grad_lse = grad_lse;
   a.dlogits = dlogits;
   a.ldd = long(ldd);
-  const bool vec = V % 8 == 0 && vectors(logits, dtype, ldl) && vectors(dlogits, dtype, ldd);
-  const hipError_t e = flce::launch_token_logprobs_grad(a, dtype, vec, stream);
+  const hipError_t e = flce::launch_token_logprobs_grad(a, dtype, stream);
   if (e != hipSuccess) return hip_fail(e, "token log-prob gradient kernel launch");
   return ok();
 }

@@ -79,7 +79,7 @@ struct TokenLogprobGradArgs {
   void* dlogits;
   long ldd;
 };
-hipError_t launch_token_logprobs_grad(const TokenLogprobGradArgs& a, int dtype, bool vec, hipStream_t s);
+hipError_t launch_token_logprobs_grad(const TokenLogprobGradArgs& a, int dtype, hipStream_t s);
 
 // ---------------------------------------------------------------- matrix product with an epilogue
 // Activations: the values of the C ABI's enumeration.
@@ -146,8 +146,9 @@ struct LinearGradArgs {
 };
 hipError_t launch_linear_grad(LinearGradArgs a, hipStream_t s);
 
-// A few rows of X: the weights streamed past them.
-constexpr int kLinearFewRows = 8;
+// A few rows of X: W streamed past them, up to kLinearDotRows of them by dot products.
+constexpr int kLinearFewRows = 32, kLinearDotRows = 2;
+bool linear_takes_few(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_few(const LinearProduct& a, const LinearEpilogue& e, hipStream_t s);
 
 // dpre = dy act'(pre) in bf16, and the column sums of its unrounded values.

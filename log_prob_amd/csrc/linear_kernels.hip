@@ -11,7 +11,7 @@
 // The rate of the matrix pipe bounds large products, the bytes of W small ones.  Tiles are
 // 256 x 256 where they fill the chip, smaller ones (two or three workgroups a compute unit)
 // otherwise; a long K over few tiles is split, the fp32 partial products added in order by a
-// second kernel.  A decoding step (up to 8 rows) has a kernel of its own that streams W.
+// second kernel.  A decoding step (up to 32 rows) has kernels of its own that stream W.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -328,20 +328,35 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearEpilogue e, cons
 }
 
 // ---------------------------------------------------------------------------
-// Up to MT <= 8 rows of X: W is read once, and bounds the call.  A wave takes R rows of W, its
+// One or two (MT) rows of X: W is read once, and bounds the call.  A wave takes R rows of W, its
 // lanes 8 consecutive K each (1 KiB of a row at once), in batches of U loads a row; the next
 // batch is in flight under the work on this one.  X lies in LDS, at most 64 KiB of it at a time,
 // staged under the first batch, and is read from there once for the R rows.  Products of a pair of
-// bf16 go through v_dot2: two multiplications and no unpacking (with unpacking and fp32 fused
-// multiply-adds 8 rows of X would take more time than the loads of W).
+// bf16 go through v_dot2: two multiplications and no unpacking.  1 x 4096 x 4096 8.7 us (3.9 TB/s, of
+// which 2.5 us are the launch's), 1 x 50257 x 1600 26.7 (6.0 TB/s); R of 1 or 4 and U of 1 or 4 are
+// up to 20% slower on one or the other.
+__device__ __forceinline__ float load1(const void* p, int dtype, long at) {
+  return dtype == kF32 ? static_cast<const float*>(p)[at] : Bf16::to_f32(static_cast<const uint16_t*>(p)[at]);
+}
+// The epilogue of one element.
+__device__ __forceinline__ void finish1(const LinearEpilogue& e, long m, int n, float v) {
+  if (e.bias) v += load1(e.bias, e.bias_dtype, n);
+  if (e.pre) e.pre[m * e.ldp + n] = Bf16::from_f32(v);
+  with_act(e.act, [&](auto a) { v = activate<decltype(a)::value>(v); });
+  if (e.residual) v += load1(e.residual, e.residual_dtype, m * e.ldr + n);
+  if (e.out_dtype == kF32) static_cast<float*>(e.out)[m * e.ldo + n] = v;
+  else static_cast<uint16_t*>(e.out)[m * e.ldo + n] = Bf16::from_f32(v);
+}
+
 constexpr int FEW_LDS = 64 * 1024;
-constexpr int few_rows(int mt) { return mt <= 2 ? 2 : 4; }
+typedef float f32x4_acc __attribute__((ext_vector_type(4)));
+constexpr int FEW_R = 2;
 typedef __bf16 bf16x2_v __attribute__((ext_vector_type(2)));
 
 template <int MT>
 __global__ __launch_bounds__(256) void linear_few_kernel(LinearProduct p, LinearEpilogue e, int k_stage) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  constexpr int R = few_rows(MT), U = 4 / R, NVAL = R * MT, BATCH = 512 * U;
+  constexpr int R = FEW_R, U = 2, NVAL = R * MT, BATCH = 512 * U;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const u32x4_t zero = {0u, 0u, 0u, 0u};
   u32x4_t* xs = reinterpret_cast<u32x4_t*>(smem);  // [MT][k_stage / 8]
@@ -420,18 +435,90 @@ __global__ __launch_bounds__(256) void linear_few_kernel(LinearProduct p, Linear
     float v = acc[0];
     for (; off > 0; off /= 2) v += __shfl_xor(v, off);
     const int r = which / MT, m = which % MT, n = n0 + r;
-    if ((lane & (64 / NVAL - 1)) == 0 && m < p.M && n < p.N) {
-      if (e.bias)
-        v += e.bias_dtype == kF32 ? static_cast<const float*>(e.bias)[n]
-                                  : Bf16::to_f32(static_cast<const uint16_t*>(e.bias)[n]);
-      if (e.pre) e.pre[m * e.ldp + n] = Bf16::from_f32(v);
-      with_act(e.act, [&](auto a) { v = activate<decltype(a)::value>(v); });
-      if (e.residual)
-        v += e.residual_dtype == kF32 ? static_cast<const float*>(e.residual)[m * e.ldr + n]
-                                      : Bf16::to_f32(static_cast<const uint16_t*>(e.residual)[m * e.ldr + n]);
-      if (e.out_dtype == kF32) static_cast<float*>(e.out)[m * e.ldo + n] = v;
-      else static_cast<uint16_t*>(e.out)[m * e.ldo + n] = Bf16::from_f32(v);
+    if ((lane & (64 / NVAL - 1)) == 0 && m < p.M && n < p.N) finish1(e, m, n, v);
+  }
+}
+
+// Up to 16 MB rows of X on the matrix instruction (16 x 16 x 32): a workgroup takes 16 rows of W,
+// 512 K a stage through a ring of LDS stages by direct-to-LDS loads of 1 KiB of one row each; its
+// four waves multiply 128 K of a stage each, and the four partial products meet in LDS and are
+// added in order.  X is staged beside W, from L2.  Chunk c (16 bytes) of row r lies at position c ^
+// (r % 16) of the row's 64, so that the 16 rows a fragment read touches fall on all banks.  (Loaded
+// straight into the instruction's operands, 64 bytes of 16 rows at once, 16 x 50257 x 1600 took 52 us.)
+template <int MB>
+struct StreamShape {
+  static constexpr int W_BYTES = 16 * 1024, STAGE = W_BYTES + MB * 16 * 1024;
+  static constexpr int NS = 3;                  // stages (4 and 5 no quicker, 2 slower by a fifth)
+  static constexpr int LOADS = 4 + 4 * MB;      // of a wave for a stage
+  static_assert(NS * STAGE <= 160 * 1024 && 4 * MB * 1024 <= NS * STAGE, "LDS");
+};
+
+template <int MB>
+__global__ __launch_bounds__(256) void linear_stream_kernel(LinearProduct p, LinearEpilogue e) {
+  using C = StreamShape<MB>;
+  __shared__ __attribute__((aligned(1024))) char smem[C::NS * C::STAGE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4, n0 = 16 * (int)blockIdx.x;
+  const int nk = (p.K + 511) / 512, wvalid = p.N - n0;
+  const i32x4 wr = make_rsrc_fixed(p.b + (long)n0 * p.ldb), xr = make_rsrc_fixed(p.a);
+  const uint32_t lds0 = lds_addr_of(smem), ldw = (uint32_t)p.ldb * 2u, ldx = (uint32_t)p.lda * 2u;
+  auto issue = [&](int k, int slot) {
+    const uint32_t st = lds0 + (uint32_t)(slot * C::STAGE);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * wave + i, c = 64 * k + (lane ^ row);
+      const bool ok = row < wvalid && 8 * c < p.K;
+      dma16<0>(wr, ok ? (uint32_t)row * ldw + 16u * (uint32_t)c : OOB_OFFSET, 0u, st + 1024u * (uint32_t)row);
     }
+#pragma unroll
+    for (int i = 0; i < 4 * MB; ++i) {
+      const int row = 4 * MB * wave + i, c = 64 * k + (lane ^ (row & 15));
+      const bool ok = row < p.M && 8 * c < p.K;
+      dma16<0>(xr, ok ? (uint32_t)row * ldx + 16u * (uint32_t)c : OOB_OFFSET, 0u,
+               st + (uint32_t)C::W_BYTES + 1024u * (uint32_t)row);
+    }
+  };
+  f32x4_acc acc[MB];
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) acc[mb] = f32x4_acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < C::NS - 1; ++k) issue(k, k);
+  int slot = 0;
+  for (int k = 0; k < nk; ++k) {
+    // stage k has landed, and every wave is done with stage k - 1, whose slot the next loads take
+    // (steps past K only zero-fill it)
+    wait_vmcnt<C::LOADS*(C::NS - 2)>();
+    __syncthreads();
+    issue(k + C::NS - 1, slot == 0 ? C::NS - 1 : slot - 1);
+    const char* st = smem + slot * C::STAGE;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = ((16 * wave + 4 * i + q) ^ r) << 4;
+      const bf16x8 w = *reinterpret_cast<const bf16x8*>(st + 1024 * r + at);
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const bf16x8 x = *reinterpret_cast<const bf16x8*>(st + C::W_BYTES + 1024 * (16 * mb + r) + at);
+        acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, x, acc[mb], 0, 0, 0);
+      }
+    }
+    slot = slot == C::NS - 1 ? 0 : slot + 1;
+  }
+  // the zero fills past the end must land before the LDS is used again
+  wait_vmcnt<0>();
+  __syncthreads();
+  // lane l, element j: row 4 (l / 16) + j of W, row l % 16 of X's block
+  float(*red)[MB][256] = reinterpret_cast<float(*)[MB][256]>(smem);
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) red[wave][mb][(4 * q + j) * 16 + r] = acc[mb][j];
+  __syncthreads();
+  // neighbouring threads take neighbouring columns of a row of the result
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    const int m = 16 * mb + (int)threadIdx.x / 16, c = threadIdx.x % 16, at = c * 16 + (int)threadIdx.x / 16;
+    const float v = ((red[0][mb][at] + red[1][mb][at]) + red[2][mb][at]) + red[3][mb][at];
+    if (m < p.M && c < wvalid) finish1(e, m, n0 + c, v);
   }
 }
 
@@ -545,7 +632,8 @@ int tiles_of(const LinearPlan& p, int64_t M, int64_t N) { return int(cdiv(M, p.t
 // of 64 K takes (measured at K = 4096, the tiles of one, two and three a unit): 64 x 128 0.52,
 // 0.64, 0.80 us; 128 x 128 0.60, 0.95; 256 x 256 1.05 with few units busy and 1.65 with all of them
 // (the clock).  A launch adds 3, a split a second launch and its partial products there and back
-// at the copy rate, which also bounds the operands.  E.g. (us; tile/splits):
+// at the copy rate; the operands come at 4.4 TB/s at
+// most.  E.g. (us; tile/splits):
 //   64 x 4096 x 4096     64/8 14.7, 128/8 15.4, 256/8 22, 64/1 35
 //   512 x 4096 x 4096    64/2 31, 128/2 32, 64/1 36, 256/4 40, 128/1 40
 //   1024 x 4096 x 4096   64/1 42, 128/1 43, 256/4 54, 256/1 69
@@ -564,7 +652,7 @@ double plan_time(const LinearPlan& p, int64_t M, int64_t N, int64_t K) {
   };
   const int64_t load = cdiv(n, 256);
   double t = steps * (double(load / resident) * step(resident) + step(int(load % resident))) + 3;
-  const double bytes = 2.0 * (double(M) * K + double(N) * K) / 5.0e6;
+  const double bytes = 2.0 * (double(M) * K + double(N) * K) / 4.4e6;
   if (t < bytes) t = bytes;
   if (p.splits > 1) t += 4.5 + 8.0 * p.splits * double(M) * double(N) / 5.0e6;
   return t;
@@ -649,16 +737,35 @@ hipError_t launch_linear_grad(LinearGradArgs a, hipStream_t s) {
   return err;
 }
 
+// Whether a call takes the kernels for few rows: by dot products always, on the matrix instruction
+// where they are quicker than the tiles.  A workgroup a compute unit: a round takes 0.65 us and, for
+// each 512 K, 0.45 to 0.7 as more units are busy (0.2 more past 16 rows).  (us, these and tiles: 16 x
+// 4096 x 4096 9.6, 15; 32 x 4096 x 4096 11.6, 15.6; 16 x 11008 x 4096 22, 28; 16 x 1024 x 8192 10.8,
+// 14; 4 x 50257 x 1600 45, 35; 32 x 50257 x 1600 65, 36.)
+bool linear_takes_few(int64_t M, int64_t N, int64_t K) {
+  if (M <= kLinearDotRows) return true;
+  if (M > kLinearFewRows) return false;
+  double tiles;
+  best_plan(M, N, K, 64, 256, &tiles);
+  const double groups = double(cdiv(N, 16)), busy = groups < 256 ? groups / 256 : 1;
+  const double stage = 0.45 + 0.25 * busy + (M <= 16 ? 0.0 : 0.2);
+  return double(cdiv(int64_t(groups), 256)) * (0.65 + double(cdiv(K, 512)) * stage) + 2.5 < tiles;
+}
+
 hipError_t launch_linear_few(const LinearProduct& p, const LinearEpilogue& e, hipStream_t s) {
-  const int MT = p.M <= 1 ? 1 : p.M <= 2 ? 2 : p.M <= 4 ? 4 : 8;
+  if (p.M > kLinearDotRows) {
+    const unsigned groups = (unsigned)((p.N + 15) / 16);
+    if (p.M <= 16) linear_stream_kernel<1><<<groups, 256, 0, s>>>(p, e);
+    else linear_stream_kernel<2><<<groups, 256, 0, s>>>(p, e);
+    return hipGetLastError();
+  }
+  const int MT = p.M <= 1 ? 1 : 2;
   const int most = FEW_LDS / (2 * MT), k_stage = p.K < most ? p.K : most;
   const size_t lds = size_t(MT) * size_t(k_stage) * 2;
-  const int per = 4 * few_rows(MT), groups = (p.N + per - 1) / per;
+  const int per = 4 * FEW_R, groups = (p.N + per - 1) / per;
   const unsigned grid = (unsigned)(groups < 1024 ? groups : 1024);
   if (MT == 1) linear_few_kernel<1><<<grid, 256, lds, s>>>(p, e, k_stage);
-  else if (MT == 2) linear_few_kernel<2><<<grid, 256, lds, s>>>(p, e, k_stage);
-  else if (MT == 4) linear_few_kernel<4><<<grid, 256, lds, s>>>(p, e, k_stage);
-  else linear_few_kernel<8><<<grid, 256, lds, s>>>(p, e, k_stage);
+  else linear_few_kernel<2><<<grid, 256, lds, s>>>(p, e, k_stage);
   return hipGetLastError();
 }
 

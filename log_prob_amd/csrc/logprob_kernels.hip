@@ -342,15 +342,16 @@ struct Raw8 {
   }
 };
 
-template <class TX>
-__device__ __forceinline__ void load_step(Raw8<TX> (&raw)[NV<TX>], const typename TX::mem* x, int base, int v1) {
+// The logits of [base, v1) of the next N vectors of every thread.
+template <class TX, int N>
+__device__ __forceinline__ void load_step(Raw8<TX> (&raw)[N], const typename TX::mem* x, int base, int v1) {
   const int col = base + 8 * (int)threadIdx.x;
-  if (base + STEP<TX> <= v1) {
+  if (base + N * VEC_STEP <= v1) {
 #pragma unroll
-    for (int j = 0; j < NV<TX>; ++j) raw[j].load(x + col + j * VEC_STEP);
+    for (int j = 0; j < N; ++j) raw[j].load(x + col + j * VEC_STEP);
   } else {
 #pragma unroll
-    for (int j = 0; j < NV<TX>; ++j) {
+    for (int j = 0; j < N; ++j) {
       const int c = col + j * VEC_STEP;
       if (c + 8 <= v1) raw[j].load(x + c);
       else raw[j].load_part(x + c, v1 - c);
@@ -562,6 +563,7 @@ __global__ __launch_bounds__(T) void token_logprob_join_kernel(TokenLogprobArgs 
 // (from the logits, so dlogits may be the logits' own memory) and written over the rest after a
 // barrier; several entries of one token are added in their order.
 constexpr int LIST = kMaxTokens + kMaxTop;
+static_assert(LIST % 8 == 0, "groups of 8");
 constexpr int GRAD_NV = 4, GRAD_STEP = GRAD_NV * VEC_STEP;
 
 struct GradShared {
@@ -573,7 +575,7 @@ struct GradShared {
   int any[T / 64];
 };
 
-template <class TX, bool VEC>
+template <class TX>
 __global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradArgs p, int pieces) {
   __shared__ GradShared sh;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -584,12 +586,8 @@ __global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradA
     const int v0 = (int)(item - row * pieces) * GRAD_STEP, v1 = min(p.V, v0 + GRAD_STEP);
     const typename TX::mem* x = static_cast<const typename TX::mem*>(p.logits) + row * p.ldl;
     typename TX::mem* dx = static_cast<typename TX::mem*>(p.dlogits) + row * p.ldd;
-    Chunk8<TX, VEC> raw[GRAD_NV];
-#pragma unroll
-    for (int j = 0; j < GRAD_NV; ++j) {
-      const int col = v0 + j * VEC_STEP + 8 * tid;
-      raw[j].load(x, col, col < v1 ? (long)p.V : 0l);
-    }
+    Raw8<TX> raw[GRAD_NV];
+    load_step<TX>(raw, x, v0, v1);
     const float top = p.stats[2 * row], logs = p.stats[2 * row + 1];
     const float b = p.grad_entropy ? p.grad_entropy[row] : 0.f, ent = p.grad_entropy ? p.entropy[row] : 0.f;
     const float of_lse = p.grad_lse ? p.grad_lse[row] : 0.f;
@@ -597,6 +595,10 @@ __global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradA
     // the list of (token, gradient): their sum, and those of this piece
     float sum = 0.f;
     bool any = false;
+    if (tid < 8 && L + tid < LIST) {
+      sh.id[L + tid] = -1;
+      sh.g[L + tid] = 0.f;
+    }
     for (int j = tid; j < L; j += T) {
       const bool given = j < p.n_tokens;
       const long at = given ? row * p.n_tokens + j : row * p.n_top + (j - p.n_tokens);
@@ -637,11 +639,17 @@ __global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradA
       const int id = zero ? -1 : sh.id[j];
       int first = -1;  // the first entry of this token
       float g = 0.f;
-      if (id >= 0)
-        for (int i = L - 1; i >= 0; --i)
-          if (sh.id[i] == id) first = i;
-      if (first == j)
-        for (int i = j; i < L; ++i) g += sh.id[i] == id ? sh.g[i] : 0.f;
+      if (id >= 0) {
+        first = j;
+        // (whole groups of 8: the list is padded with entries of no token)
+        for (int i0 = 0; i0 < L; i0 += 8)
+#pragma unroll
+          for (int i = i0; i < i0 + 8; ++i) {
+            const bool same = sh.id[i] == id;
+            first = same ? min(first, i) : first;
+            g += same ? sh.g[i] : 0.f;
+          }
+      }
       sh.at[j] = first == j ? id : -1;
       if (first == j) sh.value[j] = fmaf(p.scale, g, slope(TX::to_f32(x[id]))) + add_nan;
     }
@@ -652,10 +660,10 @@ __global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradA
     for (int j = 0; j < GRAD_NV; ++j) {
       const int col = v0 + j * VEC_STEP + 8 * tid;
       float v[8];
-      raw[j].value(col, p.V, v);
+      raw[j].value(v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = zero ? 0.f : slope(v[i]) + add_nan;
-      if (col < v1) store8<TX, VEC>(dx, col, p.V, v);
+      if (col < v1) store8<TX, false>(dx, col, p.V, v);
     }
     wait_vmcnt<0>();
     __syncthreads();
@@ -701,17 +709,12 @@ hipError_t launch_token_logprobs(const TokenLogprobArgs& a, int dtype, hipStream
   return hipGetLastError();
 }
 
-hipError_t launch_token_logprobs_grad(const TokenLogprobGradArgs& a, int dtype, bool vec, hipStream_t s) {
+hipError_t launch_token_logprobs_grad(const TokenLogprobGradArgs& a, int dtype, hipStream_t s) {
   const int pieces = (a.V + GRAD_STEP - 1) / GRAD_STEP;
   const long items = a.M * pieces, most = 1 << 22;
   const unsigned grid = (unsigned)(items < most ? items : most);
-  if (dtype == kF32) {
-    if (vec) token_logprob_grad_kernel<F32, true><<<grid, T, 0, s>>>(a, pieces);
-    else token_logprob_grad_kernel<F32, false><<<grid, T, 0, s>>>(a, pieces);
-  } else {
-    if (vec) token_logprob_grad_kernel<Bf16, true><<<grid, T, 0, s>>>(a, pieces);
-    else token_logprob_grad_kernel<Bf16, false><<<grid, T, 0, s>>>(a, pieces);
-  }
+  if (dtype == kF32) token_logprob_grad_kernel<F32><<<grid, T, 0, s>>>(a, pieces);
+  else token_logprob_grad_kernel<Bf16><<<grid, T, 0, s>>>(a, pieces);
   return hipGetLastError();
 }
 

@@ -79,10 +79,10 @@ def test_linear_backward(want, kw):
 
 
 def test_workspaces():
-    assert flce.linear_workspace(1, 4096, 4096)[0] == 0 == flce.linear_workspace(8, 50257, 8192)[0]
+    assert flce.linear_workspace(1, 4096, 4096)[0] == 0 == flce.linear_workspace(16, 4096, 4096)[0]
     assert flce.linear_workspace(0, 16, 8)[0] == 0
     assert flce.linear_workspace(8192, 8192, 8192)[0] == 0
-    assert flce.linear_workspace(16, 4096, 4096)[0] > 0
+    assert flce.linear_workspace(64, 4096, 4096)[0] > 0
     assert flce.linear_workspace(5, 33, 64)[1] >= 5 * 40 * 2 + 33 * 4
     assert flce.token_logprobs_workspace(0, 1000, 5) == 0 == flce.token_logprobs_workspace(4096, 128256, 20)
     assert flce.token_logprobs_workspace(1, 128256, 5) > 0
