@@ -147,8 +147,7 @@ def linear(x, weight, bias=None, activation=None, residual=None, out_dtype=None)
     """Differentiable act(x weight^T + bias) + residual over the last axis of x, as
     flce.linear_forward: x and weight bf16, bias and residual bf16 or fp32, y bf16 (the default) or
     fp32.  residual has y's shape.  The graph keeps x and, with an activation, its argument in bf16.
-    To capture forward and backward in a graph, first let go of eager results that lead back to the
-    same leaves (see layer_norm)."""
+    For a backward captured into a graph see layer_norm."""
     if residual is not None and residual.shape != (*x.shape[:-1], weight.shape[0]):
         raise ValueError(f"residual: expected shape {(*x.shape[:-1], weight.shape[0])}, got {tuple(residual.shape)}")
     return FusedLinear.apply(x, weight, bias, activation, residual, out_dtype)
@@ -180,7 +179,8 @@ class FusedDropout(torch.autograd.Function):
 
 def dropout(x, p: float, seed, offset: int = 0, residual=None, out_dtype=None):
     """Differentiable residual + dropout(x) over x [..., H], as flce.dropout (rows are those of x as
-    a matrix of H columns).  No mask is kept; a seed given as a tensor is copied."""
+    a matrix of H columns).  No mask is kept; a seed given as a tensor is copied.  For a backward
+    captured into a graph see layer_norm."""
     if residual is not None and residual.shape != x.shape:
         raise ValueError(f"residual: expected shape {tuple(x.shape)}, got {tuple(residual.shape)}")
     return FusedDropout.apply(x, p, seed, offset, residual, out_dtype)
@@ -214,5 +214,6 @@ class LogitsLogprobs(torch.autograd.Function):
 def token_logprobs(logits, tokens=None, ignore_index: int = -100, scale: float = 1.0, n_top: int = 0,
                    compute_entropy: bool = False):
     """flce.token_logprobs with gradients of logprob, lse, entropy and top_logprob with respect to
-    the logits [M, V]; stats carries none.  The graph keeps the logits."""
+    the logits [M, V]; stats carries none.  The graph keeps the logits.  For a backward captured into
+    a graph see layer_norm."""
     return flce.TokenLogprobs(*LogitsLogprobs.apply(logits, tokens, ignore_index, scale, n_top, compute_entropy))

@@ -638,7 +638,13 @@ int tiles_of(const LinearPlan& p, int64_t M, int64_t N) { return int(cdiv(M, p.t
 //   512 x 4096 x 4096    64/2 31, 128/2 32, 64/1 36, 256/4 40, 128/1 40
 //   1024 x 4096 x 4096   64/1 42, 128/1 43, 256/4 54, 256/1 69
 //   2048 x 4096 x 4096   128/1 62, 256/1 74, 64/1 87
-//   4096 x 4096 x 4096   256/1 106, 128/1 121, 64/1 153
+//   4096 x 4096 x 4096   256/1 101, 128/1 113, 64/1 146
+// Operands past about 100 MB come from memory in earnest, which slows the small tiles' steps more,
+// as they load more for a product:
+//   257 x 50257 x 1600   128/1 83, 256/1 90, 64/1 92
+//   1024 x 32768 x 2048  256/1 117, 128/1 165, 64/1 197
+// (Other shapes of tiles: 128 x 128 with 32 K a stage and three workgroups a unit 10 to 30% slower
+// than 128/1 throughout, 128 x 256 with one workgroup 2 to 30%.)
 double plan_time(const LinearPlan& p, int64_t M, int64_t N, int64_t K) {
   const int64_t n = int64_t(tiles_of(p, M, N)) * p.splits;
   const double steps = double(cdiv(p.k_each, 64));
@@ -651,9 +657,11 @@ double plan_time(const LinearPlan& p, int64_t M, int64_t N, int64_t K) {
     return r == 1 ? 0.54 : r == 2 ? 0.64 : 0.80;
   };
   const int64_t load = cdiv(n, 256);
-  double t = steps * (double(load / resident) * step(resident) + step(int(load % resident))) + 3;
-  const double bytes = 2.0 * (double(M) * K + double(N) * K) / 4.4e6;
-  if (t < bytes) t = bytes;
+  double t = steps * (double(load / resident) * step(resident) + step(int(load % resident)));
+  const double bytes = 2.0 * (double(M) * K + double(N) * K);
+  if (bytes > 100e6) t *= p.tile_m == 256 ? 1.08 : p.tile_m == 128 ? 1.3 : 1.5;
+  t += 3;
+  if (t < bytes / 4.4e6) t = bytes / 4.4e6;
   if (p.splits > 1) t += 4.5 + 8.0 * p.splits * double(M) * double(N) / 5.0e6;
   return t;
 }
