@@ -80,6 +80,18 @@ def test_shapes(M, N, K):
         check_backward(s, act, pre, dy, (torch.float32, torch.bfloat16, None)[i % 3], f"{M}x{N}x{K} {act}")
 
 
+# where one kernel hands over to the next: dot products, W streamed for 16 and 32 rows, tiles
+EDGES = [(2, 4099, 1032), (3, 16, 8), (16, 17, 520), (17, 4100, 512), (20, 33, 1032), (32, 15, 4096), (32, 8200, 64),
+         (33, 130, 2048), (4, 40000, 72), (30, 60001, 136), (192, 16500, 320), (260, 20000, 1600)]
+
+
+@pytest.mark.parametrize("M,N,K", EDGES)
+def test_edges_between_kernels(M, N, K):
+    for i, (act, res) in enumerate((("gelu", "fp32"), (None, "bf16"))):
+        check_forward(make(M, N, K, M + N + K + i, bias="bf16", residual=res), act, ("fp32", "bf16")[i],
+                      f"{M}x{N}x{K} {act}")
+
+
 @pytest.mark.parametrize("M,N,K,act", [(4096, 4096, 256, "gelu"), (3000, 5003, 320, None), (4100, 3900, 72, "silu")])
 def test_large_tiles(M, N, K, act):
     import torch
