@@ -15,6 +15,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "block_internal.h"
 #include "mainloop_device.h"
 #include "mx_device.h"
@@ -170,7 +172,8 @@ template <class S>
 struct Slice {
   static constexpr int WN = S::WN, ROWS = 64, BLOCKS = ROWS / 32, COLS8 = WN / 8, PER = 64 / COLS8;
   static constexpr int STEPS = ROWS / PER, HALF = STEPS / 2;
-  static_assert(S::MB % BLOCKS == 0 && S::NWAVES * ROWS * WN * 4 <= S::PIPE_BYTES, "slices");
+  static constexpr int BYTES = S::NWAVES * ROWS * WN * 4;
+  static_assert(S::MB % BLOCKS == 0, "slices");
   float* sl;
   int lane, row0;  // the slice's first row in D
   __device__ __forceinline__ int row(int it) const { return PER * it + lane / COLS8; }
@@ -279,18 +282,10 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[S::MB][S::NB], ch
   static_assert(S::MB / L::BLOCKS <= 2, "slices");
 }
 
-// Workgroup `id` of n_mt x n_nt tiles times `splits` shares of K.  Workgroups of one XCD take
-// neighbouring tiles of the same share (groups of 8 tile rows).
+// The tile at (m0, n0) and share `split` of K.
 template <class S, bool A_KC, bool B_KC>
-__device__ __forceinline__ void run_tile(char* smem, int id, const LinearProduct& p, const LinearEpilogue& e,
-                                         float* part, const LinearPlan& plan) {
-  const int n_mt = (p.M + S::TM - 1) / S::TM, n_nt = (p.N + S::TN - 1) / S::TN;
-  const int tiles = n_mt * n_nt, per = tiles * plan.splits >> 3;
-  const int L = id < (per << 3) ? (id & 7) * per + (id >> 3) : id;
-  const int split = L / tiles;
-  int mt, nt;
-  group_coords(L - split * tiles, n_mt, n_nt, 8, mt, nt);
-  const int m0 = mt * S::TM, n0 = nt * S::TN;
+__device__ __forceinline__ void product_tile(char* smem, int m0, int n0, int split, const LinearProduct& p,
+                                             const LinearEpilogue& e, float* part, const LinearPlan& plan) {
   const int k0 = split * plan.k_each, k1 = min(p.K, k0 + plan.k_each);
   const TileSrc A{A_KC ? p.a + (long)m0 * p.lda + k0 : p.a + (long)k0 * p.lda + m0, p.lda, p.M - m0,
                   min(p.kvalid_a, k1) - k0, 0};
@@ -303,11 +298,37 @@ __device__ __forceinline__ void run_tile(char* smem, int id, const LinearProduct
   store_tile<S, A_KC && B_KC>(acc, smem, e, mine, ldpart, p.M, p.N, m0, n0);
 }
 
+// Workgroup `id` of n_mt x n_nt tiles times `splits` shares of K.  Workgroups of one XCD take
+// neighbouring tiles of the same share (groups of 8 tile rows).  The last tile row is one of the
+// lower shape T where that holds it.
+template <class S, class T, bool A_KC, bool B_KC>
+__device__ __forceinline__ void run_tile(char* smem, int id, const LinearProduct& p, const LinearEpilogue& e,
+                                         float* part, const LinearPlan& plan) {
+  static_assert(T::TN == S::TN && T::PIPE_BYTES <= S::PIPE_BYTES && T::NTHREADS == S::NTHREADS, "lower shape");
+  static_assert(Slice<S>::BYTES <= S::PIPE_BYTES && Slice<T>::BYTES <= S::PIPE_BYTES, "slices");
+  const int n_mt = (p.M + S::TM - 1) / S::TM, n_nt = (p.N + S::TN - 1) / S::TN;
+  const int tiles = n_mt * n_nt, per = tiles * plan.splits >> 3;
+  const int L = id < (per << 3) ? (id & 7) * per + (id >> 3) : id;
+  const int split = L / tiles;
+  int mt, nt;
+  group_coords(L - split * tiles, n_mt, n_nt, 8, mt, nt);
+  const int m0 = mt * S::TM, n0 = nt * S::TN;
+  if constexpr (T::TM < S::TM) {
+    if (p.M - m0 <= T::TM) return product_tile<T, A_KC, B_KC>(smem, m0, n0, split, p, e, part, plan);
+  }
+  product_tile<S, A_KC, B_KC>(smem, m0, n0, split, p, e, part, plan);
+}
+
+using Tile128 = Shape<128, 128, 64, 2, 2>;
+using Tile64 = Shape<64, 128, 64, 2, 2, 1, 4>;
+template <class S>
+using Lower = std::conditional_t<S::TM == 256, Shape<128, 256, 64, 2, 1>, Tile64>;
+
 template <class S>
 __global__ __launch_bounds__(S::NTHREADS, S::WAVES_PER_EU) void linear_tile_kernel(LinearProduct p, LinearEpilogue e,
                                                                                   float* part, LinearPlan plan) {
   __shared__ __attribute__((aligned(1024))) char smem[S::PIPE_BYTES];
-  run_tile<S, true, true>(smem, blockIdx.x, p, e, part, plan);
+  run_tile<S, Lower<S>, true, true>(smem, blockIdx.x, p, e, part, plan);
 }
 
 // The partial products of a split K, added in order, and the epilogue: 8 columns a thread.
@@ -619,27 +640,24 @@ __global__ __launch_bounds__(256, SX::WAVES_PER_EU) void linear_grad_kernel(Line
   __shared__ __attribute__((aligned(1024))) char smem[LDS];
   int id = blockIdx.x;
   if (id < p.n_dw) {
-    run_tile<SW, false, false>(smem, id, p.dw, p.out_dw, p.part_dw, p.plan_dw);
+    run_tile<SW, SW, false, false>(smem, id, p.dw, p.out_dw, p.part_dw, p.plan_dw);
     return;
   }
   id -= p.n_dw;
   if (id < p.n_dx) {
-    run_tile<SX, true, false>(smem, id, p.dx, p.out_dx, p.part_dx, p.plan_dx);
+    run_tile<SX, SX, true, false>(smem, id, p.dx, p.out_dx, p.part_dx, p.plan_dx);
     return;
   }
   bias_sum(smem, id - p.n_dx, p.bias);
 }
 
 // ---------------------------------------------------------------------------
-using Tile128 = Shape<128, 128, 64, 2, 2>;
-using Tile64 = Shape<64, 128, 64, 2, 2, 1, 4>;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int tiles_of(const LinearPlan& p, int64_t M, int64_t N) { return int(cdiv(M, p.tile_m) * cdiv(N, p.tile_n)); }
 
 // A plan's time in us.  Workgroups go to the 256 compute units in turn, `resident` at once.  A step
-// of 64 K takes (measured at K = 4096, the tiles of one, two and three a unit): 64 x 128 0.52,
-// 0.64, 0.80 us; 128 x 128 0.60, 0.95; 256 x 256 1.05 with few units busy and 1.65 with all of them
+// of 64 K takes (measured at K = 4096, the tiles of one, two and three a unit): 64 x 128 0.54,
+// 0.64, 0.83 us; 128 x 128 0.60, 0.90; 256 x 256 1.05 with few units busy and 1.65 with all of them
 // (the clock).  A launch adds 3, a split a second launch and its partial products there and back
 // at the copy rate; the operands come at 4.4 TB/s at
 // most.  E.g. (us; tile/splits):
@@ -654,19 +672,32 @@ int tiles_of(const LinearPlan& p, int64_t M, int64_t N) { return int(cdiv(M, p.t
 //   1024 x 32768 x 2048  256/1 117, 128/1 165, 64/1 197
 // (Other shapes of tiles: 128 x 128 with 32 K a stage and three workgroups a unit 10 to 30% slower
 // than 128/1 throughout, 128 x 256 with one workgroup 2 to 30%.)
-double plan_time(const LinearPlan& p, int64_t M, int64_t N, int64_t K) {
-  const int64_t n = int64_t(tiles_of(p, M, N)) * p.splits;
+//
+// `lower`: the last tile row is half as high where that holds it, which a unit takes beside
+// another tile for 0.12 us a step, alone for 0.5 (tiles of 256 0.9).  (us, without it and with:
+// 1025 x 4096 x 4096 55, 46; 2100 x 8192 x 2048 94, 82; 4097 x 4096 x 4096 171, 150;
+// 257 x 50257 x 1600 101, 97.  dX of the gradients won 0 to 2% from it and goes without.)
+double plan_time(const LinearPlan& p, int64_t M, int64_t N, int64_t K, bool lower) {
+  const int64_t columns = cdiv(N, p.tile_n) * p.splits, n = cdiv(M, p.tile_m) * columns;
+  const int64_t over = M % p.tile_m;
+  const int64_t low = lower && p.tile_m > 64 && over > 0 && over <= p.tile_m / 2 ? columns : 0;
   const double steps = double(cdiv(p.k_each, 64));
   const int resident = p.tile_m == 256 ? 1 : p.tile_m == 128 ? 2 : 3;
   const double full = double(n) / 256 < 1 ? double(n) / 256 : 1;
   auto step = [&](int r) {
     if (r == 0) return 0.0;
     if (p.tile_m == 256) return 1.05 + 0.6 * full * full;
-    if (p.tile_m == 128) return r == 1 ? 0.60 : 0.95;
-    return r == 1 ? 0.54 : r == 2 ? 0.64 : 0.80;
+    if (p.tile_m == 128) return r == 1 ? 0.60 : 0.90;
+    return r == 1 ? 0.54 : r == 2 ? 0.64 : 0.83;
   };
-  const int64_t load = cdiv(n, 256);
-  double t = steps * (double(load / resident) * step(resident) + step(int(load % resident)));
+  int64_t load = cdiv(n - low, 256), more = cdiv(n, 256) - load;  // tiles a unit, and lower ones
+  if (load == 0) {
+    load = more;
+    more = 0;
+  }
+  double t = double(load / resident) * step(resident) + step(int(load % resident));
+  t += double(more) * (p.tile_m == 256 ? 0.9 : load % resident ? 0.12 : 0.5);
+  t *= steps;
   const double bytes = 2.0 * (double(M) * K + double(N) * K);
   if (bytes > 100e6) t *= p.tile_m == 256 ? 1.08 : p.tile_m == 128 ? 1.3 : 1.5;
   t += 3;
@@ -685,14 +716,14 @@ LinearPlan plan_of(int tile, int64_t splits, int64_t K) {
   return p;
 }
 // The quickest plan among the tiles from `least` to `most`.
-LinearPlan best_plan(int64_t M, int64_t N, int64_t K, int least, int most, double* time) {
+LinearPlan best_plan(int64_t M, int64_t N, int64_t K, int least, int most, bool lower, double* time) {
   LinearPlan best{};
   *time = 1e30;
   for (int tile = least; tile <= most; tile *= 2)
     for (int64_t splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
       if (splits > 1 && K / splits < 128) break;
       const LinearPlan p = plan_of(tile, splits, K);
-      const double t = plan_time(p, M, N, K);
+      const double t = plan_time(p, M, N, K, lower);
       if (t < *time) {
         *time = t;
         best = p;
@@ -713,15 +744,15 @@ hipError_t join(const LinearProduct& p, const LinearPlan& plan, const LinearEpil
 
 LinearPlan linear_forward_plan(int64_t M, int64_t N, int64_t K) {
   double t;
-  return best_plan(M, N, K, 64, 256, &t);
+  return best_plan(M, N, K, 64, 256, true, &t);
 }
 
 void linear_backward_plans(int64_t M, int64_t N, int64_t K, LinearPlan* dx, LinearPlan* dw) {
   // both run in one launch: large tiles for both, or small ones (dW's operands are read by
   // columns, which takes tiles of 128 at least)
   double big_x, big_w, small_x, small_w;
-  const LinearPlan bx = best_plan(M, K, N, 256, 256, &big_x), bw = best_plan(N, K, M, 256, 256, &big_w);
-  const LinearPlan sx = best_plan(M, K, N, 64, 128, &small_x), sw = best_plan(N, K, M, 128, 128, &small_w);
+  const LinearPlan bx = best_plan(M, K, N, 256, 256, false, &big_x), bw = best_plan(N, K, M, 256, 256, false, &big_w);
+  const LinearPlan sx = best_plan(M, K, N, 64, 128, false, &small_x), sw = best_plan(N, K, M, 128, 128, false, &small_w);
   const bool big = big_x + big_w < small_x + small_w;
   *dx = big ? bx : sx;
   *dw = big ? bw : sw;
@@ -763,7 +794,7 @@ bool linear_takes_few(int64_t M, int64_t N, int64_t K) {
   if (M <= kLinearDotRows) return true;
   if (M > kLinearFewRows) return false;
   double tiles;
-  best_plan(M, N, K, 64, 256, &tiles);
+  best_plan(M, N, K, 64, 256, true, &tiles);
   const double groups = double(cdiv(N, 16)), busy = groups < 256 ? groups / 256 : 1;
   const double stage = 0.45 + 0.25 * busy + (M <= 16 ? 0.0 : 0.2);
   return double(cdiv(int64_t(groups), 256)) * (0.65 + double(cdiv(K, 512)) * stage) + 2.5 < tiles;
