@@ -92,6 +92,15 @@ def test_edges_between_kernels(M, N, K):
                       f"{M}x{N}x{K} {act}")
 
 
+# a last tile row of half the height or less, of just more, and one of a split K; tiles of 128 and 256
+@pytest.mark.parametrize("M,N,K", [(1025, 4096, 72), (320, 9001, 1024), (577, 4100, 1032), (300, 4090, 4096),
+                                   (513, 20001, 328), (2176, 4096, 256), (2177, 4099, 256)])
+def test_last_tile_row(M, N, K):
+    for i, (act, res) in enumerate((("silu", "bf16"), (None, "fp32"))):
+        check_forward(make(M, N, K, 2 * M + N + K + i, bias="fp32", residual=res), act, ("bf16", "fp32")[i],
+                      f"{M}x{N}x{K} {act}")
+
+
 @pytest.mark.parametrize("M,N,K,act", [(4096, 4096, 256, "gelu"), (3000, 5003, 320, None), (4100, 3900, 72, "silu")])
 def test_large_tiles(M, N, K, act):
     import torch
