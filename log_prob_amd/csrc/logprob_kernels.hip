@@ -21,12 +21,11 @@
 // nothing.
 //
 // Measured (us): 4096 x 128256 bf16 without alternatives 202 (5.2 TB/s, the copy rate; the entropy
-// adds 5), with 20 of them 231 to 246; 2048 x 128256 fp32 with 20 214; 257 x 50257 fp32 without 17.5, with 8
-// 26; 4 x 128256 fp32 with 5 12.7, 7.8 of it the pieces and 4 to 5 the joining kernel.  What the
-// alternatives cost is a row's fixed part, in which loads of the next step only are in flight: the
-// first threshold, two barriers a step, the last thinning (4096 x 32768 bf16: 74 with 5, 114 with
-// 50).  Whole-wave maxima by DPP instead of shuffles and 4 to 6 workgroups a unit change nothing
-// past 1%.
+// adds 5), with 20 of them 231 to 246; 2048 x 128256 fp32 with 20 214; 257 x 50257 fp32 without
+// 17.5, with 8 26; 4 x 128256 fp32 with 5 12.7, 7.6 of it the pieces and 4 to 5 the joining kernel.
+// What the alternatives cost is a row's fixed part, in which only the next step's loads are in
+// flight: the first threshold, two barriers a step, the last thinning (4096 x 32768 bf16: 74 with
+// 5, 114 with 50).  Whole-wave maxima by DPP instead of shuffles gain 1% at most.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
