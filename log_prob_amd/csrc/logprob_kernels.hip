@@ -25,7 +25,7 @@
 // 17.5, with 8 26; 4 x 128256 fp32 with 5 12.7, 7.6 of it the pieces and 4 to 5 the joining kernel.
 // What the alternatives cost is a row's fixed part, in which only the next step's loads are in
 // flight: the first threshold, two barriers a step, the last thinning (4096 x 32768 bf16: 74 with
-// 5, 114 with 50).  Whole-wave maxima by DPP instead of shuffles gain 1% at most.
+// 5, 115 with 50).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -394,11 +394,12 @@ __device__ __forceinline__ void offer_in_parts(Shared& sh, const typename TX::me
   }
 }
 
-// The next step's loads are in flight under the work on this one.  (Registers for five workgroups a
-// unit are too few in bf16, which then keeps 10 a thread in memory: 240 us against 231 at 4096 x
-// 128256 with 20 alternatives and a token.)
+// The next step's loads are in flight under the work on this one.  (Without the entropy a row's
+// steps are short, and registers for five workgroups a unit too few in bf16, which then keeps 10 a
+// thread in memory: 246 us against 239 at 4096 x 128256 with 20 alternatives.  With it five are
+// better: 247 against 252, and 115 against 127 at 4096 x 32768 with 50.)
 template <class TX, bool ENT, bool TOP>
-__global__ __launch_bounds__(T, 4) void token_logprob_kernel(TokenLogprobArgs p) {
+__global__ __launch_bounds__(T, ENT ? 5 : 4) void token_logprob_kernel(TokenLogprobArgs p) {
   __shared__ Shared sh;
   const int tid = threadIdx.x, k = p.n_top, crowded = CROWDED + 3 * k;
   const float c = p.scale * LOG2E;
