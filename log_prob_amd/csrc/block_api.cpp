@@ -103,6 +103,7 @@ struct LinearBackwardLayout {
 LinearBackwardLayout linear_backward_layout(int64_t M, int64_t N, int64_t K) {
   LinearBackwardLayout L;
   flce::linear_backward_plans(M, N, K, &L.dx, &L.dw);
+  if (flce::linear_takes_few_dx(M, K)) L.dx = flce::linear_few_dx_plan(N, K);
   L.ldd = (N + 7) / 8 * 8;
   L.groups = flce::linear_slope_groups(M, N);
   L.off_sum = align_up(size_t(M) * size_t(L.ldd) * 2);
@@ -233,7 +234,7 @@ flce_status_t flce_linear_backward(const void* dy, int dy_dtype, int64_t lddy, c
   }
   if (dW && (st = check_matrix("dW", dW, FLCE_BF16, lddw, K)) != FLCE_OK) return st;
   const LinearBackwardLayout L = linear_backward_layout(M, N, K);
-  if (dX && (st = check_grid(L.dx, M, K)) != FLCE_OK) return st;
+  if (dX && !flce::linear_takes_few_dx(M, K) && (st = check_grid(L.dx, M, K)) != FLCE_OK) return st;
   if (dW && (st = check_grid(L.dw, N, K)) != FLCE_OK) return st;
   if ((st = check_workspace(workspace, workspace_bytes, L.total, "linear backward")) != FLCE_OK) return st;
   char* ws = static_cast<char*>(workspace);
@@ -243,7 +244,8 @@ flce_status_t flce_linear_backward(const void* dy, int dy_dtype, int64_t lddy, c
                      lddy <= kMaxOperandStride;
   const uint16_t* dpre = as_is ? static_cast<const uint16_t*>(dy) : reinterpret_cast<const uint16_t*>(ws);
   const int64_t ldd = as_is ? lddy : L.ldd;
-  const bool write = !as_is && (dX || dW);
+  const bool few = flce::linear_takes_few_dx(M, K);
+  const bool write = !as_is && (dW || (dX && !few));
   if (M > 0 && (write || dbias)) {
     flce::LinearSlopeArgs a{};
     a.dy = dy;
@@ -262,9 +264,28 @@ flce_status_t flce_linear_backward(const void* dy, int dy_dtype, int64_t lddy, c
     const hipError_t e = flce::launch_linear_slope(a, stream);
     if (e != hipSuccess) return hip_fail(e, "activation gradient kernel launch");
   }
+  if (dX && M > 0 && few) {
+    flce::LinearFewDx a{};
+    a.dy = dy;
+    a.dy_dtype = dy_dtype;
+    a.lddy = long(lddy);
+    a.pre = act ? static_cast<const uint16_t*>(pre) : nullptr;
+    a.ldp = long(ldp);
+    a.act = activation;
+    a.w = static_cast<const uint16_t*>(W);
+    a.ldw = long(ldw);
+    a.M = int(M);
+    a.N = int(N);
+    a.K = int(K);
+    a.dx = static_cast<uint16_t*>(dX);
+    a.lddx = long(lddx);
+    a.part = reinterpret_cast<float*>(ws + L.off_dx);
+    const hipError_t e = flce::launch_linear_few_dx(a, L.dx, stream);
+    if (e != hipSuccess) return hip_fail(e, "linear gradient kernel launch");
+  }
   flce::LinearGradArgs g{};
   const int64_t N8 = (N + 7) / 8 * 8;
-  if (dX && M > 0) {
+  if (dX && M > 0 && !few) {
     g.dx = {dpre, static_cast<const uint16_t*>(W), long(ldd), long(ldw), int(M), int(K), int(N8), int(N8), int(N)};
     g.out_dx.out = dX;
     g.out_dx.out_dtype = FLCE_BF16;

@@ -170,4 +170,25 @@ struct LinearSlopeArgs {
 int linear_slope_groups(int64_t M, int64_t N);
 hipError_t launch_linear_slope(const LinearSlopeArgs& a, hipStream_t s);
 
+// dX of up to kLinearFewDx rows and 1024 values from dy and pre themselves.
+constexpr int kLinearFewDx = 4;
+inline bool linear_takes_few_dx(int64_t M, int64_t K) { return M <= kLinearFewDx && M * K <= 1024; }
+struct LinearFewDx {
+  const void* dy;
+  int dy_dtype;
+  long lddy;
+  const uint16_t* pre;     // bf16 [M, N], or nullptr without an activation
+  long ldp;
+  int act;
+  const uint16_t* w;       // [N, K]
+  long ldw;
+  int M, N, K;
+  uint16_t* dx;            // [M, K]
+  long lddx;
+  float* part;             // [splits][M][K]
+  int each, splits, lanes; // set by the launch: n a workgroup, shares, lanes along a row of W
+};
+LinearPlan linear_few_dx_plan(int64_t N, int64_t K);
+hipError_t launch_linear_few_dx(LinearFewDx a, const LinearPlan& plan, hipStream_t s);
+
 }  // namespace flce

@@ -612,6 +612,73 @@ __global__ __launch_bounds__(256) void linear_slope_kernel(LinearSlopeArgs p) {
   }
 }
 
+// dX of up to 4 rows and 1024 values: dX[m] = sum_n dpre[m, n] W[n], with dpre in fp32.  The rounding
+// to bf16 that the matrix instruction asks for adds as much to dX as the store's own, 1.4 times
+// together, on average; over so few values it can be more (1 x 37832 x 104: 2.4 to 2.7e-3 of the
+// norm, this way 1.6e-3).  For more of them the tiles are right and quicker (4 x 4096 x 4096 29
+// us against 43).  A workgroup takes 512 columns and a share of n, 128 of which have their dpre in LDS at a
+// time; a wave's lanes lie along a row of W, several rows at once where K is short.  The waves' and
+// rows' sums meet in LDS, the shares in the joining kernel, both in a fixed order.
+constexpr int DX_STAGE = 128, DX_COLS = 512;
+template <class TY>
+__global__ __launch_bounds__(256) void linear_few_dx_kernel(LinearFewDx p) {
+  __shared__ float d[kLinearFewDx][DX_STAGE];
+  __shared__ __attribute__((aligned(16))) float red[256][8];
+  const int tid = threadIdx.x, col0 = blockIdx.x * DX_COLS, lanes = p.lanes;
+  const int col = col0 + 8 * (tid & (lanes - 1)), sub = tid / lanes, subs = 256 / lanes;
+  const int n0 = blockIdx.y * p.each, n1 = min(p.N, n0 + p.each);
+  float acc[kLinearFewDx][8];
+#pragma unroll
+  for (int m = 0; m < kLinearFewDx; ++m)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[m][i] = 0.f;
+  for (int base = n0; base < n1; base += DX_STAGE) {
+    __syncthreads();
+#pragma unroll
+    for (int i = tid; i < kLinearFewDx * DX_STAGE; i += 256) {
+      const int m = i / DX_STAGE, n = base + i % DX_STAGE;
+      float v = 0.f;
+      if (m < p.M && n < n1) {
+        v = TY::to_f32(static_cast<const typename TY::mem*>(p.dy)[m * p.lddy + n]);
+        if (p.pre) v *= slope(Bf16::to_f32(p.pre[m * p.ldp + n]), p.act);
+      }
+      d[m][i % DX_STAGE] = v;
+    }
+    __syncthreads();
+    const int here = min(DX_STAGE, n1 - base);
+    if (col < p.K) {
+#pragma unroll 8
+      for (int j = sub; j < here; j += subs) {
+        const u32x4_t u = *reinterpret_cast<const u32x4_t*>(p.w + (long)(base + j) * p.ldw + col);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float w = i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
+#pragma unroll
+          for (int m = 0; m < kLinearFewDx; ++m) acc[m][i] = fmaf(d[m][j], w, acc[m][i]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < kLinearFewDx; ++m) {
+    if (m >= p.M) break;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[tid][i] = acc[m][i];
+    __syncthreads();
+    if (tid < lanes && col < p.K) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = red[tid][i];
+      for (int r = 1; r < subs; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += red[r * lanes + tid][i];
+      if (p.splits > 1) store_any(p.part, kF32, ((long)blockIdx.y * p.M + m) * p.K, col, p.K, v);
+      else store_any(p.dx, kBf16, m * p.lddx, col, p.K, v);
+    }
+  }
+}
+
 // The groups' column sums added in order: 32 columns a workgroup, 8 shares of the groups.
 __device__ __forceinline__ void bias_sum(char* smem, int id, const LinearBiasSum& b) {
   float(*red)[32] = reinterpret_cast<float(*)[32]>(smem);
@@ -677,7 +744,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // `lower`: the last tile row is half as high where that holds it, which a unit takes beside
 // another tile for 0.12 us a step, alone for 0.5 (tiles of 256 0.9).  (us, without it and with:
 // 1025 x 4096 x 4096 55, 46; 2100 x 8192 x 2048 94, 82; 4097 x 4096 x 4096 171, 150;
-// 257 x 50257 x 1600 101, 97.  dX of the gradients won 0 to 2% from it and goes without.)
+// 257 x 50257 x 1600 101, 97.  The gradients' products, several of which share a launch, go without.)
 double plan_time(const LinearPlan& p, int64_t M, int64_t N, int64_t K, bool lower) {
   const int64_t columns = cdiv(N, p.tile_n) * p.splits, n = cdiv(M, p.tile_m) * columns;
   const int64_t over = M % p.tile_m;
@@ -816,6 +883,37 @@ hipError_t launch_linear_few(const LinearProduct& p, const LinearEpilogue& e, hi
   if (MT == 1) linear_few_kernel<1><<<grid, 256, lds, s>>>(p, e, k_stage);
   else linear_few_kernel<2><<<grid, 256, lds, s>>>(p, e, k_stage);
   return hipGetLastError();
+}
+
+// Shares of n: enough workgroups to fill the chip, few enough to join.
+LinearPlan linear_few_dx_plan(int64_t N, int64_t K) {
+  LinearPlan p = plan_of(64, 1, N);
+  const int64_t blocks = cdiv(K, DX_COLS), want = cdiv(512, blocks), most = cdiv(N, DX_STAGE);
+  int64_t splits = want < 96 ? want : 96;
+  if (splits > most) splits = most;
+  p.k_each = int(cdiv(N, splits));
+  p.splits = int(cdiv(N, p.k_each));
+  return p;
+}
+
+hipError_t launch_linear_few_dx(LinearFewDx a, const LinearPlan& plan, hipStream_t s) {
+  a.each = plan.k_each;
+  a.splits = plan.splits;
+  a.lanes = 1;
+  while (a.lanes < 64 && 8 * a.lanes < a.K) a.lanes *= 2;
+  const dim3 grid((unsigned)cdiv(a.K, DX_COLS), (unsigned)a.splits);
+  if (a.dy_dtype == kF32) linear_few_dx_kernel<F32><<<grid, 256, 0, s>>>(a);
+  else linear_few_dx_kernel<Bf16><<<grid, 256, 0, s>>>(a);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || a.splits == 1) return err;
+  LinearProduct p{};
+  p.M = a.M;
+  p.N = a.K;
+  LinearEpilogue e{};
+  e.out = a.dx;
+  e.out_dtype = kBf16;
+  e.ldo = a.lddx;
+  return join(p, plan, e, a.part, s);
 }
 
 int linear_slope_groups(int64_t M, int64_t N) {

@@ -101,6 +101,18 @@ def test_last_tile_row(M, N, K):
                       f"{M}x{N}x{K} {act}")
 
 
+# dX of few rows and values, and just past them; N of one share, a ragged one and many
+@pytest.mark.parametrize("M,N,K", [(1, 37832, 104), (1, 1, 1024), (4, 50257, 256), (3, 129, 336), (2, 3000, 512),
+                                   (1, 130, 1032), (4, 4096, 264), (1, 20001, 8)])
+def test_gradient_of_few_values(M, N, K):
+    import torch
+    for i, act in enumerate(("silu", None)):
+        s = make(M, N, K, 3 * M + N + K + i, bias="fp32")
+        y, pre = check_forward(s, act, "bf16", f"{M}x{N}x{K} {act}")
+        for dy in (s["dy"].float(), s["dy"].bfloat16()):
+            check_backward(s, act, pre, dy, torch.float32, f"{M}x{N}x{K} {act} {dy.dtype}")
+
+
 @pytest.mark.parametrize("M,N,K,act", [(4096, 4096, 256, "gelu"), (3000, 5003, 320, None), (4100, 3900, 72, "silu")])
 def test_large_tiles(M, N, K, act):
     import torch
