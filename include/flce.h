@@ -570,10 +570,10 @@ flce_status_t flce_token_logprobs(const void* logits, int dtype, int64_t ldl, in
  *                     - b[m] p[m, v] (log p[m, v] + entropy[m]) + c[m] p[m, v])
  * over the given tokens with grad_logprob [M, n_tokens] and the alternatives with grad_top [M,
  * n_top] (NULL: none of them), b = grad_entropy [M] (NULL: 0; needs the forward's entropy), c =
- * grad_lse [M] (NULL: 0).  Ignored
+ * grad_lse [M] (NULL: 0).  The terms with p are 0 where p is 0 in fp32, at any scale and b.  Ignored
  * and invalid tokens add nothing; a token given several times adds each of its gradients.  dlogits
  * has the logits' type, any row stride, and may be their own memory.  Rows that nothing valid is
- * asked of, and rows masked throughout, get zeros.
+ * asked of, and rows masked throughout, get zeros; a NaN gradient reaches every element of its row.
  */
 flce_status_t flce_token_logprobs_backward(const void* logits, int dtype, int64_t ldl, int64_t M,
                                            int64_t V, const int64_t* tokens, int64_t n_tokens,

@@ -641,13 +641,15 @@ __global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradA
     }
     // a row that nothing is asked of, or in which everything is masked, has no gradient
     const bool zero = (!any && b == 0.f && of_lse == 0.f) || top == -INFINITY;
-    const float c0 = zero ? 0.f : p.scale * (of_lse - fmaf(b, ent, sum)), c1 = zero ? 0.f : -p.scale * b;
+    // dx = scale (g + p_v (k0 - b logp_v)), 0 where p_v is 0 however large its factor.  scale comes last:
+    // scale b times a log-prob of some hundred may pass fp32's range where dx does not.
+    const float k0 = of_lse - fmaf(b, ent, sum);
     auto slope = [&](float v) {
-      const float lp = fmaxf(fmaf(p.scale, v - top, -logs), -1e30f);
-      return __builtin_amdgcn_exp2f(lp * LOG2E) * fmaf(c1, lp, c0);
+      const float lp = fmaf(p.scale, v - top, -logs), pv = __builtin_amdgcn_exp2f(lp * LOG2E);
+      return pv > 0.f ? pv * fmaf(-b, lp, k0) : 0.f;
     };
-    // (a NaN in the row's statistics has to reach every element: fmaxf alone would drop it)
-    const float add_nan = zero ? 0.f : 0.f * (top + logs);
+    // (a NaN in the row's statistics or gradients has to reach every element: the choice would drop it)
+    const float add_nan = zero ? 0.f : 0.f * (top + logs) + (k0 != k0 ? k0 : 0.f);
 
     for (int j = tid; j < L; j += T) {
       const int id = zero ? -1 : sh.id[j];
@@ -665,7 +667,7 @@ __global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradA
           }
       }
       sh.at[j] = first == j ? id : -1;
-      if (first == j) sh.value[j] = fmaf(p.scale, g, slope(TX::to_f32(x[id]))) + add_nan;
+      if (first == j) sh.value[j] = p.scale * (g + slope(TX::to_f32(x[id]))) + add_nan;
     }
     // (every read of these logits by hand is done before any is overwritten)
     wait_vmcnt<0>();
@@ -676,7 +678,7 @@ __global__ __launch_bounds__(T) void token_logprob_grad_kernel(TokenLogprobGradA
       float v[8];
       raw[j].value(v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = zero ? 0.f : slope(v[i]) + add_nan;
+      for (int i = 0; i < 8; ++i) v[i] = zero ? 0.f : fmaf(p.scale, slope(v[i]), add_nan);
       if (col < v1) store8<TX, false>(dx, col, p.V, v);
     }
     wait_vmcnt<0>();
