@@ -106,9 +106,9 @@ def _as_rows(t, cols):
 
 
 def _as_operand(t, cols):
-    """_as_rows with 16-byte aligned rows, as the matrix product takes them."""
+    """_as_rows with rows as the matrix product takes them: 16-byte aligned, at most 2^21 elements apart."""
     t = _as_rows(t, cols)
-    if t.data_ptr() % 16 or (t.shape[0] > 1 and t.stride(0) % 8):
+    if t.data_ptr() % 16 or (t.shape[0] > 1 and (t.stride(0) % 8 or t.stride(0) > 1 << 21)):
         t = t.clone(memory_format=torch.contiguous_format)
     return t
 
