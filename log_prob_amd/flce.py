@@ -52,6 +52,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         return _lib
     if not os.path.exists(path):
         raise ImportError(f"libflce.so not built at {path}; run `python -m log_prob_amd.build`")
+    try:
+        # torch brings a HIP runtime of its own: loaded first, it is the one that libflce.so binds to
+        import torch  # noqa: F401
+    except ImportError:
+        pass
     lib = ctypes.CDLL(path)
     c = ctypes
     P, I64, SZ = c.c_void_p, c.c_int64, c.c_size_t
