@@ -493,7 +493,11 @@ typedef enum {
   FLCE_ACT_SILU = 4
 } flce_activation_t;
 
-/* Workspace bytes of flce_linear_forward and flce_linear_backward (either output may be NULL). */
+/*
+ * Workspace bytes of flce_linear_forward and flce_linear_backward (either output may be NULL).  Sizes
+ * whose tiles do not fit a launch (results of half a terabyte and more) are refused here as in the call
+ * (the backward's: with every gradient wanted).
+ */
 flce_status_t flce_linear_workspace(int64_t M, int64_t N, int64_t K, size_t* fwd_bytes,
                                     size_t* bwd_bytes);
 flce_status_t flce_linear_forward(const void* X, int64_t ldx, const void* W, int64_t ldw,

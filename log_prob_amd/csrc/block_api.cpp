@@ -87,8 +87,7 @@ flce_status_t check_linear(int64_t M, int64_t N, int64_t K) {
 bool is_activation(int a) { return a >= FLCE_ACT_NONE && a <= FLCE_ACT_SILU; }
 
 flce_status_t check_grid(const flce::LinearPlan& p, int64_t M, int64_t N) {
-  // (half of what a launch can hold: the gradient's has two products)
-  if (flce::linear_workgroups(p, M, N) > flce::kMaxWorkgroups / 2 - (1 << 16))
+  if (!flce::linear_fits(p, M, N))
     return fail(FLCE_ERR_UNSUPPORTED, "too many tiles for one launch (%lld x %lld)", (long long)M, (long long)N);
   return FLCE_OK;
 }
@@ -160,10 +159,19 @@ flce_status_t flce_linear_workspace(int64_t M, int64_t N, int64_t K, size_t* fwd
   flce_status_t st = check_linear(M, N, K);
   if (st != FLCE_OK) return st;
   if (fwd_bytes) {
-    const flce::LinearPlan p = flce::linear_forward_plan(M, N, K);
-    *fwd_bytes = flce::linear_takes_few(M, N, K) ? 0 : align_up(flce::linear_part_bytes(p, M, N));
+    *fwd_bytes = 0;
+    if (!flce::linear_takes_few(M, N, K)) {
+      const flce::LinearPlan p = flce::linear_forward_plan(M, N, K);
+      if ((st = check_grid(p, M, N)) != FLCE_OK) return st;
+      *fwd_bytes = align_up(flce::linear_part_bytes(p, M, N));
+    }
   }
-  if (bwd_bytes) *bwd_bytes = linear_backward_layout(M, N, K).total;
+  if (bwd_bytes) {
+    const LinearBackwardLayout L = linear_backward_layout(M, N, K);
+    if (!flce::linear_takes_few_dx(M, K) && (st = check_grid(L.dx, M, K)) != FLCE_OK) return st;
+    if ((st = check_grid(L.dw, N, K)) != FLCE_OK) return st;
+    *bwd_bytes = L.total;
+  }
   return ok();
 }
 

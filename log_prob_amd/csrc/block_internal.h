@@ -120,6 +120,11 @@ struct LinearPlan {
 LinearPlan linear_forward_plan(int64_t M, int64_t N, int64_t K);
 void linear_backward_plans(int64_t M, int64_t N, int64_t K, LinearPlan* dx, LinearPlan* dw);
 int64_t linear_workgroups(const LinearPlan& p, int64_t M, int64_t N);
+// Whether a launch can hold the product's workgroups: half of its limit each, as the gradient's has
+// two products, and some beside them.
+inline bool linear_fits(const LinearPlan& p, int64_t M, int64_t N) {
+  return linear_workgroups(p, M, N) <= kMaxWorkgroups / 2 - (1 << 16);
+}
 inline int64_t linear_part_ld(int64_t N) { return (N + 7) / 8 * 8; }
 inline size_t linear_part_bytes(const LinearPlan& p, int64_t M, int64_t N) {
   return p.splits > 1 ? size_t(p.splits) * size_t(M) * size_t(linear_part_ld(N)) * 4 : 0;

@@ -783,14 +783,16 @@ LinearPlan plan_of(int tile, int64_t splits, int64_t K) {
   p.splits = int(cdiv(k, p.k_each));
   return p;
 }
-// The quickest plan among the tiles from `least` to `most`.
+// The quickest plan among the tiles from `least` to `most` that a launch can hold (time 1e30, and the
+// largest tiles, where none is).
 LinearPlan best_plan(int64_t M, int64_t N, int64_t K, int least, int most, bool lower, double* time) {
-  LinearPlan best{};
+  LinearPlan best = plan_of(most, 1, K);
   *time = 1e30;
   for (int tile = least; tile <= most; tile *= 2)
     for (int64_t splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
       if (splits > 1 && K / splits < 128) break;
       const LinearPlan p = plan_of(tile, splits, K);
+      if (!linear_fits(p, M, N)) break;
       const double t = plan_time(p, M, N, K, lower);
       if (t < *time) {
         *time = t;
