@@ -511,9 +511,9 @@ flce_status_t flce_linear_forward(const void* X, int64_t ldx, const void* W, int
  * Backward of it, from the forward's pre (unused without an activation; relu's slope at 0 is 0):
  *   dpre = dy act'(pre),  dX = dpre W,  dW = dpre^T X,  dbias = sum_m dpre
  * (the residual's gradient is dy itself).  dy bf16 or fp32; dX [M, K] and dW [N, K] bf16 with any
- * row strides; dbias [N] bf16 or fp32; each may be NULL.  dpre is rounded to bf16 for the two
- * products (the operands of the matrix instruction), not for dbias.  X is needed for dW, W for
- * dX.  M = 0 writes zeros to dW and dbias.  No atomics: bitwise repeatable.  workspace as above,
+ * row strides; dbias [N] bf16 or fp32; each may be NULL.  dpre is rounded to bf16 for dW and dX
+ * (the operands of the matrix instruction), not for dbias nor for a dX of M K <= 1024 values, over
+ * which the roundings do not average out.  X is needed for dW, W for dX.  M = 0 writes zeros to dW and dbias.  No atomics: bitwise repeatable.  workspace as above,
  * with the backward bytes.
  */
 flce_status_t flce_linear_backward(const void* dy, int dy_dtype, int64_t lddy, const void* pre,

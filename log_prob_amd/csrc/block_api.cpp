@@ -102,7 +102,7 @@ struct LinearBackwardLayout {
 LinearBackwardLayout linear_backward_layout(int64_t M, int64_t N, int64_t K) {
   LinearBackwardLayout L;
   flce::linear_backward_plans(M, N, K, &L.dx, &L.dw);
-  if (flce::linear_takes_few_dx(M, K)) L.dx = flce::linear_few_dx_plan(N, K);
+  if (M > 0 && flce::linear_takes_few_dx(M, K)) L.dx = flce::linear_few_dx_plan(M, N, K);
   L.ldd = (N + 7) / 8 * 8;
   L.groups = flce::linear_slope_groups(M, N);
   L.off_sum = align_up(size_t(M) * size_t(L.ldd) * 2);

@@ -175,9 +175,9 @@ struct LinearSlopeArgs {
 int linear_slope_groups(int64_t M, int64_t N);
 hipError_t launch_linear_slope(const LinearSlopeArgs& a, hipStream_t s);
 
-// dX of up to kLinearFewDx rows and 1024 values from dy and pre themselves.
-constexpr int kLinearFewDx = 4;
-inline bool linear_takes_few_dx(int64_t M, int64_t K) { return M <= kLinearFewDx && M * K <= 1024; }
+// dX of up to kLinearFewDx values from dy and pre themselves.
+constexpr int kLinearFewDx = 1024;
+inline bool linear_takes_few_dx(int64_t M, int64_t K) { return M * K <= kLinearFewDx; }
 struct LinearFewDx {
   const void* dy;
   int dy_dtype;
@@ -193,7 +193,7 @@ struct LinearFewDx {
   float* part;             // [splits][M][K]
   int each, splits, lanes; // set by the launch: n a workgroup, shares, lanes along a row of W
 };
-LinearPlan linear_few_dx_plan(int64_t N, int64_t K);
+LinearPlan linear_few_dx_plan(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_few_dx(LinearFewDx a, const LinearPlan& plan, hipStream_t s);
 
 }  // namespace flce

@@ -612,37 +612,38 @@ __global__ __launch_bounds__(256) void linear_slope_kernel(LinearSlopeArgs p) {
   }
 }
 
-// dX of up to 4 rows and 1024 values: dX[m] = sum_n dpre[m, n] W[n], with dpre in fp32.  The rounding
-// to bf16 that the matrix instruction asks for adds as much to dX as the store's own, 1.4 times
-// together, on average; over so few values it can be more (1 x 37832 x 104: 2.4 to 2.7e-3 of the
-// norm, this way 1.6e-3).  For more of them the tiles are right and quicker (4 x 4096 x 4096 29
-// us against 43).  A workgroup takes 512 columns and a share of n, 128 of which have their dpre in LDS at a
-// time; a wave's lanes lie along a row of W, several rows at once where K is short.  The waves' and
-// rows' sums meet in LDS, the shares in the joining kernel, both in a fixed order.
-constexpr int DX_STAGE = 128, DX_COLS = 512;
+// dX of up to 1024 values: dX[m] = sum_n dpre[m, n] W[n], with dpre in fp32.  The rounding to bf16
+// that the matrix instruction asks for adds as much to dX as the store's own, 1.4 times together, on
+// average; the fewer values, the further from that average (1 x 37832 x 104: 2.4 to 2.7e-3 of the
+// norm, this way 1.6e-3).  It costs a few us (dX and dbias in a graph, this way and by tiles: 5 x 3000 x
+// 200 19, 14; 16 x 50257 x 64 33, 27; 128 x 4096 x 8 19, 15).  For more values the tiles are right, and
+// quicker by more (4 x 4096 x 4096 29 us against 43).  A workgroup takes 4 rows, 512 columns and a share of n, 128 of which have their dpre
+// in LDS at a time; a wave's lanes lie along a row of W, several rows at once where K is short.  The
+// lanes' sums meet by exchange, the waves' in LDS, the shares' in the joining kernel, in a fixed order.
+constexpr int DX_ROWS = 4, DX_STAGE = 128, DX_COLS = 512;
 template <class TY>
 __global__ __launch_bounds__(256) void linear_few_dx_kernel(LinearFewDx p) {
-  __shared__ float d[kLinearFewDx][DX_STAGE];
-  __shared__ __attribute__((aligned(16))) float red[256][8];
-  const int tid = threadIdx.x, col0 = blockIdx.x * DX_COLS, lanes = p.lanes;
+  __shared__ float d[DX_ROWS][DX_STAGE];
+  __shared__ __attribute__((aligned(16))) float red[4][DX_ROWS][DX_COLS];
+  const int tid = threadIdx.x, m0 = DX_ROWS * (int)blockIdx.z, col0 = blockIdx.x * DX_COLS, lanes = p.lanes;
   const int col = col0 + 8 * (tid & (lanes - 1)), sub = tid / lanes, subs = 256 / lanes;
   const int n0 = blockIdx.y * p.each, n1 = min(p.N, n0 + p.each);
-  float acc[kLinearFewDx][8];
+  float acc[DX_ROWS][8];
 #pragma unroll
-  for (int m = 0; m < kLinearFewDx; ++m)
+  for (int m = 0; m < DX_ROWS; ++m)
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[m][i] = 0.f;
   for (int base = n0; base < n1; base += DX_STAGE) {
     __syncthreads();
 #pragma unroll
-    for (int i = tid; i < kLinearFewDx * DX_STAGE; i += 256) {
-      const int m = i / DX_STAGE, n = base + i % DX_STAGE;
+    for (int i = tid; i < DX_ROWS * DX_STAGE; i += 256) {
+      const int m = m0 + i / DX_STAGE, n = base + i % DX_STAGE;
       float v = 0.f;
       if (m < p.M && n < n1) {
         v = TY::to_f32(static_cast<const typename TY::mem*>(p.dy)[m * p.lddy + n]);
         if (p.pre) v *= slope(Bf16::to_f32(p.pre[m * p.ldp + n]), p.act);
       }
-      d[m][i % DX_STAGE] = v;
+      d[i / DX_STAGE][i % DX_STAGE] = v;
     }
     __syncthreads();
     const int here = min(DX_STAGE, n1 - base);
@@ -654,28 +655,35 @@ __global__ __launch_bounds__(256) void linear_few_dx_kernel(LinearFewDx p) {
         for (int i = 0; i < 8; ++i) {
           const float w = i & 1 ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
 #pragma unroll
-          for (int m = 0; m < kLinearFewDx; ++m) acc[m][i] = fmaf(d[m][j], w, acc[m][i]);
+          for (int m = 0; m < DX_ROWS; ++m) acc[m][i] = fmaf(d[m][j], w, acc[m][i]);
         }
       }
     }
   }
+  // the rows of W that share a wave, then the waves in order
+  for (int off = 32; off >= lanes; off >>= 1) {
 #pragma unroll
-  for (int m = 0; m < kLinearFewDx; ++m) {
-    if (m >= p.M) break;
-    __syncthreads();
+    for (int m = 0; m < DX_ROWS; ++m)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) red[tid][i] = acc[m][i];
-    __syncthreads();
-    if (tid < lanes && col < p.K) {
-      float v[8];
+      for (int i = 0; i < 8; ++i) acc[m][i] += __shfl_xor(acc[m][i], off);
+  }
+  if ((tid & 63) < lanes) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = red[tid][i];
-      for (int r = 1; r < subs; ++r)
+    for (int m = 0; m < DX_ROWS; ++m)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += red[r * lanes + tid][i];
-      if (p.splits > 1) store_any(p.part, kF32, ((long)blockIdx.y * p.M + m) * p.K, col, p.K, v);
-      else store_any(p.dx, kBf16, m * p.lddx, col, p.K, v);
+      for (int i = 0; i < 8; ++i) red[tid >> 6][m][8 * (tid & 63) + i] = acc[m][i];
+  }
+  __syncthreads();
+  const int m = m0 + tid / lanes;
+  if (tid < DX_ROWS * lanes && m < p.M && col < p.K) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = 8 * (tid & (lanes - 1)) + i;
+      v[i] = ((red[0][m - m0][c] + red[1][m - m0][c]) + red[2][m - m0][c]) + red[3][m - m0][c];
     }
+    if (p.splits > 1) store_any(p.part, kF32, ((long)blockIdx.y * p.M + m) * p.K, col, p.K, v);
+    else store_any(p.dx, kBf16, m * p.lddx, col, p.K, v);
   }
 }
 
@@ -888,9 +896,9 @@ hipError_t launch_linear_few(const LinearProduct& p, const LinearEpilogue& e, hi
 }
 
 // Shares of n: enough workgroups to fill the chip, few enough to join.
-LinearPlan linear_few_dx_plan(int64_t N, int64_t K) {
+LinearPlan linear_few_dx_plan(int64_t M, int64_t N, int64_t K) {
   LinearPlan p = plan_of(64, 1, N);
-  const int64_t blocks = cdiv(K, DX_COLS), want = cdiv(512, blocks), most = cdiv(N, DX_STAGE);
+  const int64_t blocks = cdiv(K, DX_COLS) * cdiv(M, DX_ROWS), want = cdiv(512, blocks), most = cdiv(N, DX_STAGE);
   int64_t splits = want < 96 ? want : 96;
   if (splits > most) splits = most;
   p.k_each = int(cdiv(N, splits));
@@ -903,7 +911,7 @@ hipError_t launch_linear_few_dx(LinearFewDx a, const LinearPlan& plan, hipStream
   a.splits = plan.splits;
   a.lanes = 1;
   while (a.lanes < 64 && 8 * a.lanes < a.K) a.lanes *= 2;
-  const dim3 grid((unsigned)cdiv(a.K, DX_COLS), (unsigned)a.splits);
+  const dim3 grid((unsigned)cdiv(a.K, DX_COLS), (unsigned)a.splits, (unsigned)cdiv(a.M, DX_ROWS));
   if (a.dy_dtype == kF32) linear_few_dx_kernel<F32><<<grid, 256, 0, s>>>(a);
   else linear_few_dx_kernel<Bf16><<<grid, 256, 0, s>>>(a);
   const hipError_t err = hipGetLastError();
