@@ -481,9 +481,10 @@ flce_status_t flce_mx_forward(const void* X, const void* W_codes, const void* W_
  * 0 <= M <= 2^30 (0: nothing is touched), 1 <= N <= 2^20, K a multiple of 8 up to 2^20.  Rows of
  * X and W are 16-byte aligned, with row strides (elements) up to 2^21; the other matrices are
  * naturally aligned with any row strides >= N (rows of multiples of 8 elements at 16-byte aligned
- * addresses move fastest).  out may be residual where their types and strides agree.  workspace:
- * 256-byte aligned, at least the forward bytes of flce_linear_workspace (0: may be NULL).  Results
- * are bitwise repeatable; the order of summation depends on the shape.
+ * addresses move fastest).  out may be residual where their types and strides agree (otherwise the
+ * call is refused).  workspace: 256-byte aligned, at least the forward bytes of
+ * flce_linear_workspace (0: may be NULL).  Results are bitwise repeatable; the order of summation
+ * depends on the shape.
  */
 typedef enum {
   FLCE_ACT_NONE = 0,
@@ -535,7 +536,8 @@ flce_status_t flce_linear_backward(const void* dy, int dy_dtype, int64_t lddy, c
  * there.  A call needs a (seed, offset) of its own for masks of its own.  x, residual and y are
  * bf16 or fp32 each, with any row strides, naturally aligned; 0 <= p <= 1 (1: everything is
  * dropped); sums in fp32; a dropped infinity or NaN is gone.  0 <= M <= 2^30 (0: nothing is
- * touched), 1 <= H <= 2^20.  y may be x or residual where their types and strides agree.
+ * touched), 1 <= H <= 2^20.  y may be x or residual where their types and strides agree (otherwise
+ * the call is refused).
  */
 flce_status_t flce_dropout(const void* x, int x_dtype, int64_t ldx, const void* residual,
                            int residual_dtype, int64_t ldr, int64_t M, int64_t H, double p,

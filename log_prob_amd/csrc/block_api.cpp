@@ -48,6 +48,14 @@ flce_status_t check_matrix(const char* name, const void* p, int dtype, int64_t l
   return FLCE_OK;
 }
 
+// A result in an input's place: every element has to lie where it did (a single row has no stride).
+flce_status_t check_in_place(const char* name, const void* p, int dtype, int64_t ld, const char* result,
+                             const void* out, int out_dtype, int64_t ldo, int64_t M) {
+  if (p == out && (dtype != out_dtype || (M > 1 && ld != ldo)))
+    return fail(FLCE_ERR_INVALID_VALUE, "%s in %s's place must have its type and row stride", result, name);
+  return FLCE_OK;
+}
+
 // Whether 8 elements can be moved by whole 16-byte accesses.
 bool vectors(const void* p, int dtype, int64_t ld) {
   return !p || (is_aligned(p, 16) && ld * int64_t(bytes_of(dtype)) % 16 == 0);
@@ -133,6 +141,8 @@ flce_status_t flce_dropout(const void* x, int x_dtype, int64_t ldx, const void* 
   if ((st = check_matrix("x", x, x_dtype, ldx, H)) != FLCE_OK) return st;
   if ((st = check_matrix("y", y, y_dtype, ldy, H)) != FLCE_OK) return st;
   if (residual && (st = check_matrix("residual", residual, residual_dtype, ldr, H)) != FLCE_OK) return st;
+  if ((st = check_in_place("x", x, x_dtype, ldx, "y", y, y_dtype, ldy, M)) != FLCE_OK) return st;
+  if ((st = check_in_place("residual", residual, residual_dtype, ldr, "y", y, y_dtype, ldy, M)) != FLCE_OK) return st;
   flce::DropoutArgs a{};
   a.x = x;
   a.ldx = long(ldx);
@@ -190,6 +200,8 @@ flce_status_t flce_linear_forward(const void* X, int64_t ldx, const void* W, int
   if ((st = check_operand("W", W, ldw, K)) != FLCE_OK) return st;
   if ((st = check_matrix("out", out, out_dtype, ldo, N)) != FLCE_OK) return st;
   if (residual && (st = check_matrix("residual", residual, residual_dtype, ldr, N)) != FLCE_OK) return st;
+  if ((st = check_in_place("residual", residual, residual_dtype, ldr, "out", out, out_dtype, ldo, M)) != FLCE_OK)
+    return st;
   if (pre && (st = check_matrix("pre", pre, FLCE_BF16, ldp, N)) != FLCE_OK) return st;
   if (!is_aligned(bias, bias ? bytes_of(bias_dtype) : 1))
     return fail(FLCE_ERR_UNSUPPORTED, "bias must be naturally aligned");
@@ -418,8 +430,7 @@ flce_status_t flce_token_logprobs_backward(const void* logits, int dtype, int64_
   if (M == 0) return ok();
   if ((st = check_matrix("logits", logits, dtype, ldl, V)) != FLCE_OK) return st;
   if ((st = check_matrix("dlogits", dlogits, dtype, ldd, V)) != FLCE_OK) return st;
-  if (logits == dlogits && ldl != ldd)
-    return fail(FLCE_ERR_INVALID_VALUE, "dlogits in the logits' place must have their row stride");
+  if ((st = check_in_place("logits", logits, dtype, ldl, "dlogits", dlogits, dtype, ldd, M)) != FLCE_OK) return st;
   if (!stats) return fail(FLCE_ERR_INVALID_VALUE, "stats is NULL");
   if ((n_tokens && !tokens) || (grad_entropy && !entropy) || (grad_top && n_top && !top_ids))
     return fail(FLCE_ERR_INVALID_VALUE, "NULL pointer among tokens, entropy, top_ids");
