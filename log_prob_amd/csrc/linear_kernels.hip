@@ -865,16 +865,17 @@ hipError_t launch_linear_grad(LinearGradArgs a, hipStream_t s) {
 
 // Whether a call takes the kernels for few rows: by dot products always, on the matrix instruction
 // where they are quicker than the tiles.  A workgroup a compute unit: a round takes 0.65 us and, for
-// each 512 K, 0.45 to 0.7 as more units are busy (0.2 more past 16 rows).  (us, these and tiles: 16 x
-// 4096 x 4096 9.6, 15; 32 x 4096 x 4096 11.6, 15.6; 16 x 11008 x 4096 22, 28; 16 x 1024 x 8192 10.8,
-// 14; 4 x 50257 x 1600 45, 35; 32 x 50257 x 1600 65, 36.)
+// each 512 K, 0.2 to 0.7 as more units are busy (past 16 rows 0.65 to 0.9).  (us, these and tiles: 16 x
+// 4096 x 4096 8.9, 12.1; 32 x 4096 x 4096 12.2, 12.6; 16 x 11008 x 4096 20.7, 32; 16 x 1024 x 8192 8.2,
+// 12.7; 3 x 512 x 8192 7.2, 10.4; and the other way 4 x 50257 x 1600 44, 32; 32 x 50257 x 1600 65, 33;
+// 32 x 2048 x 8192 15.2, 13.4.)
 bool linear_takes_few(int64_t M, int64_t N, int64_t K) {
   if (M <= kLinearDotRows) return true;
   if (M > kLinearFewRows) return false;
   double tiles;
   best_plan(M, N, K, 64, 256, true, &tiles);
   const double groups = double(cdiv(N, 16)), busy = groups < 256 ? groups / 256 : 1;
-  const double stage = 0.45 + 0.25 * busy + (M <= 16 ? 0.0 : 0.2);
+  const double stage = M <= 16 ? 0.2 + 0.5 * busy : 0.65 + 0.25 * busy;
   return double(cdiv(int64_t(groups), 256)) * (0.65 + double(cdiv(K, 512)) * stage) + 2.5 < tiles;
 }
 
