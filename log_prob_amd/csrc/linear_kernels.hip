@@ -31,7 +31,9 @@ namespace {
 
 // Phi(-z) e^(z^2 / 2) for z >= 0, Phi being the normal distribution: a polynomial in 1 / (1 +
 // 0.3 z), fitted to the scaled complementary error function on [0, 15] for the least relative
-// error (6e-8; 4e-7 with fp32 arithmetic).  The library's erff takes twice as long.
+// error (6e-8; 4e-7 with fp32 arithmetic).  The library's erff takes twice as long.  The exponentials
+// beside it and in the logistic function are 2^y of an argument rounded to fp32: far in the tail, where
+// y is -100, they are off by some 1e-5 of values below 1e-30.
 __device__ __forceinline__ float scaled_tail(float z) {
   const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, z, 1.f));
   float p = 0.03842540085315704f;
@@ -146,9 +148,9 @@ __device__ __forceinline__ void store_any(void* p, int dtype, long at, int col, 
   else store8<Bf16, false>(static_cast<uint16_t*>(p) + at, col, cols, v);
 }
 // The same with bf16 past the caches: a tile's results are not read again by its launch, and
-// would push operands out of L2 (4096 x 4096 x 4096 on cold inputs: 120 -> 110 us, gelu 125 ->
-// 115).  fp32 stays in them (120 us against 131): its two stores a thread cover every other 16
-// bytes, and only the cache puts them together.
+// would push operands out of L2 (4096 x 4096 x 4096 with a bias: 107 -> 104.5 us, gelu 115 -> 113.5,
+// with residual and pre too 149 -> 138).  fp32 stays in them (112 us against 134): its two stores a
+// thread cover every other 16 bytes, and only the cache puts them together.
 __device__ __forceinline__ void stream_any(void* p, int dtype, long at, int col, int cols, const float (&v)[8]) {
   if (dtype == kF32 || col + 8 > cols) return store_any(p, dtype, at, col, cols, v);
   const u32x4_a2 u = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
@@ -362,9 +364,9 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearEpilogue e, cons
 // lanes 8 consecutive K each (1 KiB of a row at once), in batches of U loads a row; the next
 // batch is in flight under the work on this one.  X lies in LDS, at most 64 KiB of it at a time,
 // staged under the first batch, and is read from there once for the R rows.  Products of a pair of
-// bf16 go through v_dot2: two multiplications and no unpacking.  1 x 4096 x 4096 8.7 us (3.9 TB/s, of
-// which 2.5 us are the launch's), 1 x 50257 x 1600 26.7 (6.0 TB/s); R of 1 or 4 and U of 1 or 4 are
-// up to 20% slower on one or the other.
+// bf16 go through v_dot2: two multiplications and no unpacking.  1 x 4096 x 4096 8.6 us among other
+// calls (3.9 TB/s; 9.9 alone, of which 2.5 are the launch's), 1 x 50257 x 1600 25.5 (6.3 TB/s); R of 1
+// or 4 and U of 1 or 4 are up to 20% slower on one or the other.
 __device__ __forceinline__ float load1(const void* p, int dtype, long at) {
   return dtype == kF32 ? static_cast<const float*>(p)[at] : Bf16::to_f32(static_cast<const uint16_t*>(p)[at]);
 }
@@ -555,7 +557,7 @@ __global__ __launch_bounds__(256) void linear_stream_kernel(LinearProduct p, Lin
 // ---------------------------------------------------------------------------
 // dpre = dy act'(pre), 8 columns a lane and 512 a workgroup, whose four waves walk the rows of
 // its group; the column sums stay in registers and meet in LDS.
-// Bound by memory (4096 x 4096 bf16 26 us, of 100 MB; 513 x 1000 fp32 7.4, one round of waits).
+// Bound by memory (4096 x 4096 bf16 24.4 us, of 100 MB; 513 x 1000 fp32 7.2, one round of waits).
 constexpr int SLOPE_COLS = 512, SLOPE_ROWS = 4;  // rows a wave has in flight
 
 template <class TY, bool VEC>
@@ -615,11 +617,15 @@ __global__ __launch_bounds__(256) void linear_slope_kernel(LinearSlopeArgs p) {
 // dX of up to 1024 values: dX[m] = sum_n dpre[m, n] W[n], with dpre in fp32.  The rounding to bf16
 // that the matrix instruction asks for adds as much to dX as the store's own, 1.4 times together, on
 // average; the fewer values, the further from that average (1 x 37832 x 104: 2.4 to 2.7e-3 of the
-// norm, this way 1.6e-3).  It costs a few us (dX and dbias in a graph, this way and by tiles: 5 x 3000 x
-// 200 19, 14; 16 x 50257 x 64 33, 27; 128 x 4096 x 8 19, 15).  For more values the tiles are right, and
-// quicker by more (4 x 4096 x 4096 29 us against 43).  A workgroup takes 4 rows, 512 columns and a share of n, 128 of which have their dpre
-// in LDS at a time; a wave's lanes lie along a row of W, several rows at once where K is short.  The
-// lanes' sums meet by exchange, the waves' in LDS, the shares' in the joining kernel, in a fixed order.
+// norm, this way 1.6e-3).  dW, which has as many values as the layer, goes without.
+// A workgroup takes 4 rows, 512 columns and a share of n, 128 of which have their dpre in LDS at a
+// time; a wave's lanes lie along a row of W, several rows at once where K is short.  The lanes' sums
+// meet by exchange, the waves' in LDS, the shares' in the joining kernel, in a fixed order.
+// dX alone (us, this way and by tiles): 5 x 3000 x 200 11.9, 12.9; 16 x 50257 x 64 22.9, 26.5; 128 x
+// 4096 x 8 11.8, 14.4; 1 x 37832 x 104 19.9, 20.5; 1 x 4096 x 1024 14.3, 12.8; 4 x 50257 x 256 40, 26;
+// 1 x 50257 x 1024 66, 29 (20 for W's bytes at the copy rate): latency, at most 96 shares.  With dbias
+// or dW beside it this way adds 4 to 10 us for launches that the tiles share.  For more values the tiles
+// are right, and quicker by more (4 x 4096 x 4096 29 us against 43).
 constexpr int DX_ROWS = 4, DX_STAGE = 128, DX_COLS = 512;
 template <class TY>
 __global__ __launch_bounds__(256) void linear_few_dx_kernel(LinearFewDx p) {
@@ -744,15 +750,21 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //   4096 x 4096 x 4096   256/1 101, 128/1 113, 64/1 146
 // Operands past about 100 MB come from memory in earnest, which slows the small tiles' steps more,
 // as they load more for a product:
-//   257 x 50257 x 1600   128/1 83, 256/1 90, 64/1 92
-//   1024 x 32768 x 2048  256/1 117, 128/1 165, 64/1 197
+//   256 x 50257 x 1600   256/1 59, 128/1 79, 64/1 90
+//   257 x 50257 x 1600   256/1 81, 128/1 81, 64/1 87; with fp32 results 90, 87, 91
+//   1024 x 32768 x 2048  256/1 115, 128/1 165, 64/1 199
 // (Other shapes of tiles: 128 x 128 with 32 K a stage and three workgroups a unit 10 to 30% slower
-// than 128/1 throughout, 128 x 256 with one workgroup 2 to 30%.)
+// than 128/1 throughout, 128 x 256 with one workgroup 2 to 30%.)  The results' bytes are not part of the
+// model: it has 72 and 78 us for 256/1 and 128/1 at 257 rows and takes the former, also where fp32
+// results make it the slower by 4%; and 109 for 4096 x 4096 x 4096, which the whole epilogue (gelu,
+// residual, pre) makes 136 (128/1 150, 64/1 193).
 //
-// `lower`: the last tile row is half as high where that holds it, which a unit takes beside
-// another tile for 0.12 us a step, alone for 0.5 (tiles of 256 0.9).  (us, without it and with:
-// 1025 x 4096 x 4096 55, 46; 2100 x 8192 x 2048 94, 82; 4097 x 4096 x 4096 171, 150;
-// 257 x 50257 x 1600 101, 97.  The gradients' products, several of which share a launch, go without.)
+// `lower`: the last tile row is half as high where that holds it, which the model has a unit take
+// beside another tile for 0.12 us a step, alone for 0.5 (tiles of 256 0.9).  It saves the operand's
+// traffic where the last tiles run beside others (us, full height and half: 257 x 50257 x 1600 fp32 tiles
+// of 128 88, 85, of 256 93, 89; 300 x 50257 x 1600 92, 89 and 95, 89; 320 x 16384 x 4096 65, 64 and 70,
+// 67), and nothing where they run alone, as each step waits for its loads (1025 and 4097 x 4096 x 4096,
+// 2100 x 8192 x 2048).  The gradients' products, several of which share a launch, go without.
 double plan_time(const LinearPlan& p, int64_t M, int64_t N, int64_t K, bool lower) {
   const int64_t columns = cdiv(N, p.tile_n) * p.splits, n = cdiv(M, p.tile_m) * columns;
   const int64_t over = M % p.tile_m;

@@ -20,12 +20,12 @@
 // that of the logits, equal ones by their index; the order in which candidates arrive changes
 // nothing.
 //
-// Measured (us): 4096 x 128256 bf16 without alternatives 202 (5.2 TB/s, the copy rate; the entropy
-// adds 5), with 20 of them 231 to 246; 2048 x 128256 fp32 with 20 214; 257 x 50257 fp32 without
-// 17.5, with 8 26; 4 x 128256 fp32 with 5 12.7, 7.6 of it the pieces and 4 to 5 the joining kernel.
-// What the alternatives cost is a row's fixed part, in which only the next step's loads are in
-// flight: the first threshold, two barriers a step, the last thinning (4096 x 32768 bf16: 74 with
-// 5, 115 with 50).
+// Measured (us, calls among others): 4096 x 128256 bf16 without alternatives 184 (5.7 TB/s; the
+// entropy adds 4), with 20 of them 232 (242 in a trace, where a launch waits for the one before);
+// 2048 x 128256 fp32 with 20 187; 257 x 50257 fp32 without 16, with 8 25; 4 x 128256 fp32 without 6.2,
+// with 5 13, in a trace 8.2 for the pieces and 5.3 for the joining kernel.  What the alternatives cost
+// is a row's fixed part, in which only the next step's loads are in flight: the first threshold, two
+// barriers a step, the last thinning (4096 x 32768 bf16: 49 without, 74 with 5, 123 with 50).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -394,10 +394,18 @@ __device__ __forceinline__ void offer_in_parts(Shared& sh, const typename TX::me
   }
 }
 
-// The next step's loads are in flight under the work on this one.  (Without the entropy a row's
-// steps are short, and registers for five workgroups a unit too few in bf16, which then keeps 10 a
-// thread in memory: 246 us against 239 at 4096 x 128256 with 20 alternatives.  With it five are
-// better: 247 against 252, and 115 against 127 at 4096 x 32768 with 50.)
+// The next step's loads are in flight under the work on this one.  With alternatives in bf16 the
+// registers of five workgroups a unit are too few (10 a thread go to memory without the entropy, 6
+// with it; of four 2 and none), but five overlap more rows' fixed parts: neither is better throughout,
+// long rows with few alternatives want four, short ones with many five.  4096 rows of bf16, us with four
+// and five (six are 10 to 80% slower):
+//            without the entropy           with it
+//   V        k = 5     20        50        5         20        50
+//   128256   208, 235  234, 243  284, 266  212, 229  249, 242  300, 275
+//   32768    74, 76    99, 93    123, 114  76, 75    102, 95   126, 116
+// Four without the entropy and five with it are the better side at 128256 with 20.  Without
+// alternatives both take the same time (182, 188; 49, 51); fp32 at 2048 x 128256 with 20 takes 186, 195
+// and 188, 190.
 template <class TX, bool ENT, bool TOP>
 __global__ __launch_bounds__(T, ENT ? 5 : 4) void token_logprob_kernel(TokenLogprobArgs p) {
   __shared__ Shared sh;
@@ -574,8 +582,8 @@ __global__ __launch_bounds__(T) void token_logprob_join_kernel(TokenLogprobArgs 
 // (from the logits, so dlogits may be the logits' own memory) and written over the rest after a
 // barrier; several entries of one token are added in their order.
 //
-// Bound by memory: 4096 x 32768 bf16 with one token 95 us (5.6 TB/s), 513 x 50257 fp32 with 64 47
-// (4.3 TB/s), 4096 x 50257 fp32 298 (5.5 TB/s).
+// Bound by memory: 4096 x 32768 bf16 with one token 97 us (5.5 TB/s), 513 x 50257 fp32 with 64 48
+// (4.3 TB/s), 4096 x 50257 fp32 297 (5.5 TB/s).
 constexpr int LIST = kMaxTokens + kMaxTop;
 static_assert(LIST % 8 == 0, "groups of 8");
 constexpr int GRAD_NV = 4, GRAD_STEP = GRAD_NV * VEC_STEP;
